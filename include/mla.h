@@ -472,6 +472,32 @@ mla_status mla_kv_append_fp8(const void* c_kv_new, const void* k_r_new, const in
                              void* rows, float* scales, int64_t num_pages, int32_t* dev_err, void* stream);
 
 /*
+ * The quantising append with the RoPE key rotated on the way in, as a decode
+ * step or a chunk over the FP8 cache starts.  For i < n:
+ *   rows[slots[i]] = [codes(c_kv_new[i]) | rope(k_pe_new[i], positions[i])],
+ *   scales[slots[i]] = 2^k,
+ * codes and scales those of mla_kv_append_fp8, the rotation that of
+ * mla_kv_append_rope (table fp32 [max_pos, 32, 2] from mla_rope_table; fp32
+ * fused multiply-adds, one bf16 rounding).  With q_pe (bf16 [n, 128, 64], the
+ * same tokens' queries) the launch also writes
+ *   q_r[i, h, :] = rope(q_pe[i, h, :], positions[i])     (bf16 [n, 128, 64]),
+ * the values of mla_rope_q; NULL q_pe and q_r append only.  c_kv_new bf16
+ * [n, 512], k_pe_new bf16 [n, 64] (unrotated), positions int32 [n], slots
+ * int64 [n]: device.  The slots of one call are distinct (of two tokens with
+ * one slot the row would hold pieces of both).  A slot outside the pool sets
+ * MLA_DEVERR_SLOT_OOB, a position outside [0, max_pos) MLA_DEVERR_POS_OOB;
+ * either way the token's row and scale are left as they were, and its q_r rows
+ * are left as they were when the position is bad.  n == 0 is a no-op.  Host
+ * errors: MLA_ERR_INVALID_ARG (NULL pointers, only one of q_pe and q_r, the
+ * two overlapping, sizes), MLA_ERR_MISALIGNED (slots 8-byte, positions and
+ * dev_err 4-byte, the other pointers 16-byte aligned).
+ */
+mla_status mla_kv_append_rope_fp8(const void* c_kv_new, const void* k_pe_new, const void* q_pe,
+                                  const int32_t* positions, const float* table, int32_t max_pos,
+                                  const int64_t* slots, int32_t n, void* rows, float* scales, int64_t num_pages,
+                                  void* q_r, int32_t* dev_err, void* stream);
+
+/*
  * Dequantising gather: out bf16 [n_tokens, 576] = the first n_tokens cached
  * tokens of sequence b, latent as code * 2^k (exact in bf16), then the RoPE
  * values bit for bit.  Errors as for mla_gather_paged.

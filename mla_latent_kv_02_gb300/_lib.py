@@ -49,6 +49,7 @@ SIGNATURES = {
     "mla_kv_append": (C.c_int, [P, P, P, I32, P, I64, P, P]),
     "mla_gather_paged": (C.c_int, [P, I64, P, I32, I32, I32, P, P, P]),
     "mla_kv_append_fp8": (C.c_int, [P, P, P, I32, P, P, I64, P, P]),
+    "mla_kv_append_rope_fp8": (C.c_int, [P, P, P, P, P, I32, P, I32, P, P, I64, P, P, P]),
     "mla_gather_paged_fp8": (C.c_int, [P, P, I64, P, I32, I32, I32, P, P, P]),
     "mla_kv_append_nvfp4": (C.c_int, [P, P, P, I32, C.c_float, P, I64, P, P]),
     "mla_gather_paged_nvfp4": (C.c_int, [P, C.c_float, I64, P, I32, I32, I32, P, P, P]),

@@ -153,6 +153,30 @@ def mla_kv_append_fp8(c_kv_new, k_r_new, slots, rows, scales, dev_err, stream=No
                                    rows.shape[0], _ptr(dev_err), _stream(stream)))
 
 
+def mla_kv_append_rope_fp8(c_kv_new, k_pe_new, positions, table, slots, rows, scales, dev_err, q_pe=None, q_r=None,
+                           stream=None) -> None:
+    """Append to the FP8 cache with the RoPE key rotated on the way in; with
+    q_pe (bf16 [n, 128, 64], the same tokens' queries) also rotate them into q_r."""
+    n = c_kv_new.shape[0]
+    _need(c_kv_new, "c_kv_new", torch.bfloat16, (n, D_C))
+    _need(k_pe_new, "k_pe_new", torch.bfloat16, (n, D_R))
+    _need(positions, "positions", torch.int32, (n,))
+    _need(table, "table", torch.float32)
+    _need(slots, "slots", torch.int64, (n,))
+    _need(rows, "rows", torch.uint8, (rows.shape[0], PAGE, FP8_ROW_BYTES))
+    _need(scales, "scales", torch.float32, (rows.shape[0], PAGE))
+    _need(dev_err, "dev_err", torch.int32, (1,))
+    if table.dim() != 3 or tuple(table.shape[1:]) != (D_R // 2, 2):
+        raise ValueError(f"table has shape {tuple(table.shape)}, expected (max_pos, {D_R // 2}, 2)")
+    if q_pe is not None:
+        _need(q_pe, "q_pe", torch.bfloat16, (n, H, D_R))
+    if q_r is not None:
+        _need(q_r, "q_r", torch.bfloat16, (n, H, D_R))
+    _check(lib().mla_kv_append_rope_fp8(_ptr(c_kv_new), _ptr(k_pe_new), _ptr(q_pe), _ptr(positions), _ptr(table),
+                                        table.shape[0], _ptr(slots), int(n), _ptr(rows), _ptr(scales), rows.shape[0],
+                                        _ptr(q_r), _ptr(dev_err), _stream(stream)))
+
+
 def mla_gather_paged_fp8(rows, scales, block_table, b: int, n_tokens: int, out, dev_err, stream=None) -> None:
     _need(rows, "rows", torch.uint8, (rows.shape[0], PAGE, FP8_ROW_BYTES))
     _need(scales, "scales", torch.float32, (rows.shape[0], PAGE))

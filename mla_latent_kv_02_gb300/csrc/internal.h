@@ -135,6 +135,10 @@ cudaError_t launch_rope_q(const uint16_t* q_pe, const int32_t* positions, const 
 cudaError_t launch_kv_append_fp8(const uint16_t* c_kv_new, const uint16_t* k_r_new, const int64_t* slots, int32_t n,
                                  uint8_t* rows, float* scales, int64_t num_slots, int32_t* dev_err,
                                  cudaStream_t stream);
+cudaError_t launch_kv_append_rope_fp8(const uint16_t* c_kv_new, const uint16_t* k_pe_new, const uint16_t* q_pe,
+                                      const int32_t* positions, const float* table, int32_t max_pos,
+                                      const int64_t* slots, int32_t n, uint8_t* rows, float* scales, uint16_t* q_r,
+                                      int64_t num_slots, int32_t* dev_err, cudaStream_t stream);
 cudaError_t launch_gather_fp8(const uint8_t* rows, const float* scales, int64_t num_pages,
                               const int32_t* block_table, int32_t max_pages, int32_t b, int32_t n_tokens,
                               uint16_t* out, int32_t* dev_err, cudaStream_t stream);

@@ -528,6 +528,46 @@ mla_status mla_kv_append_fp8(const void* c_kv_new, const void* k_r_new, const in
   return MLA_OK;
 }
 
+mla_status mla_kv_append_rope_fp8(const void* c_kv_new, const void* k_pe_new, const void* q_pe,
+                                  const int32_t* positions, const float* table, int32_t max_pos,
+                                  const int64_t* slots, int32_t n, void* rows, float* scales, int64_t num_pages,
+                                  void* q_r, int32_t* dev_err, void* stream) {
+  if (n < 0) return fail(MLA_ERR_INVALID_ARG, "n = %d < 0", n);
+  if (n == 0) return MLA_OK;
+  CHECK_PTR(c_kv_new);
+  CHECK_PTR(k_pe_new);
+  CHECK_PTR(positions);
+  CHECK_PTR(table);
+  CHECK_PTR(slots);
+  CHECK_PTR(rows);
+  CHECK_PTR(scales);
+  CHECK_PTR(dev_err);
+  if ((q_pe == nullptr) != (q_r == nullptr))
+    return fail(MLA_ERR_INVALID_ARG, "q_pe and q_r must be given together");
+  CHECK_ALIGN16(c_kv_new);
+  CHECK_ALIGN16(k_pe_new);
+  CHECK_ALIGN16(q_pe);
+  CHECK_ALIGN16(q_r);
+  CHECK_ALIGN16(table);
+  CHECK_ALIGN16(rows);
+  CHECK_ALIGN16(scales);
+  if (!aligned(slots, 8)) return fail(MLA_ERR_MISALIGNED, "slots is not 8-byte aligned");
+  if (!aligned(positions, 4) || !aligned(dev_err, 4))
+    return fail(MLA_ERR_MISALIGNED, "positions and dev_err must be 4-byte aligned");
+  if (max_pos < 1) return fail(MLA_ERR_INVALID_ARG, "max_pos = %d < 1", max_pos);
+  if (num_pages < 1) return fail(MLA_ERR_INVALID_ARG, "num_pages = %lld < 1", (long long)num_pages);
+  if (q_pe) {
+    const uintptr_t a0 = (uintptr_t)q_pe, b0 = (uintptr_t)q_r, len = (uintptr_t)n * MLA_NUM_HEADS * MLA_ROPE_DIM * 2;
+    if (a0 < b0 + len && b0 < a0 + len) return fail(MLA_ERR_INVALID_ARG, "q_pe and q_r overlap");
+  }
+  cudaError_t e = mla::launch_kv_append_rope_fp8((const uint16_t*)c_kv_new, (const uint16_t*)k_pe_new,
+                                                 (const uint16_t*)q_pe, positions, table, max_pos, slots, n,
+                                                 (uint8_t*)rows, scales, (uint16_t*)q_r, num_pages * MLA_PAGE_SIZE,
+                                                 dev_err, (cudaStream_t)stream);
+  if (e != cudaSuccess) return cuda_fail(e, "kv_append_rope_fp8 launch");
+  return MLA_OK;
+}
+
 mla_status mla_gather_paged_fp8(const void* rows, const float* scales, int64_t num_pages,
                                 const int32_t* block_table, int32_t max_pages, int32_t b, int32_t n_tokens,
                                 void* out, int32_t* dev_err, void* stream) {

@@ -19,10 +19,12 @@
 #include <cstdint>
 
 #include "internal.h"
-#include "ptx.cuh"
+#include "rope.cuh"
 
 namespace mla {
 namespace rope {
+
+using namespace mla::dev;
 
 constexpr int kPairs = 32;   // 64 RoPE dims
 constexpr int kLatVec = 64;  // 512 bf16 = 64 x 16 B
@@ -36,17 +38,6 @@ __global__ void __launch_bounds__(256) rope_table_kernel(float2* __restrict__ ta
     const double a = (double)p * pow(base, -2.0 * (double)i / 64.0);
     table[k] = make_float2((float)cos(a), (float)sin(a));
   }
-}
-
-__device__ __forceinline__ float bf16_lo(uint32_t v) { return __uint_as_float(v << 16); }
-__device__ __forceinline__ float bf16_hi(uint32_t v) { return __uint_as_float(v & 0xFFFF0000u); }
-
-// Pair (x0, x1) turned by (c, s) in fp32, rounded to a bf16 pair.
-__device__ __forceinline__ uint32_t rotate_pair(uint32_t x, float2 cs) {
-  const float x0 = bf16_lo(x), x1 = bf16_hi(x);
-  const float y0 = fmaf(x0, cs.x, -x1 * cs.y);
-  const float y1 = fmaf(x0, cs.y, x1 * cs.x);
-  return dev::pack_bf16x2(y0, y1);
 }
 
 __global__ void __launch_bounds__(kWarps * 32)
@@ -88,12 +79,7 @@ __global__ void __launch_bounds__(256)
     const uint4 x = __ldg(q_pe + k);
     const float4 t0 = __ldg(table + (int64_t)p * (kPairs / 2) + 2 * c);
     const float4 t1 = __ldg(table + (int64_t)p * (kPairs / 2) + 2 * c + 1);
-    uint4 y;
-    y.x = rotate_pair(x.x, make_float2(t0.x, t0.y));
-    y.y = rotate_pair(x.y, make_float2(t0.z, t0.w));
-    y.z = rotate_pair(x.z, make_float2(t1.x, t1.y));
-    y.w = rotate_pair(x.w, make_float2(t1.z, t1.w));
-    q_r[k] = y;
+    q_r[k] = rotate_pairs4(x, t0, t1);
   }
 }
 
