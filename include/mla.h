@@ -523,6 +523,89 @@ mla_status mla_decode_paged_fp8(const void* q_abs, const void* q_r, const void* 
                                 size_t ws_bytes, void* o_lat, float* lse, int32_t* dev_err, void* stream);
 
 /* ---------------------------------------------------------------------------
+ * Attention with a sliding window and sinks over the paged latent cache: a
+ * sequence of any length at a bounded cost.  A row at position p sees the
+ * tokens j <= p with
+ *   j < sinks  (the first tokens, which stay visible)  or  j > p - window.
+ * Everything else is as for mla_decode_paged: the rows of a batch, several
+ * query tokens to a sequence, split rows and the combine, o_lat and lse.
+ * window >= 1 (a row always sees itself), sinks >= 0; either may exceed the
+ * sequence.  Positions are absolute: cached RoPE keys stay as they were
+ * appended.
+ *
+ * Pages that hold neither a sink nor a token of any row's window are not read:
+ * their block-table entries may be -1 and the pages may belong to others.  Of
+ * a page that is read, every slot up to the row's own position must hold
+ * finite values, and so must the rest of the last page (as for
+ * mla_decode_paged).
+ * ------------------------------------------------------------------------- */
+
+/* Summary of a window plan, filled by the planner and passed back to the decode. */
+typedef struct mla_window_info {
+  mla_plan_info plan; /* plan.magic == MLA_WINDOW_PLAN_MAGIC; total_tiles counts the tiles read */
+  int32_t window;
+  int32_t sinks;
+} mla_window_info;
+
+#define MLA_WINDOW_PLAN_MAGIC 0x574C4D41u /* "AMLW" */
+
+/*
+ * The split schedule of mla_decode_plan_host for windowed rows: the same
+ * arguments, buffers (mla_decode_plan_bytes, mla_decode_workspace_size) and
+ * errors, and window < 1 or sinks < 0 is MLA_ERR_INVALID_ARG.  A plan of one
+ * kind passed to the other kind's decode is MLA_ERR_INVALID_ARG.
+ */
+mla_status mla_window_plan_host(const int32_t* seq_lens, const int32_t* q_lens, int32_t B, int32_t window,
+                                int32_t sinks, int32_t num_clusters, void* plan_host, size_t plan_bytes,
+                                mla_window_info* info);
+
+/* As mla_window_plan_host, then copies the plan to plan_dev on `stream`. */
+mla_status mla_window_plan(const int32_t* seq_lens_host, const int32_t* q_lens_host, int32_t B, int32_t window,
+                           int32_t sinks, int32_t num_clusters, void* plan_dev, size_t plan_bytes,
+                           mla_window_info* info, void* stream);
+
+/* mla_decode_paged and mla_decode_paged_fp8 with the plan's window and sinks. */
+mla_status mla_decode_window(const void* q_abs, const void* q_r, const void* kv_cache, int64_t num_pages,
+                             const int32_t* block_table, int32_t max_pages, const void* plan_dev,
+                             const mla_window_info* info, float scale, void* workspace, size_t ws_bytes, void* o_lat,
+                             float* lse, int32_t* dev_err, void* stream);
+mla_status mla_decode_window_fp8(const void* q_abs, const void* q_r, const void* rows, const float* scales,
+                                 int64_t num_pages, const int32_t* block_table, int32_t max_pages,
+                                 const void* plan_dev, const mla_window_info* info, float scale, void* workspace,
+                                 size_t ws_bytes, void* o_lat, float* lse, int32_t* dev_err, void* stream);
+
+/* Workspace bytes mla_prefill_window_batch needs: the kept tokens' packed
+ * rows, K_c and V_c (as mla_prefill_batch_workspace_size over the kept
+ * tokens).  A sequence keeps all n_tokens[i] tokens when no token lies
+ * between the sinks and its first row's window, else sinks + window +
+ * q_lens[i] - 1.  Host int32 [nb], nb <= 64, 1 <= q_lens[i] <= n_tokens[i]. */
+mla_status mla_prefill_window_workspace_size(const int32_t* q_lens, const int32_t* n_tokens, int32_t nb,
+                                             int32_t window, int32_t sinks, size_t* bytes);
+
+/*
+ * mla_prefill_decompress_batch with a sliding window and sinks: the same
+ * arguments, buffers and errors, window >= 1 and sinks >= 0.  Only the kept
+ * tokens (above) are gathered and expanded; pages that hold none of them may
+ * be -1 in the block table.  Every slot of a kept token must hold finite
+ * values.  K_c and V_c are held in bf16 (one rounding), as in the branch
+ * without a window.
+ */
+mla_status mla_prefill_window_batch(const void* q_c, const void* q_r, const int32_t* seq_ids, const int32_t* q_starts,
+                                    const int32_t* q_lens, const int32_t* n_tokens, int32_t nb, int32_t window,
+                                    int32_t sinks, const void* kv_cache, int64_t num_pages, const int32_t* block_table,
+                                    int32_t batch, int32_t max_pages, const void* w_uk, const void* w_uv, float scale,
+                                    void* workspace, size_t ws_bytes, void* out, int32_t* dev_err, void* stream);
+
+/* The same over the FP8 cache (rows and scales 16-byte aligned). */
+mla_status mla_prefill_window_batch_fp8(const void* q_c, const void* q_r, const int32_t* seq_ids,
+                                        const int32_t* q_starts, const int32_t* q_lens, const int32_t* n_tokens,
+                                        int32_t nb, int32_t window, int32_t sinks, const void* rows,
+                                        const float* scales, int64_t num_pages, const int32_t* block_table,
+                                        int32_t batch, int32_t max_pages, const void* w_uk, const void* w_uv,
+                                        float scale, void* workspace, size_t ws_bytes, void* out, int32_t* dev_err,
+                                        void* stream);
+
+/* ---------------------------------------------------------------------------
  * NVFP4 latent cache ([P1] opening section and §5: the latent is gathered in
  * NVFP4 with 16-byte vector loads, which fault on a base that is not 16-byte
  * aligned; here the host rejects such bases with MLA_ERR_MISALIGNED before

@@ -25,6 +25,10 @@ class mla_plan_info(C.Structure):
                 ("max_pages_needed", C.c_int32), ("total_tiles", C.c_int64), ("plan_bytes", C.c_size_t)]
 
 
+class mla_window_info(C.Structure):
+    _fields_ = [("plan", mla_plan_info), ("window", C.c_int32), ("sinks", C.c_int32)]
+
+
 P = C.c_void_p
 I32 = C.c_int32
 I64 = C.c_int64
@@ -76,6 +80,16 @@ SIGNATURES = {
     "mla_decode_paged": (C.c_int, [P, P, P, I64, P, I32, P, C.POINTER(mla_plan_info), C.c_float, P, SZ, P, P, P, P]),
     "mla_decode_paged_fp8": (C.c_int, [P, P, P, P, I64, P, I32, P, C.POINTER(mla_plan_info), C.c_float, P, SZ, P, P,
                                        P, P]),
+    "mla_window_plan_host": (C.c_int, [PI32, PI32, I32, I32, I32, I32, P, SZ, C.POINTER(mla_window_info)]),
+    "mla_window_plan": (C.c_int, [PI32, PI32, I32, I32, I32, I32, P, SZ, C.POINTER(mla_window_info), P]),
+    "mla_decode_window": (C.c_int, [P, P, P, I64, P, I32, P, C.POINTER(mla_window_info), C.c_float, P, SZ, P, P, P, P]),
+    "mla_decode_window_fp8": (C.c_int, [P, P, P, P, I64, P, I32, P, C.POINTER(mla_window_info), C.c_float, P, SZ, P,
+                                        P, P, P]),
+    "mla_prefill_window_workspace_size": (C.c_int, [PI32, PI32, I32, I32, I32, C.POINTER(SZ)]),
+    "mla_prefill_window_batch": (C.c_int, [P, P, PI32, PI32, PI32, PI32, I32, I32, I32, P, I64, P, I32, I32, P, P,
+                                           C.c_float, P, SZ, P, P, P]),
+    "mla_prefill_window_batch_fp8": (C.c_int, [P, P, PI32, PI32, PI32, PI32, I32, I32, I32, P, P, I64, P, I32, I32, P,
+                                               P, C.c_float, P, SZ, P, P, P]),
     "mla_check": (C.c_int, [P, P, PI32]),
     "mla_debug_set_decode_wait_limit": (C.c_int, [C.c_uint64]),
     "mla_decode_paged_noalloc": (C.c_int, [P, P, P, I64, P, I32, PI32, PI32, I32, C.c_float, P, P, P, P]),

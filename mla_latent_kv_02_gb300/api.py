@@ -14,7 +14,7 @@ from typing import Optional, Sequence
 import numpy as np
 import torch
 
-from ._lib import lib, mla_plan_info
+from ._lib import lib, mla_plan_info, mla_window_info
 
 H, D_HC, D_C, D_R, PAGE = 128, 128, 512, 64, 64
 D_QK = D_C + D_R
@@ -537,6 +537,165 @@ def mla_decode_paged_fp8(q_abs, q_r, rows, scales, block_table, plan: DecodePlan
                                       _ptr(block_table), block_table.shape[1], _ptr(plan.plan), C.byref(plan.info),
                                       float(scale), _ptr(plan.workspace), plan.workspace.numel(), _ptr(o_lat),
                                       _ptr(lse), _ptr(dev_err), _stream(stream)))
+
+
+# ------------------------------------------------------------------ sliding window with sinks
+def mla_window_plan_host(seq_lens: Sequence[int], q_lens: Sequence[int], window: int, sinks: int, num_clusters: int):
+    """Host planner of the windowed decode only (no GPU): returns (plan int32 array, info)."""
+    sl = np.ascontiguousarray(seq_lens, dtype=np.int32)
+    ql = np.ascontiguousarray(q_lens, dtype=np.int32)
+    if sl.shape != ql.shape or sl.ndim != 1:
+        raise ValueError("seq_lens and q_lens must be lists of the same length")
+    nbytes = mla_decode_plan_bytes(int(ql.sum()) if ql.size else 0, num_clusters)
+    buf = np.zeros(nbytes // 4, dtype=np.int32)
+    info = mla_window_info()
+    P32 = C.POINTER(C.c_int32)
+    _check(lib().mla_window_plan_host(sl.ctypes.data_as(P32), ql.ctypes.data_as(P32), int(sl.size), int(window),
+                                      int(sinks), int(num_clusters), buf.ctypes.data_as(C.c_void_p), nbytes,
+                                      C.byref(info)))
+    return buf, info
+
+
+@dataclass
+class WindowPlan:
+    """A window plan on the device plus its host summary (mla_window_plan)."""
+    plan: torch.Tensor          # int32 device buffer
+    info: mla_window_info
+    workspace: torch.Tensor     # uint8 device buffer
+    host: torch.Tensor          # pinned int32 staging of the plan (reused by `into=`)
+
+    @property
+    def num_clusters(self) -> int:
+        return int(self.info.plan.num_clusters)
+
+
+def mla_window_plan(seq_lens: Sequence[int], q_lens: Sequence[int], window: int, sinks: int, device=None,
+                    num_clusters: Optional[int] = None, stream=None, into: Optional[WindowPlan] = None) -> WindowPlan:
+    """mla_decode_plan for a sliding window with sinks: one plan serves every
+    layer of a step.  A plan holds one workspace, so decodes that share it must
+    not overlap on the GPU; `into` reuses a previous plan's buffers when they
+    are large enough and nothing that reads them may still be running."""
+    if num_clusters is None:
+        num_clusters = mla_decode_max_clusters()
+    buf, info = mla_window_plan_host(seq_lens, q_lens, window, sinks, num_clusters)
+    words = (buf.size + 3) // 4 * 4
+    device = torch.device(device) if device is not None else torch.device("cuda", torch.cuda.current_device())
+    ws_bytes = max(mla_decode_workspace_size(num_clusters), 16)
+    if (into is not None and into.plan.numel() >= words and into.workspace.numel() >= ws_bytes
+            and into.plan.device == device):
+        plan, ws, host = into.plan, into.workspace, into.host
+    else:
+        plan = torch.empty(words, dtype=torch.int32, device=device)
+        ws = torch.empty(ws_bytes, dtype=torch.uint8, device=device)
+        host = torch.zeros(words, dtype=torch.int32).pin_memory()
+    host[:buf.size] = torch.from_numpy(buf)
+    with torch.cuda.stream(stream):
+        plan[:words].copy_(host[:words], non_blocking=True)
+    return WindowPlan(plan=plan, info=info, workspace=ws, host=host)
+
+
+def mla_decode_window(q_abs, q_r, kv_cache, block_table, plan: WindowPlan, o_lat, dev_err, lse=None,
+                      scale: float = 1.0 / (192 ** 0.5), stream=None) -> None:
+    """mla_decode_paged with the plan's sliding window and sinks."""
+    T = q_abs.shape[0]
+    _need(q_abs, "q_abs", torch.bfloat16, (T, H, D_C))
+    _need(q_r, "q_r", torch.bfloat16, (T, H, D_R))
+    _need(kv_cache, "kv_cache", torch.bfloat16, (kv_cache.shape[0], PAGE, D_QK))
+    _need_window(plan, T, block_table, o_lat, lse, dev_err)
+    _check(lib().mla_decode_window(_ptr(q_abs), _ptr(q_r), _ptr(kv_cache), kv_cache.shape[0], _ptr(block_table),
+                                   block_table.shape[1], _ptr(plan.plan), C.byref(plan.info), float(scale),
+                                   _ptr(plan.workspace), plan.workspace.numel(), _ptr(o_lat), _ptr(lse),
+                                   _ptr(dev_err), _stream(stream)))
+
+
+def mla_decode_window_fp8(q_abs, q_r, rows, scales, block_table, plan: WindowPlan, o_lat, dev_err, lse=None,
+                          scale: float = 1.0 / (192 ** 0.5), stream=None) -> None:
+    """mla_decode_paged_fp8 with the plan's sliding window and sinks."""
+    T = q_abs.shape[0]
+    _need(q_abs, "q_abs", torch.bfloat16, (T, H, D_C))
+    _need(q_r, "q_r", torch.bfloat16, (T, H, D_R))
+    _need(rows, "rows", torch.uint8, (rows.shape[0], PAGE, FP8_ROW_BYTES))
+    _need(scales, "scales", torch.float32, (rows.shape[0], PAGE))
+    _need_window(plan, T, block_table, o_lat, lse, dev_err)
+    _check(lib().mla_decode_window_fp8(_ptr(q_abs), _ptr(q_r), _ptr(rows), _ptr(scales), rows.shape[0],
+                                       _ptr(block_table), block_table.shape[1], _ptr(plan.plan), C.byref(plan.info),
+                                       float(scale), _ptr(plan.workspace), plan.workspace.numel(), _ptr(o_lat),
+                                       _ptr(lse), _ptr(dev_err), _stream(stream)))
+
+
+def _need_window(plan, T, block_table, o_lat, lse, dev_err) -> None:
+    if not isinstance(plan, WindowPlan):
+        raise TypeError("plan must come from mla_window_plan")
+    info = plan.info.plan
+    if info.T != T:
+        raise ValueError(f"plan has {info.T} rows, q_abs has {T}")
+    _need(block_table, "block_table", torch.int32)
+    if block_table.dim() != 2 or block_table.shape[0] < info.B:
+        raise ValueError(f"block_table has shape {tuple(block_table.shape)}, the plan has {info.B} sequences")
+    _need(o_lat, "o_lat", torch.bfloat16, (T, H, D_C))
+    _need(dev_err, "dev_err", torch.int32, (1,))
+    if lse is not None:
+        _need(lse, "lse", torch.float32, (T, H))
+
+
+def _host_i32(*lists):
+    """The host lists as int32 arrays of one length."""
+    arrs = [np.ascontiguousarray(x, dtype=np.int32) for x in lists]
+    if any(a.ndim != 1 or a.size != arrs[0].size for a in arrs):
+        raise ValueError("the sequences' lists must have the same length")
+    return arrs
+
+
+def mla_prefill_window_workspace_size(q_lens: Sequence[int], n_tokens: Sequence[int], window: int, sinks: int) -> int:
+    q, n = _host_i32(q_lens, n_tokens)
+    out = C.c_size_t()
+    P32 = C.POINTER(C.c_int32)
+    _check(lib().mla_prefill_window_workspace_size(q.ctypes.data_as(P32), n.ctypes.data_as(P32), int(n.size),
+                                                   int(window), int(sinks), C.byref(out)))
+    return int(out.value)
+
+
+def _prefill_window(call, cache, q_c, q_r, block_table, seq_ids, q_starts, q_lens, n_tokens, window, sinks, w_uk, w_uv,
+                    workspace, out, dev_err, scale, stream) -> None:
+    rows = q_c.shape[0]
+    _need(q_c, "q_c", torch.bfloat16, (rows, H, D_HC))
+    _need(q_r, "q_r", torch.bfloat16, (rows, H, D_R))
+    _need(block_table, "block_table", torch.int32)
+    if block_table.dim() != 2:
+        raise ValueError("block_table must be [sequences, pages]")
+    _need(w_uk, "w_uk", torch.bfloat16, (H, D_HC, D_C))
+    _need(w_uv, "w_uv", torch.bfloat16, (H, D_C, D_HC))
+    _need(workspace, "workspace", torch.uint8)
+    _need(out, "out", torch.bfloat16, (rows, H, D_HC))
+    _need(dev_err, "dev_err", torch.int32, (1,))
+    arrs = _host_i32(seq_ids, q_starts, q_lens, n_tokens)
+    if any(int(s0) + int(m) > rows for s0, m in zip(arrs[1], arrs[2])):
+        raise ValueError("a chunk's rows run past q_c")
+    P32 = C.POINTER(C.c_int32)
+    _check(call(_ptr(q_c), _ptr(q_r), *[a.ctypes.data_as(P32) for a in arrs], int(arrs[0].size), int(window),
+                int(sinks), *[_ptr(t) for t in cache], cache[0].shape[0], _ptr(block_table), block_table.shape[0],
+                block_table.shape[1], _ptr(w_uk), _ptr(w_uv), float(scale), _ptr(workspace), workspace.numel(),
+                _ptr(out), _ptr(dev_err), _stream(stream)))
+
+
+def mla_prefill_window_batch(q_c, q_r, kv_cache, block_table, seq_ids, q_starts, q_lens, n_tokens, window: int,
+                             sinks: int, w_uk, w_uv, workspace, out, dev_err, scale: float = 1.0 / (192 ** 0.5),
+                             stream=None) -> None:
+    """mla_prefill_decompress_batch with a sliding window and sinks: only the
+    tokens that a chunk's rows see are gathered and expanded."""
+    _need(kv_cache, "kv_cache", torch.bfloat16, (kv_cache.shape[0], PAGE, D_QK))
+    _prefill_window(lib().mla_prefill_window_batch, (kv_cache,), q_c, q_r, block_table, seq_ids, q_starts, q_lens,
+                    n_tokens, window, sinks, w_uk, w_uv, workspace, out, dev_err, scale, stream)
+
+
+def mla_prefill_window_batch_fp8(q_c, q_r, rows, scales, block_table, seq_ids, q_starts, q_lens, n_tokens, window: int,
+                                 sinks: int, w_uk, w_uv, workspace, out, dev_err, scale: float = 1.0 / (192 ** 0.5),
+                                 stream=None) -> None:
+    """mla_prefill_window_batch over the FP8 cache."""
+    _need(rows, "rows", torch.uint8, (rows.shape[0], PAGE, FP8_ROW_BYTES))
+    _need(scales, "scales", torch.float32, (rows.shape[0], PAGE))
+    _prefill_window(lib().mla_prefill_window_batch_fp8, (rows, scales), q_c, q_r, block_table, seq_ids, q_starts,
+                    q_lens, n_tokens, window, sinks, w_uk, w_uv, workspace, out, dev_err, scale, stream)
 
 
 def mla_check(dev_err, stream=None) -> int:

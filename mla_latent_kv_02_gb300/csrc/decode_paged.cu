@@ -182,13 +182,17 @@ struct Idesc {
 
 // Walks the 64-token tiles of a cluster's segments in order; a segment's
 // fields are read from the plan once, when the cursor enters it.
+template <bool kWin>
 struct TileCursor {
   const int32_t* segs;
   int s, s_end, pg, pb, pe, row, vis, slot;
-  __device__ __forceinline__ void init(const int32_t* sg, int sb, int se) {
+  int sinks, wlo;  // windowed: the segment's window starts at wlo
+  WindowTiles w;
+  __device__ __forceinline__ void init(const int32_t* sg, int sb, int se, int sinks_ = 0) {
     segs = sg;
     s = sb;
     s_end = se;
+    sinks = sinks_;
     if (s < s_end) load();
   }
   __device__ __forceinline__ void load() {
@@ -201,6 +205,27 @@ struct TileCursor {
     vis = hi.x;
     slot = hi.y;
     pg = pb;
+    if (kWin) {
+      wlo = hi.z;
+      w = window_tiles(wlo, sinks);
+    }
+  }
+  // Windowed: which of the current tile's 64 tokens the row sees, a bit each.
+  // [0, a) are sinks, [b, c) lie in the window.
+  __device__ __forceinline__ uint64_t visible() const {
+    int a, b = 0, c = 0;
+    if (pg < w.sink_tiles) {
+      a = sinks - pg * kPage;
+    } else {
+      const int p0 = (pg + w.skip) * kPage;
+      a = pg == w.sink_tiles ? w.head : 0;
+      b = wlo - p0;
+      c = vis - p0;
+    }
+    return bits_below(a) | (bits_below(c) & ~bits_below(b));
+  }
+  static __device__ __forceinline__ uint64_t bits_below(int n) {
+    return n <= 0 ? 0ull : n >= 64 ? ~0ull : (1ull << n) - 1ull;
   }
   __device__ __forceinline__ bool valid() const { return s < s_end; }
   __device__ __forceinline__ bool first() const { return pg == pb; }
@@ -219,10 +244,15 @@ __device__ __forceinline__ uint32_t as_u32(__half2 h) { return *reinterpret_cast
 // kv_map / rope_map: bf16 cache — latent chunks (3D, 128-byte swizzle) and
 // RoPE halves; FP8 cache — code rows (uint8, 256-byte boxes, no swizzle) and
 // RoPE halves of the 640-byte rows.
-template <bool kF8>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<kF8>::kThreads, 1)
-    decode_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constant__ CUtensorMap rope_map,
-                  const DecodeArgs a) {
+// kWin: a sliding window with sinks.  A row's tiles are its sink pages and its
+// window pages only; pages in between are never read.  When the last sinks
+// fill no whole page they ride in the dead space before the window's first
+// token where there is room (a merged tile, loaded as two boxes), so a window
+// of W tokens costs about W / 64 + 1 tiles.  The row's visibility in a tile is
+// a 64-bit mask, all ones inside the window.
+template <bool kF8, bool kWin>
+__device__ __forceinline__ void decode_body(const CUtensorMap& kv_map, const CUtensorMap& rope_map,
+                                            const DecodeArgs& a, const WindowArgs* win) {
   using L = Layout<kF8>;
   constexpr int kStages = L::kStages, kStageBytes = L::kStageBytes, kThreads = L::kThreads;
   constexpr int kPvWarp = L::kPvWarp, kSoftWarp0 = L::kSoftWarp0, kConvWarp0 = L::kConvWarp0;
@@ -296,6 +326,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<kF8>::kThreads, 
       const int32_t row = sg[0], b = sg[1], pb = sg[2], pe = sg[3], vis = sg[4], slot = sg[5];
       good = row >= 0 && row < a.T && b >= 0 && b < a.B && pb >= 0 && pe > pb && pe <= a.max_pages && vis >= 1 &&
              (int64_t)(pe - 1) * kPage < (int64_t)vis && slot >= -1 && slot < a.num_partials;
+      if (kWin && good) {
+        const int32_t lo = sg[6];
+        const WindowTiles w = window_tiles(lo, win->sinks);
+        const int64_t last = pe - 1 + (int64_t)(pe > w.sink_tiles ? w.skip : 0);
+        good = lo >= 0 && (lo == 0 || (lo > win->sinks && lo < vis)) && last < a.max_pages &&
+               last * kPage < (int64_t)vis;
+      }
     }
     if (!good) {
       atomicOr(err, (int32_t)MLA_DEVERR_PLAN);
@@ -342,9 +379,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<kF8>::kThreads, 
         const int32_t* sg = a.segs + 8 * s;
         const int b = sg[1], pb = sg[2], pe = sg[3];
         const int32_t* bt = a.block_table + (int64_t)b * a.max_pages;
+        WindowTiles wt = {0, 0, 0, 0};
+        if (kWin) wt = window_tiles(sg[6], win->sinks);
         for (int pg = pb; pg < pe; ++pg) {
           const uint32_t st = g % kStages, use = g / kStages;
-          int32_t pid = __ldg(bt + pg);  // in flight while the stage drains
+          int32_t pid = __ldg(bt + (kWin && pg >= wt.sink_tiles ? pg + wt.skip : pg));  // in flight while the stage drains
+          const bool merged = kWin && wt.merged && pg == wt.sink_tiles;
+          int32_t spid = merged ? __ldg(bt + win->sinks / kPage) : 0;  // the sinks' page
           if (pg == pe - 1 && s + 1 < s_end) {
             // The next segment's query row is read right after this segment's
             // last QK^T: warm L2 with it (each CTA one half of q_abs[row],
@@ -363,7 +404,35 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<kF8>::kThreads, 
             pid = 0;
           }
           const uint32_t dst = base + kOffKV + st * kStageBytes;
-          if constexpr (kF8) {
+          if (merged) {
+            // tokens [0, split) of the sinks' page and [split, 64) of the
+            // window's first page, at their places in the tile; split is a
+            // multiple of eight, so every box starts on a swizzle atom
+            if (spid < 0 || (int64_t)spid >= a.num_pages) {
+              atomicOr(err, (int32_t)MLA_DEVERR_PAGE_OOB);
+              spid = 0;
+            }
+            const int n0 = win->split, y0 = spid * kPage, y1 = pid * kPage + n0;
+            if constexpr (kF8) {
+              const uint32_t bar = BAR(B_F8_FULL + st);
+              mbar_arrive_expect_tx(bar, (uint32_t)kF8Payload);
+              tma_load_2d(dst, &win->kv_head, (int)(256 * rank), y0, bar);
+              tma_load_2d(dst + n0 * 256, &win->kv_tail, (int)(256 * rank), y1, bar);
+              tma_load_2d(dst + kF8RopeOff, &win->rope_head, 256 + (int)rank * kRopeHalf, y0, bar);
+              tma_load_2d(dst + kF8RopeOff + n0 * 64, &win->rope_tail, 256 + (int)rank * kRopeHalf, y1, bar);
+              bulk_load_g2s(dst + kF8ScaleOff, a.kv_scales + (size_t)y0, n0 * 4, bar);
+              bulk_load_g2s(dst + kF8ScaleOff + n0 * 4, a.kv_scales + (size_t)y1, (kPage - n0) * 4, bar);
+            } else {
+              const uint32_t bar = BAR(B_KV_FULL + st);
+              mbar_arrive_expect_tx(bar, (uint32_t)kStageBytes);
+              for (int c = 0; c < 4; ++c) {
+                tma_load_3d(dst + c * kChunkBytes, &win->kv_head, 0, y0, (int)(4 * rank) + c, bar);
+                tma_load_3d(dst + c * kChunkBytes + n0 * 128, &win->kv_tail, 0, y1, (int)(4 * rank) + c, bar);
+              }
+              tma_load_2d(dst + 4 * kChunkBytes, &win->rope_head, kDC + (int)rank * kRopeHalf, y0, bar);
+              tma_load_2d(dst + 4 * kChunkBytes + n0 * 64, &win->rope_tail, kDC + (int)rank * kRopeHalf, y1, bar);
+            }
+          } else if constexpr (kF8) {
             // this CTA's 256 codes of each of the page's 64 rows, its RoPE
             // half, and the page's 64 token scales
             mbar_arrive_expect_tx(BAR(B_F8_FULL + st), (uint32_t)kF8Payload);
@@ -393,7 +462,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<kF8>::kThreads, 
     // QK^T issue (the tensor pipe throttles it) never delays P·V, nor the
     // other way round; the two streams share only the tensor pipe.
     if (lane == 0) {
-      TileCursor cq;
+      TileCursor<false> cq;
       cq.init(a.segs, s_begin, s_end);
       // Stage-0 descriptors: latent chunks (K-major) and the RoPE half,
       // advanced by adding the byte offset >> 4 to the start-address field
@@ -437,7 +506,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<kF8>::kThreads, 
   auto role_pv = [&]() {
     // ---------------------------------------------------------------- P·V issue
     if (lane == 0) {
-      TileCursor cp;
+      TileCursor<false> cp;
       cp.init(a.segs, s_begin, s_end);
       // The latent chunks read MN-major for P·V, and the ones tile.
       const uint64_t vdesc0 = sdesc_sw128(base + kOffKV, 8192, 1024);
@@ -654,7 +723,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<kF8>::kThreads, 
     // partial to the peer, and load the next segment's Q if tile
     // t ends a segment (its QK^T was the segment's last).  `own` keeps the
     // rounded values.
-    auto fetch_push = [&](uint32_t t, const TileCursor& c, uint32_t (&own)[kWords]) -> bool {
+    auto fetch_push = [&](uint32_t t, const TileCursor<kWin>& c, uint32_t (&own)[kWords]) -> bool {
       bool w = wait_phase<false, true>(BAR(B_S_FULL0 + (t & 1u)), (t >> 1) & 1u, err, abort_flag, a.wait_limit, a.wait_every);
       if (!__all_sync(0xffffffffu, w)) return false;
       tc_fence_after();
@@ -700,8 +769,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<kF8>::kThreads, 
         mbar_arrive_expect_tx(BAR(B_X_FULL0 + t), (uint32_t)kXBytes);
         armed[t] = (int32_t)t;
       }
-    TileCursor cf;  // this warpgroup's tile
-    cf.init(a.segs, s_begin, s_end);
+    TileCursor<kWin> cf;  // this warpgroup's tile
+    cf.init(a.segs, s_begin, s_end, kWin ? win->sinks : 0);
     if (wg == 1 && cf.valid()) cf.next();
     if (wg == 0 && G > 0) load_q(s_begin);
     uint32_t own[kWords];
@@ -736,8 +805,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<kF8>::kThreads, 
       }
 
       // ---- causal/length mask and the row max of this tile
-      const int valid = cf.vis - cf.pg * kPage;
-      if (valid < kPage) {
+      if constexpr (kWin) {
+        const uint64_t seen = cf.visible();
+        if (seen != ~0ull) {
+#pragma unroll
+          for (int j = 0; j < kWords; ++j) {
+            if (!((seen >> (2 * j)) & 1u)) own[j] = (own[j] & 0xFFFF0000u) | 0xFC00u;
+            if (!((seen >> (2 * j + 1)) & 1u)) own[j] = (own[j] & 0x0000FFFFu) | 0xFC000000u;
+          }
+        }
+      } else if (const int valid = cf.vis - cf.pg * kPage; valid < kPage) {
 #pragma unroll
         for (int j = 0; j < kWords; ++j) {
           if (2 * j >= valid) own[j] = (own[j] & 0xFFFF0000u) | 0xFC00u;          // low half -> -inf
@@ -956,7 +1033,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<kF8>::kThreads, 
 #undef BAR
 }
 
-// Merge split rows: lse = log2 Σ 2^{lse_s} (log2 domain), o = Σ 2^{lse_s - lse} o_s.
+template <bool kF8>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<kF8>::kThreads, 1)
+    decode_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constant__ CUtensorMap rope_map,
+                  const DecodeArgs a) {
+  decode_body<kF8, false>(kv_map, rope_map, a, nullptr);
+}
+
+template <bool kF8>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<kF8>::kThreads, 1)
+    decode_window_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constant__ CUtensorMap rope_map,
+                         const DecodeArgs a, const __grid_constant__ WindowArgs win) {
+  decode_body<kF8, true>(kv_map, rope_map, a, &win);
+}
+
 }  // namespace decode
 
 int decode_smem_bytes() { return decode::Layout<false>::kSmemBytes; }
@@ -966,6 +1056,17 @@ template <bool kF8>
 static cudaError_t decode_prepare() {
   return cudaFuncSetAttribute(decode::decode_kernel<kF8>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                               decode::Layout<kF8>::kSmemBytes);
+}
+
+template <bool kF8>
+static cudaError_t run_window(const CUtensorMap& kv_map, const CUtensorMap& rope_map, const DecodeArgs& args,
+                              const WindowArgs& window, int num_clusters, cudaStream_t stream) {
+  auto* kern = decode::decode_window_kernel<kF8>;
+  constexpr int smem = decode::Layout<kF8>::kSmemBytes;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  kern<<<2 * num_clusters, decode::Layout<kF8>::kThreads, smem, stream>>>(kv_map, rope_map, args, window);
+  return cudaGetLastError();
 }
 
 cudaError_t decode_max_clusters(int* out) {
@@ -996,6 +1097,12 @@ cudaError_t launch_decode(const CUtensorMap& kv_map, const CUtensorMap& rope_map
     decode::decode_kernel<false><<<2 * num_clusters, decode::Layout<false>::kThreads,
                                    decode::Layout<false>::kSmemBytes, stream>>>(kv_map, rope_map, args);
   return cudaGetLastError();
+}
+
+cudaError_t launch_decode_window(const CUtensorMap& kv_map, const CUtensorMap& rope_map, const DecodeArgs& args,
+                                 const WindowArgs& window, int num_clusters, bool fp8, cudaStream_t stream) {
+  return fp8 ? run_window<true>(kv_map, rope_map, args, window, num_clusters, stream)
+             : run_window<false>(kv_map, rope_map, args, window, num_clusters, stream);
 }
 
 }  // namespace mla

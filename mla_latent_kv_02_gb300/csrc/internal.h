@@ -21,7 +21,7 @@ mla_status set_last_error(mla_status s, const char* message);
 //   [8..15] reserved
 //   seg_off   at kPlanHeader, num_clusters + 1 entries
 //   segments  at seg_base, num_segments x 8: {row, b, page_begin, page_end,
-//             visible, out_slot (-1 = final), 0, 0}
+//             visible, out_slot (-1 = final), window's first token, 0}
 //   split rows at split_base, num_split_rows x 4: {row, slot_begin, n_slots, 0}
 constexpr int kPlanHeader = 16;
 constexpr int kSegWords = 8;
@@ -40,6 +40,38 @@ inline int64_t plan_max_split_rows(int64_t T, int64_t num_clusters) {
   return T < num_clusters ? T : num_clusters;
 }
 inline int64_t plan_max_partials(int64_t num_clusters) { return 2 * num_clusters; }
+
+// Sliding window with sinks: a row at position p sees the tokens j <= p with
+// j < sinks or j >= lo, lo = p - window + 1.  A plan segment carries lo in
+// word 6 (0: every token up to p; the planner writes 0 whenever lo <= sinks),
+// and its page_begin / page_end count the tiles the row reads: its sink
+// pages, then its window pages.
+//   * full sink pages 0 .. sinks / 64 - 1, then a page with the last
+//     sinks % 64 sinks, unless
+//   * that page is the window's first page (`shared`: one tile, two visible
+//     pieces), or
+//   * the window's first page has room for them before lo (`merged`: the tile
+//     is loaded from both pages, its first `split` = sinks % 64 rounded up to
+//     eight tokens from the sinks' page and the rest from the window's page).
+struct WindowTiles {
+  int32_t sink_tiles;  // tiles before the window's first page
+  int32_t skip;        // page of tile v: v < sink_tiles ? v : v + skip
+  int32_t head;        // sinks visible at the start of tile sink_tiles
+  int32_t merged;      // tile sink_tiles takes its first `split` tokens from page sinks / 64
+};
+__host__ __device__ inline int32_t window_split(int32_t sinks) { return (sinks % 64 + 7) / 8 * 8; }
+__host__ __device__ inline WindowTiles window_tiles(int32_t lo, int32_t sinks) {
+  WindowTiles w = {0, 0, 0, 0};
+  if (lo == 0) return w;
+  const int32_t first = lo / 64, full = sinks / 64, rest = sinks % 64;
+  const bool shared = rest > 0 && first == full;
+  const bool merged = rest > 0 && !shared && window_split(sinks) <= lo % 64;
+  w.sink_tiles = full + (rest > 0 && !shared && !merged ? 1 : 0);
+  w.skip = first - w.sink_tiles;
+  w.head = shared || merged ? rest : 0;
+  w.merged = merged ? 1 : 0;
+  return w;
+}
 
 struct DecodeArgs {
   const uint16_t* q_abs;  // bf16 [T, 128, 512]
@@ -88,6 +120,8 @@ struct PrefillArgs {
   float scale_log2;     // scale * log2(e)
   uint16_t* out;        // bf16 [rows, 128, 128]
   int32_t* dev_err;
+  int32_t window;       // sliding window with sinks over the packed rows (launch_prefill_window)
+  int32_t sinks;
   PrefillSeq seq[kPrefillMaxSeqs];
 };
 
@@ -102,6 +136,22 @@ struct GatherBatch {
   int64_t off[kPrefillMaxSeqs];
 };
 
+// The packed gather of windowed sequences: row j of sequence i comes from
+// position j < cut[i] ? j : j + shift[i].
+struct WindowGather {
+  int32_t nb;
+  int32_t max_pages;
+  int64_t total;        // Σ n[i]
+  int64_t num_pages;
+  const int32_t* block_table;
+  int32_t* dev_err;
+  int32_t b[kPrefillMaxSeqs];
+  int32_t n[kPrefillMaxSeqs];
+  int32_t cut[kPrefillMaxSeqs];
+  int32_t shift[kPrefillMaxSeqs];
+  int32_t off[kPrefillMaxSeqs];
+};
+
 struct CombineArgs {
   const int32_t* split_rows;
   const float* part_o;
@@ -113,6 +163,16 @@ struct CombineArgs {
   int32_t* dev_err;
 };
 
+// What the windowed decode takes beside DecodeArgs: the boxes of a merged
+// tile, head (split rows) and tail (64 - split rows).  With split == 0 no tile
+// is merged and the maps are not read.
+struct WindowArgs {
+  CUtensorMap kv_head, kv_tail;      // bf16: one 64-column chunk a box; FP8: 256 codes a row
+  CUtensorMap rope_head, rope_tail;
+  int32_t sinks;
+  int32_t split;                     // window_split(sinks)
+};
+
 int decode_smem_bytes();
 int decode_threads();
 cudaError_t decode_max_clusters(int* out);
@@ -122,6 +182,8 @@ cudaError_t decode_max_clusters(int* out);
 // swizzle), rope_map as above over the 640-byte rows; args.kv_scales set.
 cudaError_t launch_decode(const CUtensorMap& kv_map, const CUtensorMap& rope_map, const DecodeArgs& args,
                           int num_clusters, bool fp8, cudaStream_t stream);
+cudaError_t launch_decode_window(const CUtensorMap& kv_map, const CUtensorMap& rope_map, const DecodeArgs& args,
+                                 const WindowArgs& window, int num_clusters, bool fp8, cudaStream_t stream);
 cudaError_t launch_combine(const CombineArgs& args, int num_split_rows, cudaStream_t stream);
 
 cudaError_t launch_kv_append(const uint16_t* c_kv_new, const uint16_t* k_r_new, const int64_t* slots, int32_t n,
@@ -158,6 +220,9 @@ cudaError_t launch_gather_batch(const uint16_t* kv_cache, int64_t num_pages, con
                                 int32_t max_pages, const GatherBatch& g, uint16_t* out, int32_t* dev_err,
                                 cudaStream_t stream);
 
+cudaError_t launch_gather_window(const void* cache, const float* scales, bool fp8, const WindowGather& g,
+                                 uint16_t* out, cudaStream_t stream);
+
 // Decompress-branch expansion: K_c and V_c in one pass (head-major outputs).
 cudaError_t launch_expand_kv(const CUtensorMap& a_map, const CUtensorMap& k_map, const CUtensorMap& v_map,
                              const CUtensorMap& kc_map, const CUtensorMap& vc_map, int32_t n, int32_t* err,
@@ -166,6 +231,9 @@ int prefill_smem_bytes();
 cudaError_t launch_prefill_attn(const CUtensorMap& q_map, const CUtensorMap& r_map, const CUtensorMap& k_map,
                                 const CUtensorMap& kr_map, const CUtensorMap& v_map, const PrefillArgs& args,
                                 cudaStream_t stream);
+cudaError_t launch_prefill_window(const CUtensorMap& q_map, const CUtensorMap& r_map, const CUtensorMap& k_map,
+                                  const CUtensorMap& kr_map, const CUtensorMap& v_map, const PrefillArgs& args,
+                                  cudaStream_t stream);
 
 // Per-head GEMM C[t, h, :] = A[t, h, :] · W[h] (bf16 in, fp32 accumulate, bf16 out).
 enum class HeadGemm { kAbsorbQ, kUpV };

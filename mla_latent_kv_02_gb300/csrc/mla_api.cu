@@ -92,15 +92,17 @@ mla_status make_map(CUtensorMap* m, const void* base, int rank, const uint64_t* 
 struct PlanRow {
   int32_t b;
   int32_t visible;
-  int32_t npages;
+  int32_t npages;  // tiles the row reads
+  int32_t lo;      // the window's first token; 0: the row sees every token up to its own
 };
 
 // Minimum 64-token tiles per cluster: below it, the per-range fixed costs
 // (query load, epilogue, a combine partial) outweigh the added parallelism.
 constexpr int64_t kMinTilesPerCluster = 2;
 
+// window == 0: full attention; otherwise a sliding window with sinks.
 mla_status build_plan(const int32_t* seq_lens, const int32_t* q_lens, int32_t B, int32_t num_clusters,
-                      int32_t* out, size_t out_words, mla_plan_info* info) {
+                      int32_t* out, size_t out_words, mla_plan_info* info, int32_t window = 0, int32_t sinks = 0) {
   if (B < 0) return fail(MLA_ERR_INVALID_ARG, "B = %d is negative", B);
   if (B > 0) {
     CHECK_PTR(seq_lens);
@@ -114,11 +116,15 @@ mla_status build_plan(const int32_t* seq_lens, const int32_t* q_lens, int32_t B,
     const int32_t n = seq_lens[b], q = q_lens[b];
     if (n < 1) return fail(MLA_ERR_INVALID_ARG, "seq_lens[%d] = %d < 1", b, n);
     if (q < 0 || q > n) return fail(MLA_ERR_INVALID_ARG, "q_lens[%d] = %d outside [0, seq_len = %d]", b, q, n);
-    max_pages = std::max<int32_t>(max_pages, (n + MLA_PAGE_SIZE - 1) / MLA_PAGE_SIZE);
+    max_pages = std::max<int32_t>(max_pages, (n - 1) / MLA_PAGE_SIZE + 1);
     for (int32_t i = 0; i < q; ++i) {
       const int32_t vis = n - q + i + 1;
-      const int32_t np = (vis + MLA_PAGE_SIZE - 1) / MLA_PAGE_SIZE;
-      rows.push_back({b, vis, np});
+      int32_t np = (vis - 1) / MLA_PAGE_SIZE + 1, lo = 0;
+      if (window > 0 && vis - (int64_t)window > (int64_t)sinks) {  // tokens between the sinks and the window
+        lo = vis - window;
+        np -= mla::window_tiles(lo, sinks).skip;
+      }
+      rows.push_back({b, vis, np, lo});
       total += np;
     }
     if ((int64_t)rows.size() > (int64_t)INT32_MAX / MLA_NUM_HEADS)
@@ -151,7 +157,7 @@ mla_status build_plan(const int32_t* seq_lens, const int32_t* q_lens, int32_t B,
   const int32_t clusters_per_lane = num_clusters / lanes;
   // segments
   struct Seg {
-    int32_t row, b, pb, pe, vis, slot;
+    int32_t row, b, pb, pe, vis, slot, lo;
   };
   std::vector<Seg> segs;
   std::vector<int32_t> seg_off;
@@ -175,7 +181,7 @@ mla_status build_plan(const int32_t* seq_lens, const int32_t* q_lens, int32_t B,
         const int32_t rr = lr[kk];
         const int64_t pb = std::max<int64_t>(lo - rs, 0), pe = std::min<int64_t>(hi - rs, rows[rr].npages);
         if (pe <= pb) continue;
-        segs.push_back({rr, rows[rr].b, (int32_t)pb, (int32_t)pe, rows[rr].visible, -1});
+        segs.push_back({rr, rows[rr].b, (int32_t)pb, (int32_t)pe, rows[rr].visible, -1, rows[rr].lo});
         ++row_pieces[rr];
       }
     }
@@ -202,7 +208,8 @@ mla_status build_plan(const int32_t* seq_lens, const int32_t* q_lens, int32_t B,
     return fail(MLA_ERR_INVALID_ARG, "plan buffer holds %zu bytes, %lld needed", out_words * 4,
                 (long long)L.words * 4);
   std::fill(out, out + L.words, 0);
-  out[0] = (int32_t)MLA_PLAN_MAGIC;
+  const uint32_t magic = window > 0 ? MLA_WINDOW_PLAN_MAGIC : MLA_PLAN_MAGIC;
+  out[0] = (int32_t)magic;
   out[1] = (int32_t)T;
   out[2] = B;
   out[3] = (int32_t)used;
@@ -219,10 +226,11 @@ mla_status build_plan(const int32_t* seq_lens, const int32_t* q_lens, int32_t B,
     w[3] = segs[i].pe;
     w[4] = segs[i].vis;
     w[5] = segs[i].slot;
+    w[6] = segs[i].lo;
   }
   std::copy(split.begin(), split.end(), out + L.split_base);
   if (info) {
-    info->magic = MLA_PLAN_MAGIC;
+    info->magic = magic;
     info->T = (int32_t)T;
     info->B = B;
     info->num_clusters = (int32_t)used;
@@ -716,6 +724,12 @@ static mla_status head_gemm(mla::HeadGemm kind, const void* a, const void* w, vo
   return MLA_OK;
 }
 
+static mla_status window_check(int32_t window, int32_t sinks) {
+  if (window < 1) return fail(MLA_ERR_INVALID_ARG, "window = %d < 1", window);
+  if (sinks < 0) return fail(MLA_ERR_INVALID_ARG, "sinks = %d < 0", sinks);
+  return MLA_OK;
+}
+
 // ------------------------------------------------------------------ decompress branch
 int32_t mla_prefill_threshold(void) { return MLA_PREFILL_THRESHOLD; }
 
@@ -794,7 +808,8 @@ static mla_status prefill_attention_launch(const void* q_c, const void* q_r, int
   if (s == MLA_OK) s = make_map(&vm, v_c, 3, kd, ks, kbox, "V_c");
   if (s == MLA_OK) s = make_map(&krm, rows, 2, krd, krs, box2, "k_R rows");
   if (s != MLA_OK) return s;
-  cudaError_t e = mla::launch_prefill_attn(qm, rm, km, krm, vm, a, (cudaStream_t)stream);
+  cudaError_t e = a.window > 0 ? mla::launch_prefill_window(qm, rm, km, krm, vm, a, (cudaStream_t)stream)
+                               : mla::launch_prefill_attn(qm, rm, km, krm, vm, a, (cudaStream_t)stream);
   if (e != cudaSuccess) return cuda_fail(e, "prefill attention launch");
   return MLA_OK;
 }
@@ -926,6 +941,148 @@ mla_status mla_prefill_decompress_batch(const void* q_c, const void* q_r, const 
   return prefill_attention_launch(q_c, q_r, rows_end, rows, k_c, v_c, total, a, stream);
 }
 
+// The tokens of one sequence that a chunk's window and sinks keep, packed:
+// row j holds position j < cut ? j : j + shift.
+struct KeptTokens {
+  int32_t n, cut, shift;
+};
+static KeptTokens kept_tokens(int32_t M, int32_t N, int32_t window, int32_t sinks) {
+  const int64_t lo = (int64_t)N - M + 1 - window;  // the first row's window starts here
+  if (lo <= sinks) return {N, N, 0};
+  return {(int32_t)(sinks + N - lo), sinks, (int32_t)(lo - sinks)};
+}
+
+mla_status mla_prefill_window_workspace_size(const int32_t* q_lens, const int32_t* n_tokens, int32_t nb,
+                                             int32_t window, int32_t sinks, size_t* bytes) {
+  CHECK_PTR(bytes);
+  if (nb < 0 || nb > mla::kPrefillMaxSeqs)
+    return fail(MLA_ERR_INVALID_ARG, "nb = %d outside [0, %d]", nb, mla::kPrefillMaxSeqs);
+  mla_status s = window_check(window, sinks);
+  if (s != MLA_OK) return s;
+  if (nb > 0) {
+    CHECK_PTR(q_lens);
+    CHECK_PTR(n_tokens);
+  }
+  int64_t total = 0;
+  for (int32_t i = 0; i < nb; ++i) {
+    if (q_lens[i] < 1 || n_tokens[i] < q_lens[i])
+      return fail(MLA_ERR_INVALID_ARG, "sequence %d: q_len %d must be in [1, n_tokens = %d]", i, q_lens[i], n_tokens[i]);
+    total += kept_tokens(q_lens[i], n_tokens[i], window, sinks).n;
+  }
+  if (total > (1 << 24)) return fail(MLA_ERR_INVALID_ARG, "%lld kept tokens in all: too many", (long long)total);
+  *bytes = prefill_ws_bytes(total);
+  return MLA_OK;
+}
+
+static mla_status prefill_window(const void* q_c, const void* q_r, const int32_t* seq_ids, const int32_t* q_starts,
+                                 const int32_t* q_lens, const int32_t* n_tokens, int32_t nb, int32_t window,
+                                 int32_t sinks, const void* cache, const float* scales, bool fp8, int64_t num_pages,
+                                 const int32_t* block_table, int32_t batch, int32_t max_pages, const void* w_uk,
+                                 const void* w_uv, float scale, void* workspace, size_t ws_bytes, void* out,
+                                 int32_t* dev_err, void* stream) {
+  if (nb < 0 || nb > mla::kPrefillMaxSeqs)
+    return fail(MLA_ERR_INVALID_ARG, "nb = %d outside [0, %d]", nb, mla::kPrefillMaxSeqs);
+  mla_status s = window_check(window, sinks);
+  if (s != MLA_OK) return s;
+  if (nb == 0) return MLA_OK;
+  CHECK_PTR(seq_ids);
+  CHECK_PTR(q_starts);
+  CHECK_PTR(q_lens);
+  CHECK_PTR(n_tokens);
+  CHECK_PTR(q_c);
+  CHECK_PTR(q_r);
+  CHECK_PTR(cache);
+  CHECK_PTR(block_table);
+  CHECK_PTR(w_uk);
+  CHECK_PTR(w_uv);
+  CHECK_PTR(workspace);
+  CHECK_PTR(out);
+  CHECK_PTR(dev_err);
+  if (fp8) {
+    CHECK_PTR(scales);
+    CHECK_ALIGN16(scales);
+  }
+  CHECK_ALIGN16(q_c);
+  CHECK_ALIGN16(q_r);
+  CHECK_ALIGN16(cache);
+  CHECK_ALIGN16(w_uk);
+  CHECK_ALIGN16(w_uv);
+  CHECK_ALIGN16(workspace);
+  CHECK_ALIGN16(out);
+  if (!aligned(block_table, 4) || !aligned(dev_err, 4))
+    return fail(MLA_ERR_MISALIGNED, "block_table and dev_err must be 4-byte aligned");
+  if (!(scale > 0.f) || !std::isfinite(scale)) return fail(MLA_ERR_INVALID_ARG, "scale must be finite and positive");
+  if (num_pages < 1 || batch < 1 || max_pages < 1) return fail(MLA_ERR_INVALID_ARG, "bad pool/table sizes");
+  mla::WindowGather g = {};
+  mla::PrefillArgs a = {};
+  int64_t total = 0, rows_end = 0;
+  for (int32_t i = 0; i < nb; ++i) {
+    const int32_t b = seq_ids[i], M = q_lens[i], N = n_tokens[i], q0 = q_starts[i];
+    if (b < 0 || b >= batch) return fail(MLA_ERR_INVALID_ARG, "seq_ids[%d] = %d outside [0, %d)", i, b, batch);
+    if (M < 1 || N < M)
+      return fail(MLA_ERR_INVALID_ARG, "sequence %d: q_len %d must be in [1, n_tokens = %d]", i, M, N);
+    if ((N - 1) / MLA_PAGE_SIZE >= max_pages)
+      return fail(MLA_ERR_INVALID_ARG, "sequence %d: %d tokens need more than max_pages = %d pages", i, N, max_pages);
+    if (q0 < 0) return fail(MLA_ERR_INVALID_ARG, "q_starts[%d] = %d < 0", i, q0);
+    const KeptTokens k = kept_tokens(M, N, window, sinks);
+    g.b[i] = b;
+    g.n[i] = k.n;
+    g.cut[i] = k.cut;
+    g.shift[i] = k.shift;
+    g.off[i] = (int32_t)total;
+    a.seq[i] = {M, k.n, q0, (int32_t)total};
+    total += k.n;
+    rows_end = std::max<int64_t>(rows_end, (int64_t)q0 + M);
+    if (total > (1 << 24)) return fail(MLA_ERR_INVALID_ARG, "%lld kept tokens in all: too many", (long long)total);
+  }
+  if (rows_end > (1 << 24)) return fail(MLA_ERR_INVALID_ARG, "query rows past 2^24");
+  if (ws_bytes < prefill_ws_bytes(total))
+    return fail(MLA_ERR_INVALID_ARG, "workspace holds %zu bytes, %lld kept tokens need %zu", ws_bytes,
+                (long long)total, prefill_ws_bytes(total));
+  g.nb = nb;
+  g.max_pages = max_pages;
+  g.total = total;
+  g.num_pages = num_pages;
+  g.block_table = block_table;
+  g.dev_err = dev_err;
+  a.nb = nb;
+  a.scale_log2 = (float)((double)scale * 1.4426950408889634);
+  a.out = (uint16_t*)out;
+  a.dev_err = dev_err;
+  a.window = window;
+  a.sinks = sinks;
+  uint8_t* rows = (uint8_t*)workspace;
+  uint8_t* k_c = rows + prefill_rows_bytes(total);
+  uint8_t* v_c = k_c + (size_t)total * MLA_NUM_HEADS * MLA_HEAD_DIM_C * 2;
+  cudaError_t e = mla::launch_gather_window(cache, scales, fp8, g, (uint16_t*)rows, (cudaStream_t)stream);
+  if (e != cudaSuccess) return cuda_fail(e, "window gather launch");
+  s = mla_expand_kv(rows, (int32_t)total, w_uk, w_uv, k_c, v_c, dev_err, stream);
+  if (s != MLA_OK) return s;
+  return prefill_attention_launch(q_c, q_r, rows_end, rows, k_c, v_c, total, a, stream);
+}
+
+mla_status mla_prefill_window_batch(const void* q_c, const void* q_r, const int32_t* seq_ids, const int32_t* q_starts,
+                                    const int32_t* q_lens, const int32_t* n_tokens, int32_t nb, int32_t window,
+                                    int32_t sinks, const void* kv_cache, int64_t num_pages, const int32_t* block_table,
+                                    int32_t batch, int32_t max_pages, const void* w_uk, const void* w_uv, float scale,
+                                    void* workspace, size_t ws_bytes, void* out, int32_t* dev_err, void* stream) {
+  return prefill_window(q_c, q_r, seq_ids, q_starts, q_lens, n_tokens, nb, window, sinks, kv_cache, nullptr, false,
+                        num_pages, block_table, batch, max_pages, w_uk, w_uv, scale, workspace, ws_bytes, out, dev_err,
+                        stream);
+}
+
+mla_status mla_prefill_window_batch_fp8(const void* q_c, const void* q_r, const int32_t* seq_ids,
+                                        const int32_t* q_starts, const int32_t* q_lens, const int32_t* n_tokens,
+                                        int32_t nb, int32_t window, int32_t sinks, const void* rows,
+                                        const float* scales, int64_t num_pages, const int32_t* block_table,
+                                        int32_t batch, int32_t max_pages, const void* w_uk, const void* w_uv,
+                                        float scale, void* workspace, size_t ws_bytes, void* out, int32_t* dev_err,
+                                        void* stream) {
+  return prefill_window(q_c, q_r, seq_ids, q_starts, q_lens, n_tokens, nb, window, sinks, rows, scales, true,
+                        num_pages, block_table, batch, max_pages, w_uk, w_uv, scale, workspace, ws_bytes, out, dev_err,
+                        stream);
+}
+
 mla_status mla_prefill_decompress(const void* q_c, const void* q_r, int32_t M, const void* kv_cache, int64_t num_pages,
                                   const int32_t* block_table, int32_t max_pages, int32_t b, int32_t N,
                                   const void* w_uk, const void* w_uv, float scale, void* workspace, size_t ws_bytes,
@@ -998,13 +1155,51 @@ mla_status mla_decode_plan(const int32_t* seq_lens_host, const int32_t* q_lens_h
   return MLA_OK;
 }
 
+mla_status mla_window_plan_host(const int32_t* seq_lens, const int32_t* q_lens, int32_t B, int32_t window,
+                                int32_t sinks, int32_t num_clusters, void* plan_host, size_t plan_bytes,
+                                mla_window_info* info) {
+  CHECK_PTR(plan_host);
+  CHECK_PTR(info);
+  if (!aligned(plan_host, 4)) return fail(MLA_ERR_MISALIGNED, "plan_host is not 4-byte aligned");
+  mla_status s = window_check(window, sinks);
+  if (s != MLA_OK) return s;
+  s = build_plan(seq_lens, q_lens, B, num_clusters, (int32_t*)plan_host, plan_bytes / 4, &info->plan, window, sinks);
+  if (s != MLA_OK) return s;
+  info->window = window;
+  info->sinks = sinks;
+  return MLA_OK;
+}
+
+mla_status mla_window_plan(const int32_t* seq_lens_host, const int32_t* q_lens_host, int32_t B, int32_t window,
+                           int32_t sinks, int32_t num_clusters, void* plan_dev, size_t plan_bytes,
+                           mla_window_info* info, void* stream) {
+  CHECK_PTR(plan_dev);
+  CHECK_PTR(info);
+  CHECK_ALIGN16(plan_dev);
+  std::vector<int32_t> host(plan_bytes / 4 + 1);
+  mla_status s = mla_window_plan_host(seq_lens_host, q_lens_host, B, window, sinks, num_clusters, host.data(),
+                                      plan_bytes, info);
+  if (s != MLA_OK) return s;
+  // Pageable source: the call returns once the data is staged, so `host` may go.
+  cudaError_t e = cudaMemcpyAsync(plan_dev, host.data(), info->plan.plan_bytes, cudaMemcpyHostToDevice,
+                                  (cudaStream_t)stream);
+  if (e != cudaSuccess) return cuda_fail(e, "plan copy");
+  return MLA_OK;
+}
+
+// window: the windowed decode's parameters, null for full attention.
 static mla_status decode_common(const void* q_abs, const void* q_r, const void* kv_cache, const float* kv_scales,
                                 int64_t num_pages, const int32_t* block_table, int32_t max_pages,
                                 const void* plan_dev, const mla_plan_info* info, float scale, void* workspace,
                                 size_t ws_bytes, void* o_lat, float* lse, int32_t* dev_err, void* stream,
-                                bool fp8) {
+                                bool fp8, const mla_window_info* window = nullptr) {
   CHECK_PTR(info);
-  if (info->magic != MLA_PLAN_MAGIC) return fail(MLA_ERR_INVALID_ARG, "info is not a decode plan summary");
+  if (info->magic != (window ? MLA_WINDOW_PLAN_MAGIC : MLA_PLAN_MAGIC))
+    return fail(MLA_ERR_INVALID_ARG, "info is not a %s plan summary", window ? "window" : "decode");
+  if (window) {
+    const mla_status ws = window_check(window->window, window->sinks);
+    if (ws != MLA_OK) return ws;
+  }
   if (info->T == 0 || info->num_clusters == 0) return MLA_OK;
   CHECK_PTR(q_abs);
   CHECK_PTR(q_r);
@@ -1069,6 +1264,38 @@ static mla_status decode_common(const void* q_abs, const void* q_r, const void* 
     if (s != MLA_OK) return s;
   }
 
+  // Merged tiles: the sinks' first `split` tokens of a page and the rest of
+  // another as boxes of their own.
+  mla::WindowArgs win = {};
+  if (window) {
+    win.sinks = window->sinks;
+    win.split = mla::window_split(window->sinks);
+    if (win.split > 0 && win.split < MLA_PAGE_SIZE) {
+      for (int part = 0; part < 2; ++part) {
+        const uint32_t n = (uint32_t)(part ? MLA_PAGE_SIZE - win.split : win.split);
+        CUtensorMap* km = part ? &win.kv_tail : &win.kv_head;
+        CUtensorMap* rm = part ? &win.rope_tail : &win.rope_head;
+        const uint64_t tokens = (uint64_t)num_pages * MLA_PAGE_SIZE;
+        const uint32_t rbox[2] = {32, n};
+        if (fp8) {
+          const uint64_t cdims[2] = {MLA_FP8_ROW_BYTES, tokens}, rdims[2] = {MLA_FP8_ROW_BYTES / 2, tokens};
+          const uint64_t str[1] = {MLA_FP8_ROW_BYTES};
+          const uint32_t cbox[2] = {256, n};
+          s = make_map(km, kv_cache, 2, cdims, str, cbox, "fp8 codes of a merged tile", CU_TENSOR_MAP_SWIZZLE_NONE,
+                       CU_TENSOR_MAP_DATA_TYPE_UINT8);
+          if (s == MLA_OK) s = make_map(rm, kv_cache, 2, rdims, str, rbox, "RoPE of a merged tile", CU_TENSOR_MAP_SWIZZLE_64B);
+        } else {
+          const uint64_t ldims[3] = {64, tokens, MLA_LATENT_DIM / 64}, rdims[2] = {MLA_TOKEN_ELEMS, tokens};
+          const uint64_t lstr[2] = {(uint64_t)kRowBytes, 128}, rstr[1] = {(uint64_t)kRowBytes};
+          const uint32_t lbox[3] = {64, n, 1};
+          s = make_map(km, kv_cache, 3, ldims, lstr, lbox, "latent chunk of a merged tile");
+          if (s == MLA_OK) s = make_map(rm, kv_cache, 2, rdims, rstr, rbox, "RoPE of a merged tile", CU_TENSOR_MAP_SWIZZLE_64B);
+        }
+        if (s != MLA_OK) return s;
+      }
+    }
+  }
+
   const mla::PlanLayout L = mla::plan_layout(info->num_clusters, info->num_segments, info->num_split_rows);
   const int32_t* plan = (const int32_t*)plan_dev;
   float* part_o = (float*)workspace;
@@ -1095,7 +1322,8 @@ static mla_status decode_common(const void* q_abs, const void* q_r, const void* 
   a.kv_scales = fp8 ? kv_scales : nullptr;
   a.wait_limit = g_decode_wait_limit.load(std::memory_order_relaxed);
   a.wait_every = a.wait_limit < (1ull << 20) ? 0u : 255u;
-  cudaError_t e = mla::launch_decode(kv_map, rope_map, a, info->num_clusters, fp8, (cudaStream_t)stream);
+  cudaError_t e = window ? mla::launch_decode_window(kv_map, rope_map, a, win, info->num_clusters, fp8, (cudaStream_t)stream)
+                         : mla::launch_decode(kv_map, rope_map, a, info->num_clusters, fp8, (cudaStream_t)stream);
   if (e != cudaSuccess) return cuda_fail(e, "decode launch");
   if (info->num_split_rows > 0) {
     mla::CombineArgs c = {};
@@ -1127,6 +1355,24 @@ mla_status mla_decode_paged_fp8(const void* q_abs, const void* q_r, const void* 
                                 size_t ws_bytes, void* o_lat, float* lse, int32_t* dev_err, void* stream) {
   return decode_common(q_abs, q_r, rows, scales, num_pages, block_table, max_pages, plan_dev, info, scale,
                        workspace, ws_bytes, o_lat, lse, dev_err, stream, true);
+}
+
+mla_status mla_decode_window(const void* q_abs, const void* q_r, const void* kv_cache, int64_t num_pages,
+                             const int32_t* block_table, int32_t max_pages, const void* plan_dev,
+                             const mla_window_info* info, float scale, void* workspace, size_t ws_bytes, void* o_lat,
+                             float* lse, int32_t* dev_err, void* stream) {
+  CHECK_PTR(info);
+  return decode_common(q_abs, q_r, kv_cache, nullptr, num_pages, block_table, max_pages, plan_dev, &info->plan, scale,
+                       workspace, ws_bytes, o_lat, lse, dev_err, stream, false, info);
+}
+
+mla_status mla_decode_window_fp8(const void* q_abs, const void* q_r, const void* rows, const float* scales,
+                                 int64_t num_pages, const int32_t* block_table, int32_t max_pages,
+                                 const void* plan_dev, const mla_window_info* info, float scale, void* workspace,
+                                 size_t ws_bytes, void* o_lat, float* lse, int32_t* dev_err, void* stream) {
+  CHECK_PTR(info);
+  return decode_common(q_abs, q_r, rows, scales, num_pages, block_table, max_pages, plan_dev, &info->plan, scale,
+                       workspace, ws_bytes, o_lat, lse, dev_err, stream, true, info);
 }
 
 mla_status mla_debug_set_decode_wait_limit(uint64_t cycles) {

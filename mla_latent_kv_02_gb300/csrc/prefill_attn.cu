@@ -97,14 +97,23 @@ static_assert(B_COUNT <= kNumBars, "barrier area too small");
 __device__ __forceinline__ __half2 as_h2(uint32_t u) { return *reinterpret_cast<const __half2*>(&u); }
 __device__ __forceinline__ uint32_t as_u32(__half2 h) { return *reinterpret_cast<const uint32_t*>(&h); }
 
+// The low n bits set, n clamped to [0, 64].
+__device__ __forceinline__ uint64_t bits_below(int n) {
+  return n <= 0 ? 0ull : n >= 64 ? ~0ull : (1ull << n) - 1ull;
+}
+
 // q_map: q_c [M, 128, 128] as {128, 128 heads, M}; r_map: q_r {64, 128, M};
 // k_map / v_map: K_c / V_c [128, N, 128] as {128, N, 128 heads}; kr_map: the
 // gathered cache rows [N, 576] as {576, N} (k_R at column 512).  Boxes of
 // 64 columns x 128 rows, 128-byte swizzle.
-__global__ void __launch_bounds__(kThreads, 1)
-    prefill_attn_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__ CUtensorMap r_map,
-                        const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap kr_map,
-                        const __grid_constant__ CUtensorMap v_map, const PrefillArgs a) {
+// kWin: row i (position pos) sees the tokens j <= pos with j < sinks or
+// j > pos - window.  The CTA reads the key tiles that hold sinks and those
+// from its first row's window on; a row may see nothing of its CTA's first
+// tiles (its window starts later), so its running maximum starts at -inf.
+template <bool kWin>
+__device__ __forceinline__ void prefill_body(const CUtensorMap& q_map, const CUtensorMap& r_map,
+                                             const CUtensorMap& k_map, const CUtensorMap& kr_map,
+                                             const CUtensorMap& v_map, const PrefillArgs& a) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t bars = raw;
@@ -122,7 +131,15 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int M = sq.M, N = sq.N;
   const int kv_base = N - M;                          // position of query row 0
   const int last_row = min(i0 + kBM, M) - 1;
-  const int n_tiles = (kv_base + last_row) / kBN + 1;  // tiles any row of this CTA sees
+  // tiles any row of this CTA sees; the key tile of tile j is j, from sink_tiles on j + skip
+  int n_tiles = (kv_base + last_row) / kBN + 1, sink_tiles = 0, skip = 0;
+  if (kWin) {
+    const int first = max(kv_base + i0 - a.window + 1, 0) / kBN;
+    sink_tiles = a.sinks / kBN + (a.sinks % kBN > 0 ? 1 : 0);
+    skip = max(first - sink_tiles, 0);
+    n_tiles -= skip;
+  }
+  auto key_tile = [&](int j) { return kWin && j >= sink_tiles ? j + skip : j; };
   int32_t* err = a.dev_err;
 
   if (threadIdx.x == 0) {
@@ -183,7 +200,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         bool progressed = false;
         if (nk < n_tiles && (nk < kStages ? (nk != kQStage || mbar_test_wait(BAR(B_Q_TMEM), 0))
                                           : mbar_test_wait(BAR(B_K_EMPTY + nk % kStages), ((nk - kStages) / kStages) & 1))) {
-          const int st = nk % kStages, t0 = sq.kv_off + nk * kBN;
+          const int st = nk % kStages, t0 = sq.kv_off + key_tile(nk) * kBN;
           const uint32_t dst = base + kOffK + st * kKBytes;
           mbar_arrive_expect_tx(BAR(B_K_FULL + st), (uint32_t)kKBytes);
           tma_load_3d(dst, &k_map, 0, t0, h, BAR(B_K_FULL + st));
@@ -193,7 +210,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           progressed = true;
         }
         if (nv < nk && (nv < kVStages || mbar_test_wait(BAR(B_V_EMPTY + nv % kVStages), ((nv - kVStages) / kVStages) & 1))) {
-          const int st = nv % kVStages, t0 = sq.kv_off + nv * kBN;
+          const int st = nv % kVStages, t0 = sq.kv_off + key_tile(nv) * kBN;
           const uint32_t dst = base + kOffV + st * kVBytes;
           mbar_arrive_expect_tx(BAR(B_V_FULL + st), (uint32_t)kVBytes);
           tma_load_3d(dst, &v_map, 0, t0, h, BAR(B_V_FULL + st));
@@ -352,8 +369,18 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(BAR(B_S_FREE + sb));
       // causal mask: token j*128 + 64 half + c is visible iff it is <= pos
-      const int valid = pos - j * kBN - 64 * half + 1;
-      if (valid < 64) {
+      if constexpr (kWin) {
+        const int base0 = key_tile(j) * kBN + 64 * half;
+        const uint64_t seen = bits_below(a.sinks - base0) & bits_below(pos + 1 - base0) |
+                              bits_below(pos + 1 - base0) & ~bits_below(pos - a.window + 1 - base0);
+        if (seen != ~0ull) {
+#pragma unroll
+          for (int k = 0; k < 32; ++k) {
+            if (!((seen >> (2 * k)) & 1u)) own[k] = (own[k] & 0xFFFF0000u) | 0xFC00u;
+            if (!((seen >> (2 * k + 1)) & 1u)) own[k] = (own[k] & 0x0000FFFFu) | 0xFC000000u;
+          }
+        }
+      } else if (const int valid = pos - j * kBN - 64 * half + 1; valid < 64) {
 #pragma unroll
         for (int k = 0; k < 32; ++k) {
           if (2 * k >= valid) own[k] = (own[k] & 0xFFFF0000u) | 0xFC00u;
@@ -391,7 +418,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         m = mt;
         resc = true;
       }
-      const __half2 mc2 = __float2half2_rn(-m * c2);
+      // windowed: a row that has seen nothing yet (m = -inf) takes P = 2^-inf = 0
+      const __half2 mc2 = __float2half2_rn(kWin && m == -INFINITY ? 0.f : -m * c2);
       float rs0 = 0.f, rs1 = 0.f;                  // row sum of the bf16 P the tensor core accumulates
 #pragma unroll
       for (int k = 0; k < 32; ++k) {
@@ -478,6 +506,20 @@ __global__ void __launch_bounds__(kThreads, 1)
 #undef BAR
 }
 
+__global__ void __launch_bounds__(kThreads, 1)
+    prefill_attn_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__ CUtensorMap r_map,
+                        const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap kr_map,
+                        const __grid_constant__ CUtensorMap v_map, const PrefillArgs a) {
+  prefill_body<false>(q_map, r_map, k_map, kr_map, v_map, a);
+}
+
+__global__ void __launch_bounds__(kThreads, 1)
+    prefill_window_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__ CUtensorMap r_map,
+                          const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap kr_map,
+                          const __grid_constant__ CUtensorMap v_map, const PrefillArgs a) {
+  prefill_body<true>(q_map, r_map, k_map, kr_map, v_map, a);
+}
+
 }  // namespace prefill
 }  // namespace mla
 
@@ -485,19 +527,30 @@ namespace mla {
 
 int prefill_smem_bytes() { return prefill::kSmemBytes; }
 
-cudaError_t launch_prefill_attn(const CUtensorMap& q_map, const CUtensorMap& r_map, const CUtensorMap& k_map,
-                                const CUtensorMap& kr_map, const CUtensorMap& v_map, const PrefillArgs& args,
-                                cudaStream_t stream) {
+template <typename Kernel>
+static cudaError_t launch_prefill(Kernel* kern, const CUtensorMap& q_map, const CUtensorMap& r_map,
+                                  const CUtensorMap& k_map, const CUtensorMap& kr_map, const CUtensorMap& v_map,
+                                  const PrefillArgs& args, cudaStream_t stream) {
   int max_m = 0;
   for (int i = 0; i < args.nb; ++i) max_m = args.seq[i].M > max_m ? args.seq[i].M : max_m;
   if (args.nb <= 0 || max_m <= 0) return cudaSuccess;
-  cudaError_t e = cudaFuncSetAttribute(prefill::prefill_attn_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       prefill::kSmemBytes);
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, prefill::kSmemBytes);
   if (e != cudaSuccess) return e;
   dim3 grid((max_m + prefill::kBM - 1) / prefill::kBM, 128, args.nb);
-  prefill::prefill_attn_kernel<<<grid, prefill::kThreads, prefill::kSmemBytes, stream>>>(q_map, r_map, k_map,
-                                                                                        kr_map, v_map, args);
+  kern<<<grid, prefill::kThreads, prefill::kSmemBytes, stream>>>(q_map, r_map, k_map, kr_map, v_map, args);
   return cudaGetLastError();
+}
+
+cudaError_t launch_prefill_attn(const CUtensorMap& q_map, const CUtensorMap& r_map, const CUtensorMap& k_map,
+                                const CUtensorMap& kr_map, const CUtensorMap& v_map, const PrefillArgs& args,
+                                cudaStream_t stream) {
+  return launch_prefill(prefill::prefill_attn_kernel, q_map, r_map, k_map, kr_map, v_map, args, stream);
+}
+
+cudaError_t launch_prefill_window(const CUtensorMap& q_map, const CUtensorMap& r_map, const CUtensorMap& k_map,
+                                  const CUtensorMap& kr_map, const CUtensorMap& v_map, const PrefillArgs& args,
+                                  cudaStream_t stream) {
+  return launch_prefill(prefill::prefill_window_kernel, q_map, r_map, k_map, kr_map, v_map, args, stream);
 }
 
 }  // namespace mla
