@@ -653,6 +653,38 @@ mla_status mla_gather_paged_nvfp4_batch(const void* rows, float tensor_scale, in
                                         const int32_t* seq_ids, const int64_t* out_offsets, int32_t nb,
                                         int64_t total_tokens, void* out, int32_t* dev_err, void* stream);
 
+/* ---------------------------------------------------------------------------
+ * Steps A2 and A5 with 4-bit weights: W_UK and W_UV held as signed 4-bit codes
+ * with one bf16 scale per group of `group` consecutive contraction values of a
+ * column (4.25 to 4.5 bits a weight against 16),
+ *   W[h, k, n] = scales[h, k / group, n] * code[h, k, n],  code in [-8, 7].
+ * words uint32 [128, K/8, N]: the code of k = 8 kb + i is the two's-complement
+ * nibble in bits [4i, 4i + 4) of words[h, kb, n]; scales bf16 [128, K/group, N].
+ * A2 has K = 128, N = 512 (W_UK), A5 K = 512, N = 128 (W_UV); group 32, 64 or
+ * 128 (else MLA_ERR_UNSUPPORTED).
+ * ------------------------------------------------------------------------- */
+
+/*
+ * Quantise bf16 weights w [128, K, N] into words and scales, once per model:
+ * of each group of a column, scale = bf16(amax / 7) and code = w / scale
+ * rounded to nearest even and clamped to [-8, 7]; a group whose scale is zero
+ * has zero codes.  Weights must be finite.  All pointers device, 16-byte aligned.
+ */
+mla_status mla_pack_w4(const void* w, int32_t K, int32_t N, int32_t group, void* words, void* scales, void* stream);
+
+/*
+ * mla_absorb_q and mla_up_v over such weights: q_c bf16 [T, 128, 128] -> q_abs
+ * bf16 [T, 128, 512]; o_lat bf16 [T, 128, 512] -> out bf16 [T, 128, 128].  The
+ * codes enter the products as integers and each group's scale multiplies the
+ * group's fp32 sum: one rounding, to the bf16 result.  T in [0, 2^18], 0 is a
+ * no-op; an input that overlaps the output is MLA_ERR_INVALID_ARG.  dev_err as
+ * for mla_absorb_q.
+ */
+mla_status mla_absorb_q_w4(const void* q_c, const void* words, const void* scales, int32_t group, void* q_abs,
+                           int32_t T, int32_t* dev_err, void* stream);
+mla_status mla_up_v_w4(const void* o_lat, const void* words, const void* scales, int32_t group, void* out, int32_t T,
+                       int32_t* dev_err, void* stream);
+
 /*
  * Synchronise `stream`, read the device error word into *word_out (may be
  * NULL) and map it: 0 -> MLA_OK, MLA_DEVERR_TIMEOUT set -> MLA_ERR_TIMEOUT,

@@ -90,6 +90,9 @@ SIGNATURES = {
                                            C.c_float, P, SZ, P, P, P]),
     "mla_prefill_window_batch_fp8": (C.c_int, [P, P, PI32, PI32, PI32, PI32, I32, I32, I32, P, P, I64, P, I32, I32, P,
                                                P, C.c_float, P, SZ, P, P, P]),
+    "mla_pack_w4": (C.c_int, [P, I32, I32, I32, P, P, P]),
+    "mla_absorb_q_w4": (C.c_int, [P, P, P, I32, P, I32, P, P]),
+    "mla_up_v_w4": (C.c_int, [P, P, P, I32, P, I32, P, P]),
     "mla_check": (C.c_int, [P, P, PI32]),
     "mla_debug_set_decode_wait_limit": (C.c_int, [C.c_uint64]),
     "mla_decode_paged_noalloc": (C.c_int, [P, P, P, I64, P, I32, PI32, PI32, I32, C.c_float, P, P, P, P]),

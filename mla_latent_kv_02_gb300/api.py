@@ -698,6 +698,48 @@ def mla_prefill_window_batch_fp8(q_c, q_r, rows, scales, block_table, seq_ids, q
                     q_lens, n_tokens, window, sinks, w_uk, w_uv, workspace, out, dev_err, scale, stream)
 
 
+# ------------------------------------------------------------------ 4-bit weights
+def mla_pack_w4(w, group: int, stream=None):
+    """Quantise W_UK [128, 128, 512] or W_UV [128, 512, 128] (bf16) to 4-bit codes
+    with a bf16 scale per group of the contraction (dim 1); returns (words, scales)."""
+    if not isinstance(w, torch.Tensor) or w.dim() != 3:
+        raise TypeError("w must be a torch.Tensor [128, K, N]")
+    K, N = w.shape[1], w.shape[2]
+    _need(w, "w", torch.bfloat16, (H, K, N))
+    if group < 8:
+        raise ValueError(f"group = {group}: 32, 64 and 128 are supported")
+    with torch.cuda.stream(stream):
+        words = torch.empty((H, K // 8, N), dtype=torch.int32, device=w.device)
+        scales = torch.empty((H, max(K // group, 1), N), dtype=torch.bfloat16, device=w.device)
+    _check(lib().mla_pack_w4(_ptr(w), int(K), int(N), int(group), _ptr(words), _ptr(scales), _stream(stream)))
+    return words, scales
+
+
+def _w4(call, x, x_name, words, scales, y, y_name, K, N, dev_err, stream) -> None:
+    T = x.shape[0]
+    _need(x, x_name, torch.bfloat16, (T, H, K))
+    _need(words, "words", torch.int32, (H, K // 8, N))
+    if scales.dim() != 3:
+        raise ValueError(f"scales has shape {tuple(scales.shape)}, expected ({H}, groups, {N})")
+    _need(scales, "scales", torch.bfloat16, (H, scales.shape[1], N))
+    _need(y, y_name, torch.bfloat16, (T, H, N))
+    _need(dev_err, "dev_err", torch.int32, (1,))
+    groups = scales.shape[1]
+    if groups < 1 or K % groups:
+        raise ValueError(f"scales has {groups} groups of {K} values")
+    _check(call(_ptr(x), _ptr(words), _ptr(scales), K // groups, _ptr(y), int(T), _ptr(dev_err), _stream(stream)))
+
+
+def mla_absorb_q_w4(q_c, words, scales, q_abs, dev_err, stream=None) -> None:
+    """mla_absorb_q over W_UK in 4 bits (mla_pack_w4); the group is 128 / scales.shape[1]."""
+    _w4(lib().mla_absorb_q_w4, q_c, "q_c", words, scales, q_abs, "q_abs", D_HC, D_C, dev_err, stream)
+
+
+def mla_up_v_w4(o_lat, words, scales, out, dev_err, stream=None) -> None:
+    """mla_up_v over W_UV in 4 bits (mla_pack_w4); the group is 512 / scales.shape[1]."""
+    _w4(lib().mla_up_v_w4, o_lat, "o_lat", words, scales, out, "out", D_C, D_HC, dev_err, stream)
+
+
 def mla_check(dev_err, stream=None) -> int:
     """Synchronise and return the device error word; raises on a non-zero word."""
     word = C.c_int32()

@@ -240,4 +240,19 @@ enum class HeadGemm { kAbsorbQ, kUpV };
 cudaError_t launch_head_gemm(HeadGemm kind, const CUtensorMap& a_map, const CUtensorMap& w_map,
                              const CUtensorMap& c_map, int32_t T, int32_t* err, cudaStream_t stream);
 
+// The same with 4-bit weights (w4_gemm.cu): words uint32 [128, K/8, N] of
+// eight codes along K, scales bf16 [128, K/group, N].
+struct W4Args {
+  const uint16_t* x;       // bf16 [T, 128, K]
+  const uint32_t* words;
+  const uint16_t* scales;
+  int32_t group;           // 32, 64 or 128
+  int32_t T;
+  uint16_t* y;             // bf16 [T, 128, N]
+  int32_t* dev_err;
+};
+cudaError_t launch_w4_gemm(HeadGemm kind, const W4Args& args, cudaStream_t stream);
+cudaError_t launch_w4_pack(const uint16_t* w, int K, int N, int group, uint32_t* words, uint16_t* scales,
+                           cudaStream_t stream);
+
 }  // namespace mla

@@ -1105,6 +1105,74 @@ mla_status mla_up_v(const void* o_lat, const void* w_uv, void* out, int32_t T, i
   return head_gemm(mla::HeadGemm::kUpV, o_lat, w_uv, out, T, dev_err, stream);
 }
 
+static mla_status w4_group_check(int32_t group) {
+  if (group != 32 && group != 64 && group != 128)
+    return fail(MLA_ERR_UNSUPPORTED, "group = %d: 32, 64 and 128 are supported", group);
+  return MLA_OK;
+}
+
+static mla_status w4_gemm(mla::HeadGemm kind, const void* x, const void* words, const void* scales, int32_t group,
+                          void* y, int32_t T, int32_t* dev_err, void* stream) {
+  if (T < 0) return fail(MLA_ERR_INVALID_ARG, "T = %d < 0", T);
+  mla_status s = w4_group_check(group);
+  if (s != MLA_OK) return s;
+  if (T == 0) return MLA_OK;
+  CHECK_PTR(x);
+  CHECK_PTR(words);
+  CHECK_PTR(scales);
+  CHECK_PTR(y);
+  CHECK_PTR(dev_err);
+  CHECK_ALIGN16(x);
+  CHECK_ALIGN16(words);
+  CHECK_ALIGN16(scales);
+  CHECK_ALIGN16(y);
+  if (!aligned(dev_err, 4)) return fail(MLA_ERR_MISALIGNED, "dev_err is not 4-byte aligned");
+  if (T > (1 << 18)) return fail(MLA_ERR_INVALID_ARG, "T = %d too large", T);
+  const bool absorb = kind == mla::HeadGemm::kAbsorbQ;
+  const uintptr_t row = (uintptr_t)MLA_NUM_HEADS * 2 * (uintptr_t)T;
+  const uintptr_t x0 = (uintptr_t)x, x_bytes = row * (absorb ? MLA_HEAD_DIM_C : MLA_LATENT_DIM);
+  const uintptr_t y0 = (uintptr_t)y, y_bytes = row * (absorb ? MLA_LATENT_DIM : MLA_HEAD_DIM_C);
+  if (x0 < y0 + y_bytes && y0 < x0 + x_bytes) return fail(MLA_ERR_INVALID_ARG, "the input and the output overlap");
+  mla::W4Args a = {};
+  a.x = (const uint16_t*)x;
+  a.words = (const uint32_t*)words;
+  a.scales = (const uint16_t*)scales;
+  a.group = group;
+  a.T = T;
+  a.y = (uint16_t*)y;
+  a.dev_err = dev_err;
+  cudaError_t e = mla::launch_w4_gemm(kind, a, (cudaStream_t)stream);
+  if (e != cudaSuccess) return cuda_fail(e, absorb ? "absorb_q_w4 launch" : "up_v_w4 launch");
+  return MLA_OK;
+}
+
+mla_status mla_absorb_q_w4(const void* q_c, const void* words, const void* scales, int32_t group, void* q_abs,
+                           int32_t T, int32_t* dev_err, void* stream) {
+  return w4_gemm(mla::HeadGemm::kAbsorbQ, q_c, words, scales, group, q_abs, T, dev_err, stream);
+}
+
+mla_status mla_up_v_w4(const void* o_lat, const void* words, const void* scales, int32_t group, void* out, int32_t T,
+                       int32_t* dev_err, void* stream) {
+  return w4_gemm(mla::HeadGemm::kUpV, o_lat, words, scales, group, out, T, dev_err, stream);
+}
+
+mla_status mla_pack_w4(const void* w, int32_t K, int32_t N, int32_t group, void* words, void* scales, void* stream) {
+  if (!((K == MLA_HEAD_DIM_C && N == MLA_LATENT_DIM) || (K == MLA_LATENT_DIM && N == MLA_HEAD_DIM_C)))
+    return fail(MLA_ERR_UNSUPPORTED, "K = %d, N = %d: 128 x 512 (W_UK) and 512 x 128 (W_UV) are supported", K, N);
+  mla_status s = w4_group_check(group);
+  if (s != MLA_OK) return s;
+  CHECK_PTR(w);
+  CHECK_PTR(words);
+  CHECK_PTR(scales);
+  CHECK_ALIGN16(w);
+  CHECK_ALIGN16(words);
+  CHECK_ALIGN16(scales);
+  cudaError_t e = mla::launch_w4_pack((const uint16_t*)w, K, N, group, (uint32_t*)words, (uint16_t*)scales,
+                                      (cudaStream_t)stream);
+  if (e != cudaSuccess) return cuda_fail(e, "pack_w4 launch");
+  return MLA_OK;
+}
+
 // ------------------------------------------------------------------ decode
 mla_status mla_decode_max_clusters(int32_t* out) {
   CHECK_PTR(out);

@@ -162,3 +162,38 @@ def test_chunk_window_workspace_and_refusals(api):
                dict(q=(1001,)), dict(cols=15), dict(ws=1000), dict(scale=-1.0), dict(out=0), dict(out=0x90008),
                dict(n=(2 ** 31 - 1,), window=2 ** 31 - 1)]:
         assert call(**kw) in (1, 2), kw
+
+
+def test_append_rope_fp8_refusals(api):
+    lib = _lib.lib()
+
+    def call(n=4, c=0x10000, q=0x20000, q_r=0x900000, slots=0x30000, table=0x40000, pos=0x50000, max_pos=9, pages=3,
+             scales=0x60000):
+        v = lambda a: C.c_void_p(a) if a else None  # noqa: E731
+        return lib.mla_kv_append_rope_fp8(v(c), v(0x70000), v(q), v(pos), v(table), max_pos, v(slots), n, v(0x80000),
+                                          v(scales), pages, v(q_r), v(0xA0000), None)
+
+    for kw in [dict(n=-1), dict(c=0), dict(q=0), dict(q_r=0), dict(q_r=0x20010), dict(max_pos=0), dict(pages=0)]:
+        assert call(**kw) == 1, kw
+    for kw in [dict(c=0x10008), dict(slots=0x30004), dict(pos=0x50002), dict(table=0x40004), dict(scales=0x60004),
+               dict(q=0x20002)]:
+        assert call(**kw) == 2, kw
+    assert call(n=0, c=0) == 0
+
+
+def test_w4_refusals(api):
+    lib = _lib.lib()
+
+    def call(f="mla_absorb_q_w4", x=0x10000, w=0x2000000, s=0x3000000, group=64, y=0x4000000, T=2, err=0x50000):
+        v = lambda a: C.c_void_p(a) if a else None  # noqa: E731
+        return getattr(lib, f)(v(x), v(w), v(s), group, v(y), T, v(err), None)
+
+    for f in ("mla_absorb_q_w4", "mla_up_v_w4"):
+        for kw, want in [(dict(T=-1), 1), (dict(T=2 ** 18 + 1), 1), (dict(group=16), 3), (dict(group=0), 3), (dict(x=0), 1),
+                         (dict(w=0), 1), (dict(s=0), 1), (dict(y=0), 1), (dict(err=0), 1), (dict(x=0x10008), 2),
+                         (dict(y=0x4000002), 2), (dict(err=0x50002), 2), (dict(y=0x10100), 1), (dict(T=0, x=0), 0)]:
+            assert call(f, **kw) == want, (f, kw)
+    p = C.c_void_p(0x10000)
+    assert lib.mla_pack_w4(p, 128, 128, 64, p, p, None) == 3 and lib.mla_pack_w4(p, 128, 512, 48, p, p, None) == 3
+    assert lib.mla_pack_w4(None, 128, 512, 64, p, p, None) == 1
+    assert lib.mla_pack_w4(p, 512, 128, 64, C.c_void_p(0x10004), p, None) == 2
