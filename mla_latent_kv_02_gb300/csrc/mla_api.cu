@@ -1141,7 +1141,17 @@ static mla_status w4_gemm(mla::HeadGemm kind, const void* x, const void* words, 
   a.T = T;
   a.y = (uint16_t*)y;
   a.dev_err = dev_err;
-  cudaError_t e = mla::launch_w4_gemm(kind, a, (cudaStream_t)stream);
+  CUtensorMap xm = {}, ym = {};
+  if (mla::w4_uses_maps(T)) {
+    const uint64_t K = absorb ? MLA_HEAD_DIM_C : MLA_LATENT_DIM, N = absorb ? MLA_LATENT_DIM : MLA_HEAD_DIM_C;
+    const uint64_t xd[3] = {K, MLA_NUM_HEADS, (uint64_t)T}, xs[2] = {K * 2, K * 2 * MLA_NUM_HEADS};
+    const uint64_t yd[3] = {N, MLA_NUM_HEADS, (uint64_t)T}, ys[2] = {N * 2, N * 2 * MLA_NUM_HEADS};
+    const uint32_t xbox[3] = {64, 1, 128}, ybox[3] = {32, 1, 128};
+    s = make_map(&xm, x, 3, xd, xs, xbox, "activations");
+    if (s == MLA_OK) s = make_map(&ym, y, 3, yd, ys, ybox, "outputs", CU_TENSOR_MAP_SWIZZLE_64B);
+    if (s != MLA_OK) return s;
+  }
+  cudaError_t e = mla::launch_w4_gemm(kind, a, xm, ym, (cudaStream_t)stream);
   if (e != cudaSuccess) return cuda_fail(e, absorb ? "absorb_q_w4 launch" : "up_v_w4 launch");
   return MLA_OK;
 }

@@ -10,6 +10,12 @@
 // * w4_rows_kernel: up to 8 tokens a block, fp32 on the CUDA cores.  A thread
 //   owns one column and 128 values of k (16 words, all requested at once); the
 //   K = 512 step joins four threads' sums through shared memory.
+// * w4_gemm_kernel: 128 tokens a tile on the tensor cores (tcgen05).  The codes
+//   become exact bf16 integers in shared memory once per (head, column block);
+//   the fp32 sums of all K / G groups of a column block fill the tensor memory
+//   (K / G x kNC = 512 columns), and the epilogue adds them up under their
+//   scales.  See the kernel.
+#include <cuda.h>
 #include <cuda_runtime.h>
 
 #include <cstdint>
@@ -25,6 +31,7 @@ using namespace mla::dev;
 constexpr int kSlice = 128;        // values of k per thread
 constexpr int kWordsPer = kSlice / 8;
 constexpr int kRowThreads = 256;
+constexpr int32_t kRowsMax = 8;    // more tokens go to the tensor cores
 
 // Eight codes to fp32, exactly: a nibble OR-ed into the mantissa of a power of
 // two whose last place it fills reads 2^(23 - 4i) + nibble; the codes are
@@ -116,8 +123,279 @@ cudaError_t run_rows(const W4Args& a, cudaStream_t stream) {
   return cudaGetLastError();
 }
 
+// ------------------------------------------------------------------ tensor cores
+// A CTA takes a contiguous range of the work units (head, column block, token
+// tile), token tiles fastest, so a column block's weights are unpacked once
+// and its token tiles stream past them.
+// Warps: 0 loads x by TMA (chunks of 64 k, a ring of kStages), 1 issues the
+// MMAs, 2-9 unpack the weights and run the epilogue: two warps per TMEM lane
+// quarter (thread = token row), taking alternate 32-column boxes.
+//   D[g][128 x kNC] = x[128 x G] . C_g[G x kNC]   (codes as bf16 integers)
+//   y = sum_g s_g D[g]                            (fp32, one bf16 rounding)
+// B is K-major: a word's eight codes are eight consecutive k of a column, one
+// 16-byte store into the 128-byte swizzled row of that column.
+// Every wait is bounded; the epilogue warps take each tile's decision to go on
+// together, so that no named barrier is left short.
+constexpr int kStages = 4;
+constexpr int kChunkBytes = 128 * 64 * 2;        // [128 tokens x 64 k] bf16
+constexpr int kBoxCols = 32;
+constexpr int kBoxBytes = 128 * kBoxCols * 2;    // one output box, 64-byte swizzled rows
+constexpr int kEpiWarps = 8;
+constexpr int kThreads = 32 * (2 + kEpiWarps);
+constexpr uint32_t kEpiBar = 1, kHalfBar = 2;    // named barriers: all epilogue warps; the four of a half
+
+template <int N, int K, int G>
+struct Cfg {
+  static constexpr int kGroups = K / G;
+  static constexpr int kNC = 512 / kGroups < N ? 512 / kGroups : N;   // columns of a block
+  static constexpr int kBlocks = N / kNC;
+  static constexpr int kChunks = K / 64;
+  static constexpr int kWChunkBytes = kNC * 128;                      // [kNC columns x 64 k] bf16
+  static constexpr int kWBytes = kChunks * kWChunkBytes;
+  static constexpr int kBoxes = kNC / kBoxCols;
+  static constexpr int kMmaN = kNC < 256 ? kNC : 256;
+  static constexpr uint32_t kIdesc = idesc_bf16_f32(128, kMmaN, false, false);
+  static constexpr int kOffA = kWBytes;
+  static constexpr int kOffOut = kOffA + kStages * kChunkBytes;
+  static constexpr int kOffScale = kOffOut + 2 * kBoxBytes;           // fp32 [kGroups][kNC]
+  static constexpr int kOffBar = kOffScale + 512 * 4;
+  static constexpr int kSmem = kOffBar + 128 + 1024;
+  static_assert(kGroups * kNC <= 512 && kNC % kBoxCols == 0 && kNC * kBlocks == N, "column blocks");
+  static_assert(kSmem <= 232448, "shared memory layout does not fit");
+};
+
+// Eight codes of a word (k ascending) to four bf16 pairs: 0x4300 | v is 128 + v.
+__device__ __forceinline__ uint4 codes_to_bf16(uint32_t w) {
+  w ^= 0x88888888u;
+  uint32_t r[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const uint32_t two = ((w >> (8 * j)) & 0xFFu) * 0x1001u;          // low nibble at 0, high nibble at 16
+    const uint32_t v = (two & 0x000F000Fu) | 0x43004300u;
+    const __nv_bfloat162 d = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&v), __floats2bfloat162_rn(136.f, 136.f));
+    r[j] = *reinterpret_cast<const uint32_t*>(&d);
+  }
+  return make_uint4(r[0], r[1], r[2], r[3]);
+}
+
+template <int N, int K, int G>
+__global__ void __launch_bounds__(kThreads, 1)
+    w4_gemm_kernel(const __grid_constant__ CUtensorMap x_map, const __grid_constant__ CUtensorMap y_map,
+                   const uint32_t* __restrict__ words, const uint16_t* __restrict__ scales, int32_t tiles, int32_t* err) {
+  using C = Cfg<N, K, G>;
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw = smem_u32(smem_raw);
+  const uint32_t base = (raw + 1023u) & ~1023u;
+  uint8_t* gbase = smem_raw + (base - raw);
+  const uint32_t bars = base + C::kOffBar;
+  const uint32_t full0 = bars, empty0 = bars + 8 * kStages, d_full = bars + 16 * kStages, d_free = d_full + 8,
+                 w_ready = d_full + 16, drain = d_full + 24;
+  volatile int32_t* abort_flag = reinterpret_cast<volatile int32_t*>(gbase + C::kOffBar + 112);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(gbase + C::kOffBar + 120);
+  float* sc = reinterpret_cast<float*>(gbase + C::kOffScale);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int64_t units = (int64_t)MLA_NUM_HEADS * C::kBlocks * tiles;
+  const int64_t u0 = units * blockIdx.x / gridDim.x, u1 = units * (blockIdx.x + 1) / gridDim.x;
+
+  if (threadIdx.x == 0) {
+    *abort_flag = 0;
+    for (int i = 0; i < kStages; ++i) {
+      mbar_init(full0 + 8 * i, 1);
+      mbar_init(empty0 + 8 * i, 1);
+    }
+    mbar_init(d_full, 1);
+    mbar_init(d_free, kEpiWarps);
+    mbar_init(w_ready, kEpiWarps);
+    mbar_init(drain, 1);
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    __syncwarp();
+    tmem_alloc(smem_u32(tmem_slot), 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+
+  if (warp == 0) {
+    // ---------------------------------------------------------------- x loads
+    if (lane == 0) {
+      prefetch_tmap(&x_map);
+      prefetch_tmap(&y_map);
+      uint32_t n = 0;
+      bool ok = true;
+      for (int64_t u = u0; ok && u < u1; ++u) {
+        const int h = (int)(u / tiles / C::kBlocks), m0 = (int)(u % tiles) * 128;
+        for (int kc = 0; kc < C::kChunks; ++kc, ++n) {
+          const uint32_t st = n % kStages, use = n / kStages;
+          if (use > 0 && !wait_phase(empty0 + 8 * st, (use - 1) & 1u, err, abort_flag)) {
+            ok = false;
+            break;
+          }
+          mbar_arrive_expect_tx(full0 + 8 * st, (uint32_t)kChunkBytes);
+          tma_load_3d(base + C::kOffA + st * kChunkBytes, &x_map, kc * 64, h, m0, full0 + 8 * st);
+        }
+      }
+      for (uint32_t k = n > (uint32_t)kStages ? n - kStages : 0u; k < n; ++k)
+        wait_phase_drain(full0 + 8 * (k % kStages), (k / kStages) & 1u);
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    // ---------------------------------------------------------------- MMA issue
+    if (lane == 0) {
+      uint32_t n = 0, i = 0, blocks = 0;
+      int64_t hb_now = -1;
+      bool ok = true;
+      for (int64_t u = u0; ok && u < u1; ++u, ++i) {
+        const int64_t hb = u / tiles;
+        if (hb != hb_now) {
+          hb_now = hb;
+          ok = wait_phase(w_ready, blocks++ & 1u, err, abort_flag);
+        }
+        if (ok && i > 0) ok = wait_phase(d_free, (i - 1) & 1u, err, abort_flag);
+        for (int kc = 0; ok && kc < C::kChunks; ++kc, ++n) {
+          const uint32_t st = n % kStages;
+          if (!wait_phase(full0 + 8 * st, (n / kStages) & 1u, err, abort_flag)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t sa = base + C::kOffA + st * kChunkBytes, sb = base + kc * C::kWChunkBytes;
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk) {
+            const int k = kc * 64 + kk * 16;
+#pragma unroll
+            for (int nh = 0; nh < C::kNC / C::kMmaN; ++nh)
+              mma_ss(tmem + (k / G) * C::kNC + nh * C::kMmaN, sdesc_sw128(sa + kk * 32, 16, 1024),
+                     sdesc_sw128(sb + nh * C::kMmaN * 128 + kk * 32, 16, 1024), C::kIdesc, k % G ? 1u : 0u);
+          }
+          tc_commit(empty0 + 8 * st);
+        }
+        if (ok) tc_commit(d_full);
+      }
+      tc_commit(drain);  // every MMA has finished before TMEM is released
+      wait_phase_drain(drain, 0);
+    }
+    __syncwarp();
+  } else {
+    // ---------------------------------------------------------------- weights and epilogue
+    const int tid = threadIdx.x - 64;                // 0 .. 255
+    const int q4 = warp & 3, half = (warp - 2) >> 2;
+    const uint32_t r = (uint32_t)(q4 * 32 + lane);   // token row = TMEM lane
+    const uint32_t tl = tmem + ((uint32_t)(q4 * 32) << 16);
+    const uint32_t out = base + C::kOffOut + half * kBoxBytes;
+    const bool leader = (warp - 2) % 4 == 0 && lane == 0;
+    int64_t hb_now = -1;
+    uint32_t i = 0;
+    for (int64_t u = u0; u < u1; ++u, ++i) {
+      const int64_t hb = u / tiles;
+      const int h = (int)(hb / C::kBlocks), n0 = (int)(hb % C::kBlocks) * C::kNC, m0 = (int)(u % tiles) * 128;
+      if (hb != hb_now) {
+        // Every MMA of the block before has completed (its last tile's d_full)
+        // and every warp has read that tile's scales: the barrier below.
+        hb_now = hb;
+        constexpr int kPer = C::kNC * (K / 8) / 256, kBatch = kPer < 16 ? kPer : 16;
+        const uint32_t* wp = words + (int64_t)h * (K / 8) * N + n0;
+        named_bar_sync(kEpiBar, 32 * kEpiWarps);
+        for (int s = tid; s < C::kGroups * C::kNC; s += 256)
+          sc[s] = __uint_as_float((uint32_t)__ldg(scales + ((int64_t)h * C::kGroups + s / C::kNC) * N + n0 + s % C::kNC) << 16);
+#pragma unroll 1
+        for (int b = 0; b < kPer; b += kBatch) {
+          uint32_t w[kBatch];
+#pragma unroll
+          for (int j = 0; j < kBatch; ++j) {
+            const int at = (b + j) * 256 + tid;
+            w[j] = __ldg(wp + (int64_t)(at / C::kNC) * N + at % C::kNC);
+          }
+#pragma unroll
+          for (int j = 0; j < kBatch; ++j) {
+            const int at = (b + j) * 256 + tid, n = at % C::kNC, kb = at / C::kNC;
+            const uint4 v = codes_to_bf16(w[j]);
+            st_shared_v4(base + (kb / 8) * C::kWChunkBytes + n * 128 + (((kb & 7) ^ (n & 7)) << 4), v.x, v.y, v.z, v.w);
+          }
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(w_ready);
+      }
+      const bool w = wait_phase(d_full, i & 1u, err, abort_flag);
+      if (!named_bar_and(kEpiBar, 32 * kEpiWarps, w)) break;
+      tc_fence_after();
+#pragma unroll 1
+      for (int b = half; b < C::kBoxes; b += 2) {
+        float acc[kBoxCols];
+#pragma unroll
+        for (int j = 0; j < kBoxCols; ++j) acc[j] = 0.f;
+#pragma unroll 1
+        for (int g = 0; g < C::kGroups; ++g) {
+          uint32_t d[32];
+          tmem_ld32_sync(tl + g * C::kNC + b * kBoxCols, d);
+          const float4* s4 = reinterpret_cast<const float4*>(sc + g * C::kNC + b * kBoxCols);
+#pragma unroll
+          for (int j = 0; j < kBoxCols / 4; ++j) {
+            const float4 s = s4[j];
+            acc[4 * j] = fmaf(s.x, __uint_as_float(d[4 * j]), acc[4 * j]);
+            acc[4 * j + 1] = fmaf(s.y, __uint_as_float(d[4 * j + 1]), acc[4 * j + 1]);
+            acc[4 * j + 2] = fmaf(s.z, __uint_as_float(d[4 * j + 2]), acc[4 * j + 2]);
+            acc[4 * j + 3] = fmaf(s.w, __uint_as_float(d[4 * j + 3]), acc[4 * j + 3]);
+          }
+        }
+        if (b + 2 >= C::kBoxes) {  // this half's last read of the tile's sums
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(d_free);
+        }
+        if (leader) bulk_wait_all_read();  // the box's previous store has read it
+        named_bar_sync(kHalfBar + half, 128);
+        // 64-byte swizzle: row r at 64 r, 16-byte piece c at c ^ ((r / 2) & 3)
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+          st_shared_v4(out + r * 64u + (((uint32_t)c ^ ((r >> 1) & 3u)) << 4), pack_bf16x2(acc[8 * c], acc[8 * c + 1]),
+                       pack_bf16x2(acc[8 * c + 2], acc[8 * c + 3]), pack_bf16x2(acc[8 * c + 4], acc[8 * c + 5]),
+                       pack_bf16x2(acc[8 * c + 6], acc[8 * c + 7]));
+        fence_proxy_async_smem();
+        named_bar_sync(kHalfBar + half, 128);
+        if (leader) {
+          tma_store_3d(&y_map, out, n0 + b * kBoxCols, h, m0);
+          bulk_commit_group();
+        }
+      }
+      if (half >= C::kBoxes && lane == 0) mbar_arrive(d_free);  // a half without boxes
+    }
+    if (leader) bulk_wait_all_read();  // the staging boxes are released at exit
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    __syncwarp();
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+template <int N, int K, int G>
+cudaError_t run_gemm(const W4Args& a, const CUtensorMap& x_map, const CUtensorMap& y_map, cudaStream_t stream) {
+  using C = Cfg<N, K, G>;
+  auto* kern = w4_gemm_kernel<N, K, G>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+  if (e != cudaSuccess) return e;
+  const int32_t tiles = (a.T + 127) / 128;
+  const int64_t units = (int64_t)MLA_NUM_HEADS * C::kBlocks * tiles;
+  kern<<<(unsigned)(units < 152 ? units : 152), kThreads, C::kSmem, stream>>>(x_map, y_map, a.words, a.scales, tiles,
+                                                                              a.dev_err);
+  return cudaGetLastError();
+}
+
 template <int N, int K>
-cudaError_t run(const W4Args& a, cudaStream_t stream) {
+cudaError_t run(const W4Args& a, const CUtensorMap& x_map, const CUtensorMap& y_map, cudaStream_t stream) {
+  if (a.T > kRowsMax) {
+    if (a.group == 128) return run_gemm<N, K, 128>(a, x_map, y_map, stream);
+    if (a.group == 64) return run_gemm<N, K, 64>(a, x_map, y_map, stream);
+    return run_gemm<N, K, 32>(a, x_map, y_map, stream);
+  }
   if (a.T == 1) return run_rows<N, K, 1>(a, stream);
   if (a.T == 2) return run_rows<N, K, 2>(a, stream);
   if (a.T <= 4) return run_rows<N, K, 4>(a, stream);
@@ -154,9 +432,13 @@ __global__ void __launch_bounds__(256)
 
 }  // namespace w4
 
-cudaError_t launch_w4_gemm(HeadGemm kind, const W4Args& args, cudaStream_t stream) {
+bool w4_uses_maps(int32_t T) { return T > w4::kRowsMax; }
+
+cudaError_t launch_w4_gemm(HeadGemm kind, const W4Args& args, const CUtensorMap& x_map, const CUtensorMap& y_map,
+                           cudaStream_t stream) {
   if (args.T <= 0) return cudaSuccess;
-  return kind == HeadGemm::kAbsorbQ ? w4::run<512, 128>(args, stream) : w4::run<128, 512>(args, stream);
+  return kind == HeadGemm::kAbsorbQ ? w4::run<512, 128>(args, x_map, y_map, stream)
+                                    : w4::run<128, 512>(args, x_map, y_map, stream);
 }
 
 cudaError_t launch_w4_pack(const uint16_t* w, int K, int N, int group, uint32_t* words, uint16_t* scales,
