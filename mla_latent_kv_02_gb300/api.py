@@ -59,6 +59,26 @@ def _need(t: torch.Tensor, name: str, dtype, shape=None, cuda: bool = True):
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
 
 
+_Tensor = torch.Tensor
+_raw_stream = torch._C._cuda_getCurrentRawStream
+
+
+def _in(t, name: str, dtype, shape, dev: int) -> int:
+    """A device argument's address: what _need checks, and that the tensor lives
+    on the current device `dev` (the one the call launches on)."""
+    if not (type(t) is _Tensor and t.dtype is dtype and t.shape == shape and t.get_device() == dev
+            and t.is_contiguous()):
+        _need(t, name, dtype, shape)
+        if t.get_device() != dev:
+            raise ValueError(f"{name} is on {t.device}, the current device is cuda:{dev}")
+    return t.data_ptr()
+
+
+def _on(stream, dev: int) -> int:
+    """The raw handle of `stream`, or of the current stream of device `dev`."""
+    return _raw_stream(dev) if stream is None else stream.cuda_stream
+
+
 # ------------------------------------------------------------------ host-only calls
 def mla_version() -> int:
     return int(lib().mla_version())
@@ -157,24 +177,17 @@ def mla_kv_append_rope_fp8(c_kv_new, k_pe_new, positions, table, slots, rows, sc
                            stream=None) -> None:
     """Append to the FP8 cache with the RoPE key rotated on the way in; with
     q_pe (bf16 [n, 128, 64], the same tokens' queries) also rotate them into q_r."""
-    n = c_kv_new.shape[0]
-    _need(c_kv_new, "c_kv_new", torch.bfloat16, (n, D_C))
-    _need(k_pe_new, "k_pe_new", torch.bfloat16, (n, D_R))
-    _need(positions, "positions", torch.int32, (n,))
-    _need(table, "table", torch.float32)
-    _need(slots, "slots", torch.int64, (n,))
-    _need(rows, "rows", torch.uint8, (rows.shape[0], PAGE, FP8_ROW_BYTES))
-    _need(scales, "scales", torch.float32, (rows.shape[0], PAGE))
-    _need(dev_err, "dev_err", torch.int32, (1,))
-    if table.dim() != 3 or tuple(table.shape[1:]) != (D_R // 2, 2):
-        raise ValueError(f"table has shape {tuple(table.shape)}, expected (max_pos, {D_R // 2}, 2)")
-    if q_pe is not None:
-        _need(q_pe, "q_pe", torch.bfloat16, (n, H, D_R))
-    if q_r is not None:
-        _need(q_r, "q_r", torch.bfloat16, (n, H, D_R))
-    _check(lib().mla_kv_append_rope_fp8(_ptr(c_kv_new), _ptr(k_pe_new), _ptr(q_pe), _ptr(positions), _ptr(table),
-                                        table.shape[0], _ptr(slots), int(n), _ptr(rows), _ptr(scales), rows.shape[0],
-                                        _ptr(q_r), _ptr(dev_err), _stream(stream)))
+    dev = torch.cuda.current_device()
+    n, pages, max_pos = c_kv_new.shape[0], rows.shape[0], table.shape[0]
+    _check(lib().mla_kv_append_rope_fp8(
+        _in(c_kv_new, "c_kv_new", torch.bfloat16, (n, D_C), dev), _in(k_pe_new, "k_pe_new", torch.bfloat16, (n, D_R), dev),
+        None if q_pe is None else _in(q_pe, "q_pe", torch.bfloat16, (n, H, D_R), dev),
+        _in(positions, "positions", torch.int32, (n,), dev),
+        _in(table, "table", torch.float32, (max_pos, D_R // 2, 2), dev), max_pos,
+        _in(slots, "slots", torch.int64, (n,), dev), n, _in(rows, "rows", torch.uint8, (pages, PAGE, FP8_ROW_BYTES), dev),
+        _in(scales, "scales", torch.float32, (pages, PAGE), dev), pages,
+        None if q_r is None else _in(q_r, "q_r", torch.bfloat16, (n, H, D_R), dev),
+        _in(dev_err, "dev_err", torch.int32, (1,), dev), _on(stream, dev)))
 
 
 def mla_gather_paged_fp8(rows, scales, block_table, b: int, n_tokens: int, out, dev_err, stream=None) -> None:
@@ -597,45 +610,41 @@ def mla_window_plan(seq_lens: Sequence[int], q_lens: Sequence[int], window: int,
 def mla_decode_window(q_abs, q_r, kv_cache, block_table, plan: WindowPlan, o_lat, dev_err, lse=None,
                       scale: float = 1.0 / (192 ** 0.5), stream=None) -> None:
     """mla_decode_paged with the plan's sliding window and sinks."""
-    T = q_abs.shape[0]
-    _need(q_abs, "q_abs", torch.bfloat16, (T, H, D_C))
-    _need(q_r, "q_r", torch.bfloat16, (T, H, D_R))
-    _need(kv_cache, "kv_cache", torch.bfloat16, (kv_cache.shape[0], PAGE, D_QK))
-    _need_window(plan, T, block_table, o_lat, lse, dev_err)
-    _check(lib().mla_decode_window(_ptr(q_abs), _ptr(q_r), _ptr(kv_cache), kv_cache.shape[0], _ptr(block_table),
-                                   block_table.shape[1], _ptr(plan.plan), C.byref(plan.info), float(scale),
-                                   _ptr(plan.workspace), plan.workspace.numel(), _ptr(o_lat), _ptr(lse),
-                                   _ptr(dev_err), _stream(stream)))
+    dev = torch.cuda.current_device()
+    pages = kv_cache.shape[0]
+    cache = (_in(kv_cache, "kv_cache", torch.bfloat16, (pages, PAGE, D_QK), dev),)
+    _decode_window(lib().mla_decode_window, cache, pages, q_abs, q_r, block_table, plan, o_lat, dev_err, lse, scale,
+                   stream, dev)
 
 
 def mla_decode_window_fp8(q_abs, q_r, rows, scales, block_table, plan: WindowPlan, o_lat, dev_err, lse=None,
                           scale: float = 1.0 / (192 ** 0.5), stream=None) -> None:
     """mla_decode_paged_fp8 with the plan's sliding window and sinks."""
-    T = q_abs.shape[0]
-    _need(q_abs, "q_abs", torch.bfloat16, (T, H, D_C))
-    _need(q_r, "q_r", torch.bfloat16, (T, H, D_R))
-    _need(rows, "rows", torch.uint8, (rows.shape[0], PAGE, FP8_ROW_BYTES))
-    _need(scales, "scales", torch.float32, (rows.shape[0], PAGE))
-    _need_window(plan, T, block_table, o_lat, lse, dev_err)
-    _check(lib().mla_decode_window_fp8(_ptr(q_abs), _ptr(q_r), _ptr(rows), _ptr(scales), rows.shape[0],
-                                       _ptr(block_table), block_table.shape[1], _ptr(plan.plan), C.byref(plan.info),
-                                       float(scale), _ptr(plan.workspace), plan.workspace.numel(), _ptr(o_lat),
-                                       _ptr(lse), _ptr(dev_err), _stream(stream)))
+    dev = torch.cuda.current_device()
+    pages = rows.shape[0]
+    cache = (_in(rows, "rows", torch.uint8, (pages, PAGE, FP8_ROW_BYTES), dev),
+             _in(scales, "scales", torch.float32, (pages, PAGE), dev))
+    _decode_window(lib().mla_decode_window_fp8, cache, pages, q_abs, q_r, block_table, plan, o_lat, dev_err, lse, scale,
+                   stream, dev)
 
 
-def _need_window(plan, T, block_table, o_lat, lse, dev_err) -> None:
+def _decode_window(call, cache, pages, q_abs, q_r, block_table, plan, o_lat, dev_err, lse, scale, stream, dev) -> None:
     if not isinstance(plan, WindowPlan):
         raise TypeError("plan must come from mla_window_plan")
-    info = plan.info.plan
-    if info.T != T:
-        raise ValueError(f"plan has {info.T} rows, q_abs has {T}")
-    _need(block_table, "block_table", torch.int32)
-    if block_table.dim() != 2 or block_table.shape[0] < info.B:
-        raise ValueError(f"block_table has shape {tuple(block_table.shape)}, the plan has {info.B} sequences")
-    _need(o_lat, "o_lat", torch.bfloat16, (T, H, D_C))
-    _need(dev_err, "dev_err", torch.int32, (1,))
-    if lse is not None:
-        _need(lse, "lse", torch.float32, (T, H))
+    T, sums = q_abs.shape[0], plan.info.plan
+    if sums.T != T:
+        raise ValueError(f"plan has {sums.T} rows, q_abs has {T}")
+    if block_table.dim() != 2 or block_table.shape[0] < sums.B:
+        raise ValueError(f"block_table has shape {tuple(block_table.shape)}, the plan has {sums.B} sequences")
+    cols = block_table.shape[1]
+    ws_bytes = plan.workspace.numel()
+    _check(call(_in(q_abs, "q_abs", torch.bfloat16, (T, H, D_C), dev), _in(q_r, "q_r", torch.bfloat16, (T, H, D_R), dev),
+                *cache, pages, _in(block_table, "block_table", torch.int32, (block_table.shape[0], cols), dev), cols,
+                _in(plan.plan, "plan.plan", torch.int32, (plan.plan.numel(),), dev), plan.info, scale,
+                _in(plan.workspace, "plan.workspace", torch.uint8, (ws_bytes,), dev), ws_bytes,
+                _in(o_lat, "o_lat", torch.bfloat16, (T, H, D_C), dev),
+                None if lse is None else _in(lse, "lse", torch.float32, (T, H), dev),
+                _in(dev_err, "dev_err", torch.int32, (1,), dev), _on(stream, dev)))
 
 
 def _host_i32(*lists):
@@ -655,27 +664,25 @@ def mla_prefill_window_workspace_size(q_lens: Sequence[int], n_tokens: Sequence[
     return int(out.value)
 
 
-def _prefill_window(call, cache, q_c, q_r, block_table, seq_ids, q_starts, q_lens, n_tokens, window, sinks, w_uk, w_uv,
-                    workspace, out, dev_err, scale, stream) -> None:
+def _prefill_window(call, cache, pages, q_c, q_r, block_table, seq_ids, q_starts, q_lens, n_tokens, window, sinks,
+                    w_uk, w_uv, workspace, out, dev_err, scale, stream, dev) -> None:
     rows = q_c.shape[0]
-    _need(q_c, "q_c", torch.bfloat16, (rows, H, D_HC))
-    _need(q_r, "q_r", torch.bfloat16, (rows, H, D_R))
-    _need(block_table, "block_table", torch.int32)
     if block_table.dim() != 2:
         raise ValueError("block_table must be [sequences, pages]")
-    _need(w_uk, "w_uk", torch.bfloat16, (H, D_HC, D_C))
-    _need(w_uv, "w_uv", torch.bfloat16, (H, D_C, D_HC))
-    _need(workspace, "workspace", torch.uint8)
-    _need(out, "out", torch.bfloat16, (rows, H, D_HC))
-    _need(dev_err, "dev_err", torch.int32, (1,))
+    batch, cols = block_table.shape
     arrs = _host_i32(seq_ids, q_starts, q_lens, n_tokens)
-    if any(int(s0) + int(m) > rows for s0, m in zip(arrs[1], arrs[2])):
+    if arrs[0].size and int((arrs[1].astype(np.int64) + arrs[2]).max()) > rows:
         raise ValueError("a chunk's rows run past q_c")
     P32 = C.POINTER(C.c_int32)
-    _check(call(_ptr(q_c), _ptr(q_r), *[a.ctypes.data_as(P32) for a in arrs], int(arrs[0].size), int(window),
-                int(sinks), *[_ptr(t) for t in cache], cache[0].shape[0], _ptr(block_table), block_table.shape[0],
-                block_table.shape[1], _ptr(w_uk), _ptr(w_uv), float(scale), _ptr(workspace), workspace.numel(),
-                _ptr(out), _ptr(dev_err), _stream(stream)))
+    ws_bytes = workspace.numel()
+    _check(call(_in(q_c, "q_c", torch.bfloat16, (rows, H, D_HC), dev), _in(q_r, "q_r", torch.bfloat16, (rows, H, D_R), dev),
+                *[a.ctypes.data_as(P32) for a in arrs], arrs[0].size, window, sinks, *cache, pages,
+                _in(block_table, "block_table", torch.int32, (batch, cols), dev), batch, cols,
+                _in(w_uk, "w_uk", torch.bfloat16, (H, D_HC, D_C), dev),
+                _in(w_uv, "w_uv", torch.bfloat16, (H, D_C, D_HC), dev), scale,
+                _in(workspace, "workspace", torch.uint8, (ws_bytes,), dev), ws_bytes,
+                _in(out, "out", torch.bfloat16, (rows, H, D_HC), dev), _in(dev_err, "dev_err", torch.int32, (1,), dev),
+                _on(stream, dev)))
 
 
 def mla_prefill_window_batch(q_c, q_r, kv_cache, block_table, seq_ids, q_starts, q_lens, n_tokens, window: int,
@@ -683,19 +690,23 @@ def mla_prefill_window_batch(q_c, q_r, kv_cache, block_table, seq_ids, q_starts,
                              stream=None) -> None:
     """mla_prefill_decompress_batch with a sliding window and sinks: only the
     tokens that a chunk's rows see are gathered and expanded."""
-    _need(kv_cache, "kv_cache", torch.bfloat16, (kv_cache.shape[0], PAGE, D_QK))
-    _prefill_window(lib().mla_prefill_window_batch, (kv_cache,), q_c, q_r, block_table, seq_ids, q_starts, q_lens,
-                    n_tokens, window, sinks, w_uk, w_uv, workspace, out, dev_err, scale, stream)
+    dev = torch.cuda.current_device()
+    pages = kv_cache.shape[0]
+    cache = (_in(kv_cache, "kv_cache", torch.bfloat16, (pages, PAGE, D_QK), dev),)
+    _prefill_window(lib().mla_prefill_window_batch, cache, pages, q_c, q_r, block_table, seq_ids, q_starts, q_lens,
+                    n_tokens, window, sinks, w_uk, w_uv, workspace, out, dev_err, scale, stream, dev)
 
 
 def mla_prefill_window_batch_fp8(q_c, q_r, rows, scales, block_table, seq_ids, q_starts, q_lens, n_tokens, window: int,
                                  sinks: int, w_uk, w_uv, workspace, out, dev_err, scale: float = 1.0 / (192 ** 0.5),
                                  stream=None) -> None:
     """mla_prefill_window_batch over the FP8 cache."""
-    _need(rows, "rows", torch.uint8, (rows.shape[0], PAGE, FP8_ROW_BYTES))
-    _need(scales, "scales", torch.float32, (rows.shape[0], PAGE))
-    _prefill_window(lib().mla_prefill_window_batch_fp8, (rows, scales), q_c, q_r, block_table, seq_ids, q_starts,
-                    q_lens, n_tokens, window, sinks, w_uk, w_uv, workspace, out, dev_err, scale, stream)
+    dev = torch.cuda.current_device()
+    pages = rows.shape[0]
+    cache = (_in(rows, "rows", torch.uint8, (pages, PAGE, FP8_ROW_BYTES), dev),
+             _in(scales, "scales", torch.float32, (pages, PAGE), dev))
+    _prefill_window(lib().mla_prefill_window_batch_fp8, cache, pages, q_c, q_r, block_table, seq_ids, q_starts, q_lens,
+                    n_tokens, window, sinks, w_uk, w_uv, workspace, out, dev_err, scale, stream, dev)
 
 
 # ------------------------------------------------------------------ 4-bit weights
@@ -716,18 +727,15 @@ def mla_pack_w4(w, group: int, stream=None):
 
 
 def _w4(call, x, x_name, words, scales, y, y_name, K, N, dev_err, stream) -> None:
+    dev = torch.cuda.current_device()
     T = x.shape[0]
-    _need(x, x_name, torch.bfloat16, (T, H, K))
-    _need(words, "words", torch.int32, (H, K // 8, N))
-    if scales.dim() != 3:
-        raise ValueError(f"scales has shape {tuple(scales.shape)}, expected ({H}, groups, {N})")
-    _need(scales, "scales", torch.bfloat16, (H, scales.shape[1], N))
-    _need(y, y_name, torch.bfloat16, (T, H, N))
-    _need(dev_err, "dev_err", torch.int32, (1,))
+    if scales.dim() != 3 or scales.shape[1] < 1 or K % scales.shape[1]:
+        raise ValueError(f"scales has shape {tuple(scales.shape)}, expected ({H}, groups of {K} values, {N})")
     groups = scales.shape[1]
-    if groups < 1 or K % groups:
-        raise ValueError(f"scales has {groups} groups of {K} values")
-    _check(call(_ptr(x), _ptr(words), _ptr(scales), K // groups, _ptr(y), int(T), _ptr(dev_err), _stream(stream)))
+    _check(call(_in(x, x_name, torch.bfloat16, (T, H, K), dev), _in(words, "words", torch.int32, (H, K // 8, N), dev),
+                _in(scales, "scales", torch.bfloat16, (H, groups, N), dev), K // groups,
+                _in(y, y_name, torch.bfloat16, (T, H, N), dev), T, _in(dev_err, "dev_err", torch.int32, (1,), dev),
+                _on(stream, dev)))
 
 
 def mla_absorb_q_w4(q_c, words, scales, q_abs, dev_err, stream=None) -> None:
