@@ -78,6 +78,7 @@ constexpr int kXWarp = 32 * kXRow;                        // one warp's 32 rows 
 constexpr int kXBufs = 4;                                 // exchange ring depth
 constexpr int kXLead = kXBufs - 2;                        // staging buffer offset
 static_assert(kXLead >= 1 && kXLead <= kXBufs - 2, "the exchange ring needs two tiles between staging and reuse");
+constexpr int kQWarp = 2048;                              // a warp's query rows on their way to TMEM, 64 bytes of each of 32 rows
 constexpr int kOnesBytes = 16 * kChunk * 2;               // [16 x 64] bf16 ones for the row sums
 
 // FP8 stage (one page, this CTA's half): the 32 KB latent area, whose first
@@ -94,8 +95,8 @@ constexpr uint32_t kConvBarrier = 1;                      // named barrier of th
 static_assert(kF8ScaleOff + kPage * 4 <= kF8StageBytes, "FP8 stage too small");
 
 // Shared memory: a small region (barriers, row-max slots, flags) at the
-// start, then the 1024-byte aligned region (page ring, FP8 staging ring,
-// exchange ring, the ones tile).
+// start, then the 1024-byte aligned region (page ring, exchange ring, the ones
+// tile, the query staging).
 constexpr int kNumBars = 32;
 constexpr int kSmallBar = 0;
 constexpr int kSmallPair = kSmallBar + 8 * kNumBars;      // uint2 [4][128]: {reference max bits, tile}
@@ -139,8 +140,11 @@ struct Layout : Cfg<kF8> {
   static constexpr int kOffKV = 0;
   static constexpr int kOffX = C::kStages * C::kStageBytes;
   static constexpr int kOffOnes = kOffX + kXBufs * kXBytes;
-  static constexpr int kAlignedBytes = kOffOnes + kOnesBytes;
-  static constexpr int kSmemBytes = kSmallBytes + kAlignedBytes + 1024;
+  static constexpr int kOffQ = kOffOnes + kOnesBytes;
+  static constexpr int kAlignedBytes = kOffQ + 4 * kQWarp;
+  // The aligned region starts at the first 1024-byte boundary past the small
+  // one; the dynamic window itself is aligned (layout_fits checks).
+  static constexpr int kSmemBytes = (kSmallBytes + 1023) / 1024 * 1024 + kAlignedBytes;
   static_assert(kSmemBytes <= 232448, "shared memory layout does not fit");
   enum : int {
     B_KV_FULL = 0,
@@ -238,6 +242,11 @@ struct TileCursor {
   }
 };
 
+template <bool kValue>
+struct Flag {
+  static constexpr bool value = kValue;
+};
+
 __device__ __forceinline__ __half2 as_h2(uint32_t u) { return *reinterpret_cast<const __half2*>(&u); }
 __device__ __forceinline__ uint32_t as_u32(__half2 h) { return *reinterpret_cast<const uint32_t*>(&h); }
 
@@ -256,7 +265,7 @@ __device__ __forceinline__ void decode_body(const CUtensorMap& kv_map, const CUt
   using L = Layout<kF8>;
   constexpr int kStages = L::kStages, kStageBytes = L::kStageBytes, kThreads = L::kThreads;
   constexpr int kPvWarp = L::kPvWarp, kSoftWarp0 = L::kSoftWarp0, kConvWarp0 = L::kConvWarp0;
-  constexpr int kOffKV = L::kOffKV, kOffX = L::kOffX, kOffOnes = L::kOffOnes;
+  constexpr int kOffKV = L::kOffKV, kOffX = L::kOffX, kOffOnes = L::kOffOnes, kOffQ = L::kOffQ;
   constexpr int kAlignedBytes = L::kAlignedBytes, kSmemBytes = L::kSmemBytes;
   constexpr int B_KV_FULL = L::B_KV_FULL, B_KV_EMPTY = L::B_KV_EMPTY, B_S_FULL0 = L::B_S_FULL0,
                 B_S_FULL1 = L::B_S_FULL1, B_S_FREE = L::B_S_FREE, B_P_FULL = L::B_P_FULL,
@@ -362,7 +371,10 @@ __device__ __forceinline__ void decode_body(const CUtensorMap& kv_map, const CUt
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  cluster_sync();  // the peer's barriers exist before any copy or arrive reaches them
+  // The peer's barriers must exist before a copy reaches them: every thread
+  // arrives here, the softmax warps wait before their first push and the
+  // others before the exit barrier, so that the loads start at once.
+  cluster_arrive();
   const uint32_t tmem = *tmem_slot;
 
   const int s_begin = seg_range[0];
@@ -666,53 +678,55 @@ __device__ __forceinline__ void decode_body(const CUtensorMap& kv_map, const CUt
     const float rescale_thr = 8.f / c2;  // lazy-rescale threshold: 8 in log2 units
     const __half2 c2h = __float2half2_rn(c2);
     __syncwarp();
+    bool peer_ready = false;  // this warp has waited for the cluster barrier of the set-up
 
-    // Q_r of a segment's row into TMEM, this thread's row (144 columns), in
-    // two rounds of loads so that at most 20 16-byte values are live.
+    // Q_r of a segment's row into TMEM, this warp's 32 head rows (144 columns
+    // each), 64 bytes of every row a round.  A thread needs its own row, but
+    // the rows lie 1 KB apart: the warp loads four lanes to a row, so that a
+    // load covers 8 lines instead of 32, and the pieces change hands through
+    // shared memory.  Nine rounds (eight latent, one RoPE) in three batches, a
+    // batch's loads all in flight.
+    const uint32_t qbuf = base + kOffQ + (uint32_t)(q4 * kQWarp);
     auto load_q = [&](int s) {
-      const int row = a.segs[8 * s];
-      const uint4* lat = reinterpret_cast<const uint4*>(a.q_abs + ((size_t)row * kH + h) * kDC + rank * 256);
-      const uint4* rp = reinterpret_cast<const uint4*>(a.q_r + ((size_t)row * kH + h) * kDR + rank * kRopeHalf);
+      const size_t row0 = (size_t)a.segs[8 * s] * kH + q4 * 32 + (lane >> 2);
+      const uint4* lat = reinterpret_cast<const uint4*>(a.q_abs + row0 * kDC + rank * 256) + (lane & 3);
+      const uint4* rp = reinterpret_cast<const uint4*>(a.q_r + row0 * kDR + rank * kRopeHalf) + (lane & 3);
+      auto pass = [&](const uint4 (&v)[4], uint32_t col) {
 #pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        uint4 v[20];
+        for (int i = 0; i < 4; ++i) {
+          const uint32_t r = (uint32_t)(8 * i + (lane >> 2));
+          st_shared_v4(qbuf + r * 64u + ((((uint32_t)lane & 3u) ^ ((r >> 1) & 3u)) << 4), v[i].x, v[i].y, v[i].z, v[i].w);
+        }
+        __syncwarp();
+        uint32_t r[16];
 #pragma unroll
-        for (int j = 0; j < 16; ++j) v[j] = __ldg(lat + half * 16 + j);
-        if (half == 0) {
+        for (int j = 0; j < 4; ++j) {
+          const float4 x = ld_shared_v4(qbuf + (uint32_t)lane * 64u + (((uint32_t)j ^ (((uint32_t)lane >> 1) & 3u)) << 4));
+          r[4 * j] = __float_as_uint(x.x);
+          r[4 * j + 1] = __float_as_uint(x.y);
+          r[4 * j + 2] = __float_as_uint(x.z);
+          r[4 * j + 3] = __float_as_uint(x.w);
+        }
+        __syncwarp();
+        if constexpr (kF8) {
 #pragma unroll
-          for (int j = 0; j < 4; ++j) v[16 + j] = __ldg(rp + j);
+          for (int j = 0; j < 16; ++j) r[j] = bf16x2_to_f16x2(r[j]);
+        }
+        tmem_st16(tl + kColQ + col, r);
+      };
+#pragma unroll 1
+      for (int k0 = 0; k0 < 9; k0 += 3) {
+        uint4 v[3][4];
+#pragma unroll
+        for (int k = 0; k < 3; ++k) {
+          const bool latent = k < 2 || k0 < 6;
+          const uint4* src = latent ? lat + (k0 + k) * 4 : rp;
+          const int step = latent ? kDC : kDR;  // eight rows on, in 16-byte pieces
+#pragma unroll
+          for (int i = 0; i < 4; ++i) v[k][i] = __ldg(src + i * step);
         }
 #pragma unroll
-        for (int ci = 0; ci < 2; ++ci) {
-          uint32_t r[32];
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            r[4 * j] = v[ci * 8 + j].x;
-            r[4 * j + 1] = v[ci * 8 + j].y;
-            r[4 * j + 2] = v[ci * 8 + j].z;
-            r[4 * j + 3] = v[ci * 8 + j].w;
-          }
-          if constexpr (kF8) {
-#pragma unroll
-            for (int j = 0; j < 32; ++j) r[j] = bf16x2_to_f16x2(r[j]);
-          }
-          tmem_st32(tl + kColQ + half * 64 + ci * 32, r);
-        }
-        if (half == 0) {
-          uint32_t r[16];
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            r[4 * j] = v[16 + j].x;
-            r[4 * j + 1] = v[16 + j].y;
-            r[4 * j + 2] = v[16 + j].z;
-            r[4 * j + 3] = v[16 + j].w;
-          }
-          if constexpr (kF8) {
-#pragma unroll
-            for (int j = 0; j < 16; ++j) r[j] = bf16x2_to_f16x2(r[j]);
-          }
-          tmem_st16(tl + kColQ + 128, r);
-        }
+        for (int k = 0; k < 3; ++k) pass(v[k], (uint32_t)((k0 + k) * 16));
       }
       tmem_st_wait();
       tc_fence_before();
@@ -750,6 +764,10 @@ __device__ __forceinline__ void decode_body(const CUtensorMap& kv_map, const CUt
                      own[4 * k + 3]);
       fence_proxy_async_smem();
       __syncwarp();
+      if (!peer_ready) {
+        cluster_wait();
+        peer_ready = true;
+      }
       if (lane == 0) {
         bulk_copy_to_peer(mapa(base + kOffX + (t % kXBufs) * kXBytes + warp_off, peer), stage + warp_off,
                           (uint32_t)kXWarp, mapa(BAR(B_X_FULL0 + t % kXBufs), peer));
@@ -917,24 +935,45 @@ __device__ __forceinline__ void decode_body(const CUtensorMap& kv_map, const CUt
         tc_fence_after();
         const float lt = __uint_as_float(tmem_ld1_sync(tl + kColSum));
         const float inv = 1.f / lt;
+        // The rows lie 1 KB (partials 2 KB) apart, so a thread's own stores
+        // would write 32 lines an instruction: the warp's rows cross through
+        // its part of tile g's exchange buffer, 128 bytes of each row a round,
+        // and leave as whole lines.  That buffer is this warpgroup's until it
+        // stages tile g + 2: the scores in it are consumed, and the peer's
+        // next push into it (tile g + kXBufs) waits for tile g + 2.
+        const uint32_t ebuf = base + kOffX + (g % kXBufs) * kXBytes + warp_off;
+        const uint32_t er = (uint32_t)lane >> 3, ep = (uint32_t)lane & 7u;
+        auto put = [&](int k, uint32_t x, uint32_t y, uint32_t z, uint32_t w4) {
+          st_shared_v4(ebuf + (uint32_t)lane * 128u + (((uint32_t)k ^ ((uint32_t)lane & 7u)) << 4), x, y, z, w4);
+        };
+        auto take = [&](int i) {
+          const uint32_t r = 4u * (uint32_t)i + er;
+          return ld_shared_v4(ebuf + r * 128u + ((ep ^ (r & 7u)) << 4));
+        };
         if (slot < 0) {
-          uint4* dst = reinterpret_cast<uint4*>(a.o_lat + ((size_t)row * kH + h) * kDC + rank * 256);
+          uint16_t* dst = a.o_lat + ((size_t)row * kH + q4 * 32 + er) * kDC + rank * 256 + ep * 8;
 #pragma unroll 1
-          for (int c = 0; c < 256; c += 32) {
-            uint32_t o[32];
-            tmem_ld32_sync(tl + kColO + c, o);
+          for (int c = 0; c < 256; c += 64) {
 #pragma unroll
-            for (int v = 0; v < 4; ++v)
-              dst[c / 8 + v] = make_uint4(
-                  pack_bf16x2(__uint_as_float(o[8 * v + 0]) * inv, __uint_as_float(o[8 * v + 1]) * inv),
-                  pack_bf16x2(__uint_as_float(o[8 * v + 2]) * inv, __uint_as_float(o[8 * v + 3]) * inv),
-                  pack_bf16x2(__uint_as_float(o[8 * v + 4]) * inv, __uint_as_float(o[8 * v + 5]) * inv),
-                  pack_bf16x2(__uint_as_float(o[8 * v + 6]) * inv, __uint_as_float(o[8 * v + 7]) * inv));
+            for (int hf = 0; hf < 2; ++hf) {
+              uint32_t o[32];
+              tmem_ld32_sync(tl + kColO + c + 32 * hf, o);
+#pragma unroll
+              for (int v = 0; v < 4; ++v)
+                put(4 * hf + v, pack_bf16x2(__uint_as_float(o[8 * v + 0]) * inv, __uint_as_float(o[8 * v + 1]) * inv),
+                    pack_bf16x2(__uint_as_float(o[8 * v + 2]) * inv, __uint_as_float(o[8 * v + 3]) * inv),
+                    pack_bf16x2(__uint_as_float(o[8 * v + 4]) * inv, __uint_as_float(o[8 * v + 5]) * inv),
+                    pack_bf16x2(__uint_as_float(o[8 * v + 6]) * inv, __uint_as_float(o[8 * v + 7]) * inv));
+            }
+            __syncwarp();
+#pragma unroll
+            for (int i = 0; i < 8; ++i) *reinterpret_cast<float4*>(dst + (size_t)(4 * i) * kDC + c) = take(i);
+            __syncwarp();
           }
         } else {
           // Partials are read once, by the combine right after this kernel: kept
           // in L2 with evict-last priority through the rest of the KV stream.
-          float4* dst = reinterpret_cast<float4*>(a.part_o + ((size_t)slot * kH + h) * kDC + rank * 256);
+          float* dst = a.part_o + ((size_t)slot * kH + q4 * 32 + er) * kDC + rank * 256 + ep * 4;
           const uint64_t keep = l2_policy_evict_last();
 #pragma unroll 1
           for (int c = 0; c < 256; c += 32) {
@@ -942,10 +981,12 @@ __device__ __forceinline__ void decode_body(const CUtensorMap& kv_map, const CUt
             tmem_ld32_sync(tl + kColO + c, o);
 #pragma unroll
             for (int v = 0; v < 8; ++v)
-              st_global_v4_hint(dst + c / 4 + v,
-                                make_float4(__uint_as_float(o[4 * v]) * inv, __uint_as_float(o[4 * v + 1]) * inv,
-                                            __uint_as_float(o[4 * v + 2]) * inv, __uint_as_float(o[4 * v + 3]) * inv),
-                                keep);
+              put(v, __float_as_uint(__uint_as_float(o[4 * v]) * inv), __float_as_uint(__uint_as_float(o[4 * v + 1]) * inv),
+                  __float_as_uint(__uint_as_float(o[4 * v + 2]) * inv), __float_as_uint(__uint_as_float(o[4 * v + 3]) * inv));
+            __syncwarp();
+#pragma unroll
+            for (int i = 0; i < 8; ++i) st_global_v4_hint(dst + (size_t)(4 * i) * kDC + c, take(i), keep);
+            __syncwarp();
           }
         }
         tc_fence_before();
@@ -962,6 +1003,8 @@ __device__ __forceinline__ void decode_body(const CUtensorMap& kv_map, const CUt
       cf.next();
       cf.next();
     }
+    __syncwarp();
+    if (!peer_ready) cluster_wait();
   };
   if constexpr (kF8) {
     // 512 threads x 128 registers at launch: warpgroup 0 (producer, MMA
@@ -974,9 +1017,11 @@ __device__ __forceinline__ void decode_body(const CUtensorMap& kv_map, const CUt
       if (warp == 0) role_producer();
       else if (warp == 1) role_qk();
       else if (warp == kPvWarp) role_pv();
+      cluster_wait();
     } else if (warp >= kConvWarp0) {
       regs_dec<112>();
       role_convert();
+      cluster_wait();
     } else {
       regs_inc<168>();
       role_softmax();
@@ -986,6 +1031,7 @@ __device__ __forceinline__ void decode_body(const CUtensorMap& kv_map, const CUt
     else if (warp == 1) role_qk();
     else if (warp == kPvWarp) role_pv();
     else role_softmax();
+    if (warp < kSoftWarp0 || warp == kPvWarp) cluster_wait();
   }
 
   tc_fence_before();
