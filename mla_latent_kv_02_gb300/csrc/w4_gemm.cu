@@ -7,9 +7,9 @@
 // group's fp32 sum, so no weight is rounded: a code times a bf16 scale has up
 // to 12 significant bits and would not fit a bf16 operand.
 //
-// * w4_rows_kernel: up to 8 tokens a block, fp32 on the CUDA cores.  A thread
-//   owns one column and 128 values of k (16 words, all requested at once); the
-//   K = 512 step joins four threads' sums through shared memory.
+// * w4_rows_kernel: up to 32 tokens; the columns are the rows of mma.sync
+//   products, the codes go from a word to an operand register without passing
+//   through shared memory.
 // * w4_gemm_kernel: 128 tokens a tile on the tensor cores (tcgen05).  The codes
 //   become exact bf16 integers in shared memory once per (head, column block);
 //   the fp32 sums of all K / G groups of a column block fill the tensor memory
@@ -28,98 +28,135 @@ namespace w4 {
 
 using namespace mla::dev;
 
-constexpr int kSlice = 128;        // values of k per thread
-constexpr int kWordsPer = kSlice / 8;
+// ------------------------------------------------------------------ few tokens
+// A warp owns 16 columns of one head and 128 values of k; W^T is the
+// left operand of mma.sync (m16n8k16: 16 columns x 16 k), the tokens its eight
+// columns, kTiles such tiles of tokens a block.  The order of k inside a
+// product is free as long as both operands share it, so nothing is shuffled:
+// lane (g, q) = (lane / 4, lane % 4) takes the words of columns g and g + 8 at
+// k block 4 j + q, splits each into the pairs (k_i, k_i+4) with a shift and a
+// mask, and reads the same eight k of token g as one 16-byte load.
+//
+// Bound by the 4.2 MB of codes and by latency: a block's loads are all
+// requested before the first product, 27 warps an SM for the whole operator.
+constexpr int kSlice = 128;         // values of k a warp sums
+constexpr int kSteps = kSlice / 32; // words of a column in a slice, four lanes each one
 constexpr int kRowThreads = 256;
-constexpr int32_t kRowsMax = 8;    // more tokens go to the tensor cores
+constexpr int32_t kRowsMax = 32;    // more tokens go to tcgen05
 
-// Eight codes to fp32, exactly: a nibble OR-ed into the mantissa of a power of
-// two whose last place it fills reads 2^(23 - 4i) + nibble; the codes are
-// offset by 8 first (sign bit flipped).
-__device__ __forceinline__ void codes_to_float(uint32_t w, float (&c)[8]) {
-  w ^= 0x88888888u;
-  const uint32_t hi = w >> 20;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int at = i < 5 ? 4 * i : 4 * (i - 5);
-    const uint32_t bits = ((i < 5 ? w : hi) & (0xFu << at)) | ((uint32_t)(127 + 23 - at) << 23);
-    c[i] = __uint_as_float(bits) - (float)((1 << (23 - at)) + 8);
-  }
+// Pair i of a word (offset binary: sign bits flipped) as bf16: 0x4300 | v is 128 + v.
+__device__ __forceinline__ uint32_t code_pair(uint32_t w, int i) {
+  const uint32_t v = ((w >> (4 * i)) & 0x000F000Fu) | 0x43004300u;
+  const __nv_bfloat162 d = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&v), __floats2bfloat162_rn(136.f, 136.f));
+  return *reinterpret_cast<const uint32_t*>(&d);
 }
 
-template <int N, int K, int TT>
+__device__ __forceinline__ void mma_16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+template <int N, int K, int G, int kTiles>
 __global__ void __launch_bounds__(kRowThreads)
-    w4_rows_kernel(const uint16_t* __restrict__ x, const uint32_t* __restrict__ words,
-                   const uint16_t* __restrict__ scales, int group, int32_t T, uint16_t* __restrict__ y) {
-  constexpr int kSplits = K / kSlice;              // threads that share a column
-  constexpr int kCols = kRowThreads / kSplits;
-  __shared__ __align__(16) float xs[TT][K];
-  __shared__ float part[kSplits > 1 ? kSplits - 1 : 1][TT][kCols];
-  const int h = blockIdx.y, n0 = blockIdx.x * kCols;
-  const int64_t t0 = (int64_t)blockIdx.z * TT;
-  const int col = threadIdx.x % kCols, ks = threadIdx.x / kCols;
-  const int n = n0 + col;
-  uint32_t w[kWordsPer];
-  const uint32_t* wp = words + ((int64_t)h * (K / 8) + ks * kWordsPer) * N + n;
+    w4_rows_kernel(const uint4* __restrict__ x, const uint32_t* __restrict__ words,
+                   const uint16_t* __restrict__ scales, int32_t T, uint16_t* __restrict__ y) {
+  constexpr int kSplits = K / kSlice;              // warps that share 16 columns
+  constexpr int kCols = 16 * (kRowThreads / 32) / kSplits;
+  constexpr int kPerGroup = G / 32;                // steps of a group
+  constexpr int kGroups = kSlice / G;              // groups of a slice
+  __shared__ float part[kSplits > 1 ? kSplits - 1 : 1][kTiles * 4][kRowThreads / kSplits];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int g = lane >> 2, q = lane & 3;
+  const int h = blockIdx.y, ks = warp / (8 / kSplits), tile = warp % (8 / kSplits);
+  const int n = blockIdx.x * kCols + tile * 16 + g;
+  const uint32_t* wp = words + ((int64_t)h * (K / 8) + ks * (kSlice / 8) + q) * N + n;
+  uint32_t w[kSteps][2];
 #pragma unroll
-  for (int j = 0; j < kWordsPer; ++j) w[j] = __ldg(wp + (int64_t)j * N);
-  for (int i = threadIdx.x; i < TT * K / 2; i += kRowThreads) {
-    const int t = i / (K / 2), k2 = i % (K / 2);
-    const uint32_t v = t0 + t < T ? __ldg(reinterpret_cast<const uint32_t*>(x) + ((t0 + t) * MLA_NUM_HEADS + h) * (K / 2) + k2) : 0u;
-    xs[t][2 * k2] = __uint_as_float(v << 16);
-    xs[t][2 * k2 + 1] = __uint_as_float(v & 0xFFFF0000u);
+  for (int j = 0; j < kSteps; ++j) {
+    w[j][0] = __ldg(wp + (int64_t)(4 * j) * N);
+    w[j][1] = __ldg(wp + (int64_t)(4 * j) * N + 8);
   }
-  __syncthreads();
-  const uint16_t* sp = scales + ((int64_t)h * (K / group) + ks * kSlice / group) * N + n;
-  const int words_per_group = group / 8;
-  float acc[TT], sum[TT];
+  float s[kGroups][2];
+  const uint16_t* sp = scales + ((int64_t)h * (K / G) + ks * kGroups) * N + n;
 #pragma unroll
-  for (int t = 0; t < TT; ++t) acc[t] = sum[t] = 0.f;
+  for (int i = 0; i < kGroups; ++i) {
+    s[i][0] = __uint_as_float((uint32_t)__ldg(sp + i * N) << 16);
+    s[i][1] = __uint_as_float((uint32_t)__ldg(sp + i * N + 8) << 16);
+  }
+  uint4 v[kTiles][kSteps];
 #pragma unroll
-  for (int j = 0; j < kWordsPer; ++j) {
-    float c[8];
-    codes_to_float(w[j], c);
+  for (int t = 0; t < kTiles; ++t)
 #pragma unroll
-    for (int t = 0; t < TT; ++t) {
-      const float4 a = *reinterpret_cast<const float4*>(&xs[t][ks * kSlice + 8 * j]);
-      const float4 b = *reinterpret_cast<const float4*>(&xs[t][ks * kSlice + 8 * j + 4]);
-      sum[t] = fmaf(a.x, c[0], fmaf(a.y, c[1], fmaf(a.z, c[2], fmaf(a.w, c[3], sum[t]))));
-      sum[t] = fmaf(b.x, c[4], fmaf(b.y, c[5], fmaf(b.z, c[6], fmaf(b.w, c[7], sum[t]))));
-    }
-    if ((j + 1) % words_per_group == 0) {
-      const float s = __uint_as_float((uint32_t)__ldg(sp + (int64_t)(j / words_per_group) * N) << 16);
+    for (int j = 0; j < kSteps; ++j)
+      v[t][j] = 8 * t + g < T ? __ldg(x + ((int64_t)(8 * t + g) * MLA_NUM_HEADS + h) * (K / 8) + ks * (kSlice / 8) + 4 * j + q)
+                              : make_uint4(0u, 0u, 0u, 0u);
+  float acc[kTiles][4], sum[kTiles][4];
 #pragma unroll
-      for (int t = 0; t < TT; ++t) {
-        acc[t] = fmaf(s, sum[t], acc[t]);
-        sum[t] = 0.f;
+  for (int t = 0; t < kTiles; ++t)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) acc[t][i] = sum[t][i] = 0.f;
+#pragma unroll
+  for (int j = 0; j < kSteps; ++j) {
+    const uint32_t w0 = w[j][0] ^ 0x88888888u, w1 = w[j][1] ^ 0x88888888u;
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {  // pairs 2 half, 2 half + 1
+      const uint32_t a[4] = {code_pair(w0, 2 * half), code_pair(w1, 2 * half), code_pair(w0, 2 * half + 1),
+                             code_pair(w1, 2 * half + 1)};
+#pragma unroll
+      for (int t = 0; t < kTiles; ++t) {
+        const uint32_t lo = half ? v[t][j].y : v[t][j].x, hi = half ? v[t][j].w : v[t][j].z;
+        mma_16816(sum[t], a, __byte_perm(lo, hi, 0x5410), __byte_perm(lo, hi, 0x7632));
       }
+    }
+    if ((j + 1) % kPerGroup == 0) {
+#pragma unroll
+      for (int t = 0; t < kTiles; ++t)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {  // rows g (i < 2) and g + 8 of the product are columns n, n + 8
+          acc[t][i] = fmaf(s[j / kPerGroup][i >> 1], sum[t][i], acc[t][i]);
+          sum[t][i] = 0.f;
+        }
     }
   }
   if (kSplits > 1) {
+    const int at = tile * 32 + lane;
     if (ks > 0) {
 #pragma unroll
-      for (int t = 0; t < TT; ++t) part[ks - 1][t][col] = acc[t];
+      for (int t = 0; t < kTiles; ++t)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) part[ks - 1][4 * t + i][at] = acc[t][i];
     }
     __syncthreads();
     if (ks > 0) return;
 #pragma unroll
-    for (int t = 0; t < TT; ++t)
+    for (int t = 0; t < kTiles; ++t)
 #pragma unroll
-      for (int p = 0; p < kSplits - 1; ++p) acc[t] += part[p][t][col];
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int p = 0; p < kSplits - 1; ++p) acc[t][i] += part[p][4 * t + i][at];
   }
 #pragma unroll
-  for (int t = 0; t < TT; ++t)
-    if (t0 + t < T) {
-      const __nv_bfloat16 v = __float2bfloat16_rn(acc[t]);
-      y[((t0 + t) * MLA_NUM_HEADS + h) * N + n] = *reinterpret_cast<const uint16_t*>(&v);
+  for (int t = 0; t < kTiles; ++t)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int tok = 8 * t + 2 * q + (i & 1);
+      if (tok < T) {
+        const __nv_bfloat16 r = __float2bfloat16_rn(acc[t][i]);
+        y[((int64_t)tok * MLA_NUM_HEADS + h) * N + n + 8 * (i >> 1)] = *reinterpret_cast<const uint16_t*>(&r);
+      }
     }
 }
 
-template <int N, int K, int TT>
+template <int N, int K, int G>
 cudaError_t run_rows(const W4Args& a, cudaStream_t stream) {
-  constexpr int kCols = kRowThreads / (K / kSlice);
-  const dim3 grid(N / kCols, MLA_NUM_HEADS, (unsigned)((a.T + TT - 1) / TT));
-  w4_rows_kernel<N, K, TT><<<grid, kRowThreads, 0, stream>>>(a.x, a.words, a.scales, a.group, a.T, a.y);
+  constexpr int kCols = 16 * (kRowThreads / 32) / (K / kSlice);
+  const dim3 grid(N / kCols, MLA_NUM_HEADS);
+  const uint4* x = reinterpret_cast<const uint4*>(a.x);
+  if (a.T <= 8) w4_rows_kernel<N, K, G, 1><<<grid, kRowThreads, 0, stream>>>(x, a.words, a.scales, a.T, a.y);
+  else if (a.T <= 16) w4_rows_kernel<N, K, G, 2><<<grid, kRowThreads, 0, stream>>>(x, a.words, a.scales, a.T, a.y);
+  else w4_rows_kernel<N, K, G, 4><<<grid, kRowThreads, 0, stream>>>(x, a.words, a.scales, a.T, a.y);
   return cudaGetLastError();
 }
 
@@ -389,17 +426,16 @@ cudaError_t run_gemm(const W4Args& a, const CUtensorMap& x_map, const CUtensorMa
   return cudaGetLastError();
 }
 
-template <int N, int K>
+template <int N, int K, int G>
 cudaError_t run(const W4Args& a, const CUtensorMap& x_map, const CUtensorMap& y_map, cudaStream_t stream) {
-  if (a.T > kRowsMax) {
-    if (a.group == 128) return run_gemm<N, K, 128>(a, x_map, y_map, stream);
-    if (a.group == 64) return run_gemm<N, K, 64>(a, x_map, y_map, stream);
-    return run_gemm<N, K, 32>(a, x_map, y_map, stream);
-  }
-  if (a.T == 1) return run_rows<N, K, 1>(a, stream);
-  if (a.T == 2) return run_rows<N, K, 2>(a, stream);
-  if (a.T <= 4) return run_rows<N, K, 4>(a, stream);
-  return run_rows<N, K, 8>(a, stream);
+  return a.T <= kRowsMax ? run_rows<N, K, G>(a, stream) : run_gemm<N, K, G>(a, x_map, y_map, stream);
+}
+
+template <int N, int K>
+cudaError_t run_group(const W4Args& a, const CUtensorMap& x_map, const CUtensorMap& y_map, cudaStream_t stream) {
+  if (a.group == 128) return run<N, K, 128>(a, x_map, y_map, stream);
+  if (a.group == 64) return run<N, K, 64>(a, x_map, y_map, stream);
+  return run<N, K, 32>(a, x_map, y_map, stream);
 }
 
 // The layout above from bf16 weights: s = bf16(amax / 7) of each group of a
@@ -437,8 +473,8 @@ bool w4_uses_maps(int32_t T) { return T > w4::kRowsMax; }
 cudaError_t launch_w4_gemm(HeadGemm kind, const W4Args& args, const CUtensorMap& x_map, const CUtensorMap& y_map,
                            cudaStream_t stream) {
   if (args.T <= 0) return cudaSuccess;
-  return kind == HeadGemm::kAbsorbQ ? w4::run<512, 128>(args, x_map, y_map, stream)
-                                    : w4::run<128, 512>(args, x_map, y_map, stream);
+  return kind == HeadGemm::kAbsorbQ ? w4::run_group<512, 128>(args, x_map, y_map, stream)
+                                    : w4::run_group<128, 512>(args, x_map, y_map, stream);
 }
 
 cudaError_t launch_w4_pack(const uint16_t* w, int K, int N, int group, uint32_t* words, uint16_t* scales,
