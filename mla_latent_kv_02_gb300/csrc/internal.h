@@ -253,7 +253,7 @@ struct W4Args {
 };
 // x_map, y_map (read only where w4_uses_maps(T)): x as {K, 128 heads, T} in
 // boxes of 64 k x 128 tokens, 128-byte swizzle; y as {N, 128, T} in boxes of
-// 32 columns x 128 tokens, 64-byte swizzle.
+// 32 columns x 32 tokens, 64-byte swizzle.
 bool w4_uses_maps(int32_t T);
 cudaError_t launch_w4_gemm(HeadGemm kind, const W4Args& args, const CUtensorMap& x_map, const CUtensorMap& y_map,
                            cudaStream_t stream);

@@ -1146,7 +1146,7 @@ static mla_status w4_gemm(mla::HeadGemm kind, const void* x, const void* words, 
     const uint64_t K = absorb ? MLA_HEAD_DIM_C : MLA_LATENT_DIM, N = absorb ? MLA_LATENT_DIM : MLA_HEAD_DIM_C;
     const uint64_t xd[3] = {K, MLA_NUM_HEADS, (uint64_t)T}, xs[2] = {K * 2, K * 2 * MLA_NUM_HEADS};
     const uint64_t yd[3] = {N, MLA_NUM_HEADS, (uint64_t)T}, ys[2] = {N * 2, N * 2 * MLA_NUM_HEADS};
-    const uint32_t xbox[3] = {64, 1, 128}, ybox[3] = {32, 1, 128};
+    const uint32_t xbox[3] = {64, 1, 128}, ybox[3] = {32, 1, 32};
     s = make_map(&xm, x, 3, xd, xs, xbox, "activations");
     if (s == MLA_OK) s = make_map(&ym, y, 3, yd, ys, ybox, "outputs", CU_TENSOR_MAP_SWIZZLE_64B);
     if (s != MLA_OK) return s;

@@ -11,10 +11,9 @@
 //   products, the codes go from a word to an operand register without passing
 //   through shared memory.
 // * w4_gemm_kernel: 128 tokens a tile on the tensor cores (tcgen05).  The codes
-//   become exact bf16 integers in shared memory once per (head, column block);
-//   the fp32 sums of all K / G groups of a column block fill the tensor memory
-//   (K / G x kNC = 512 columns), and the epilogue adds them up under their
-//   scales.  See the kernel.
+//   become exact bf16 integers in shared memory once per head, each group's
+//   fp32 sums pass through a slot of tensor memory and are added up under
+//   their scales in registers.  See the kernel.
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -160,80 +159,102 @@ cudaError_t run_rows(const W4Args& a, cudaStream_t stream) {
   return cudaGetLastError();
 }
 
-// ------------------------------------------------------------------ tensor cores
-// A CTA takes a contiguous range of the work units (head, column block, token
-// tile), token tiles fastest, so a column block's weights are unpacked once
-// and its token tiles stream past them.
+// ------------------------------------------------------------------ many tokens
+// A CTA takes a contiguous range of the work units (head, token tile), token
+// tiles fastest, so a head's weights are unpacked once into shared memory (128
+// KB of exact bf16 integers) and its token tiles stream past them.
+//   for each 128-column block of y, for each group g of k:
+//     D_slot[128 x 128] = x[128 x G] . C_g[G x 128]     tcgen05, fp32 in TMEM
+//     acc += s_g D_slot                                  fp32, in registers
+//   y block = bf16(acc)
+// TMEM is a ring of four 128-column slots, so the products of one group run
+// while the sums of the one before are scaled; every group size has the same
+// shape of work.
 // Warps: 0 loads x by TMA (chunks of 64 k, a ring of kStages), 1 issues the
-// MMAs, 2-9 unpack the weights and run the epilogue: two warps per TMEM lane
-// quarter (thread = token row), taking alternate 32-column boxes.
-//   D[g][128 x kNC] = x[128 x G] . C_g[G x kNC]   (codes as bf16 integers)
-//   y = sum_g s_g D[g]                            (fp32, one bf16 rounding)
+// MMAs, 2-9 unpack the weights and scale the sums: two warps per TMEM lane
+// quarter (thread = token row), 64 columns each, which store their rows in
+// boxes of 32 x 32 by TMA without waiting for one another.
 // B is K-major: a word's eight codes are eight consecutive k of a column, one
-// 16-byte store into the 128-byte swizzled row of that column.
-// Every wait is bounded; the epilogue warps take each tile's decision to go on
-// together, so that no named barrier is left short.
+// 16-byte store into the 128-byte swizzled row of that column.  The words and
+// scales of the next head are loaded into registers a head ahead, the first
+// head's before the set-up (loading them at the switch, warmed in L2, cost
+// 2 % at 2048 tokens).
+// The MMA loop is unrolled over a chunk's four steps on precomputed
+// descriptors: rolled, with a descriptor built per step, each MMA took 550
+// cycles to issue instead of about 70.
+// Measured (A5, groups of 128, 2048 tokens, 340 MB): 62 us, 5.5 TB/s, bound by
+// the x and y streams; 128 tokens, cold weights: 9.7 us, the chain load ->
+// unpack -> products -> scale of a single tile per SM.  Groups of 32 double the
+// slots a tile passes through the epilogue: 85 us.
+// Every wait is bounded, the ones between the epilogue warps too (mbarriers).
 constexpr int kStages = 4;
 constexpr int kChunkBytes = 128 * 64 * 2;        // [128 tokens x 64 k] bf16
+constexpr int kSlots = 4, kSlotCols = 128;
 constexpr int kBoxCols = 32;
-constexpr int kBoxBytes = 128 * kBoxCols * 2;    // one output box, 64-byte swizzled rows
-constexpr int kEpiWarps = 8;
-constexpr int kThreads = 32 * (2 + kEpiWarps);
-constexpr uint32_t kEpiBar = 1, kHalfBar = 2;    // named barriers: all epilogue warps; the four of a half
+constexpr int kBoxBytes = 32 * kBoxCols * 2;     // a warp's output box, 64-byte swizzled rows
+constexpr int kEpiWarps = 8, kEpiThreads = 32 * kEpiWarps;
+constexpr int kThreads = 64 + kEpiThreads;
 
 template <int N, int K, int G>
 struct Cfg {
-  static constexpr int kGroups = K / G;
-  static constexpr int kNC = 512 / kGroups < N ? 512 / kGroups : N;   // columns of a block
-  static constexpr int kBlocks = N / kNC;
-  static constexpr int kChunks = K / 64;
-  static constexpr int kWChunkBytes = kNC * 128;                      // [kNC columns x 64 k] bf16
-  static constexpr int kWBytes = kChunks * kWChunkBytes;
-  static constexpr int kBoxes = kNC / kBoxCols;
-  static constexpr int kMmaN = kNC < 256 ? kNC : 256;
-  static constexpr uint32_t kIdesc = idesc_bf16_f32(128, kMmaN, false, false);
-  static constexpr int kOffA = kWBytes;
+  static constexpr int kGroups = K / G, kBlocks = N / kSlotCols, kChunks = K / 64;
+  static constexpr int kWChunkBytes = N * 128;                        // [N columns x 64 k] bf16
+  static constexpr int kOffA = kChunks * kWChunkBytes;
   static constexpr int kOffOut = kOffA + kStages * kChunkBytes;
-  static constexpr int kOffScale = kOffOut + 2 * kBoxBytes;           // fp32 [kGroups][kNC]
-  static constexpr int kOffBar = kOffScale + 512 * 4;
-  static constexpr int kSmem = kOffBar + 128 + 1024;
-  static_assert(kGroups * kNC <= 512 && kNC % kBoxCols == 0 && kNC * kBlocks == N, "column blocks");
+  static constexpr int kOffScale = kOffOut + kEpiWarps * kBoxBytes;   // fp32 [kGroups][N]
+  static constexpr int kOffBar = kOffScale + kGroups * N * 4;
+  static constexpr int kNumBars = 2 * kStages + 2 * kSlots + kChunks + 3;
+  static constexpr int kSmem = kOffBar + 8 * kNumBars + 16 + 1024;
+  static constexpr int kWords = N * (K / 8) / kEpiThreads;            // words a thread unpacks
+  static constexpr int kScales = kGroups * N / kEpiThreads;
+  static constexpr uint32_t kIdesc = idesc_bf16_f32(128, kSlotCols, false, false);
   static_assert(kSmem <= 232448, "shared memory layout does not fit");
 };
 
-// Eight codes of a word (k ascending) to four bf16 pairs: 0x4300 | v is 128 + v.
+// Eight codes of a word (k ascending) to four bf16 pairs.
 __device__ __forceinline__ uint4 codes_to_bf16(uint32_t w) {
   w ^= 0x88888888u;
   uint32_t r[4];
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const uint32_t two = ((w >> (8 * j)) & 0xFFu) * 0x1001u;          // low nibble at 0, high nibble at 16
-    const uint32_t v = (two & 0x000F000Fu) | 0x43004300u;
-    const __nv_bfloat162 d = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&v), __floats2bfloat162_rn(136.f, 136.f));
-    r[j] = *reinterpret_cast<const uint32_t*>(&d);
-  }
+  for (int j = 0; j < 4; ++j)
+    r[j] = code_pair(((w >> (8 * j)) & 0xFFu) * 0x1001u, 0);          // low nibble at 0, high nibble at 16
   return make_uint4(r[0], r[1], r[2], r[3]);
 }
 
 template <int N, int K, int G>
 __global__ void __launch_bounds__(kThreads, 1)
     w4_gemm_kernel(const __grid_constant__ CUtensorMap x_map, const __grid_constant__ CUtensorMap y_map,
-                   const uint32_t* __restrict__ words, const uint16_t* __restrict__ scales, int32_t tiles, int32_t* err) {
+                   const uint32_t* __restrict__ words, const uint16_t* __restrict__ scales, int32_t T, int32_t* err) {
   using C = Cfg<N, K, G>;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;
   uint8_t* gbase = smem_raw + (base - raw);
   const uint32_t bars = base + C::kOffBar;
-  const uint32_t full0 = bars, empty0 = bars + 8 * kStages, d_full = bars + 16 * kStages, d_free = d_full + 8,
-                 w_ready = d_full + 16, drain = d_full + 24;
-  volatile int32_t* abort_flag = reinterpret_cast<volatile int32_t*>(gbase + C::kOffBar + 112);
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(gbase + C::kOffBar + 120);
+  const uint32_t full0 = bars, empty0 = full0 + 8 * kStages, s_full0 = empty0 + 8 * kStages,
+                 s_free0 = s_full0 + 8 * kSlots, w_ready0 = s_free0 + 8 * kSlots, head_done = w_ready0 + 8 * C::kChunks,
+                 sc_ready = head_done + 8, drain = head_done + 16;
+  volatile int32_t* abort_flag = reinterpret_cast<volatile int32_t*>(gbase + C::kOffBar + 8 * C::kNumBars);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(gbase + C::kOffBar + 8 * C::kNumBars + 8);
   float* sc = reinterpret_cast<float*>(gbase + C::kOffScale);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int64_t units = (int64_t)MLA_NUM_HEADS * C::kBlocks * tiles;
-  const int64_t u0 = units * blockIdx.x / gridDim.x, u1 = units * (blockIdx.x + 1) / gridDim.x;
+  const int tiles = (T + 127) / 128, units = MLA_NUM_HEADS * tiles;
+  const int u0 = (int)((int64_t)units * blockIdx.x / gridDim.x), u1 = (int)((int64_t)units * (blockIdx.x + 1) / gridDim.x);
+
+  // A head's words and scales, this thread's share, into registers.
+  const int tid = threadIdx.x - 64;                  // epilogue thread 0 .. 255
+  uint32_t w[C::kWords];
+  uint16_t sv[C::kScales];
+  auto request = [&](int h) {
+    const uint32_t* wp = words + (int64_t)h * (K / 8) * N + tid;
+    const uint16_t* sp = scales + (int64_t)h * C::kGroups * N + tid;
+#pragma unroll
+    for (int j = 0; j < C::kWords; ++j) w[j] = __ldg(wp + j * kEpiThreads);
+#pragma unroll
+    for (int j = 0; j < C::kScales; ++j) sv[j] = __ldg(sp + j * kEpiThreads);
+  };
+  if (warp >= 2 && u0 < u1) request(u0 / tiles);
 
   if (threadIdx.x == 0) {
     *abort_flag = 0;
@@ -241,15 +262,19 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(full0 + 8 * i, 1);
       mbar_init(empty0 + 8 * i, 1);
     }
-    mbar_init(d_full, 1);
-    mbar_init(d_free, kEpiWarps);
-    mbar_init(w_ready, kEpiWarps);
+    for (int i = 0; i < kSlots; ++i) {
+      mbar_init(s_full0 + 8 * i, 1);
+      mbar_init(s_free0 + 8 * i, kEpiWarps);
+    }
+    for (int i = 0; i < C::kChunks; ++i) mbar_init(w_ready0 + 8 * i, kEpiWarps);
+    mbar_init(head_done, kEpiWarps);
+    mbar_init(sc_ready, kEpiWarps);
     mbar_init(drain, 1);
     fence_mbar_init();
   }
   if (warp == 1) {
     __syncwarp();
-    tmem_alloc(smem_u32(tmem_slot), 512);
+    tmem_alloc(smem_u32(tmem_slot), kSlots * kSlotCols);
     tmem_relinquish();
   }
   tc_fence_before();
@@ -264,8 +289,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       prefetch_tmap(&y_map);
       uint32_t n = 0;
       bool ok = true;
-      for (int64_t u = u0; ok && u < u1; ++u) {
-        const int h = (int)(u / tiles / C::kBlocks), m0 = (int)(u % tiles) * 128;
+      for (int u = u0; ok && u < u1; ++u) {
+        const int h = u / tiles, m0 = u % tiles * 128;
         for (int kc = 0; kc < C::kChunks; ++kc, ++n) {
           const uint32_t st = n % kStages, use = n / kStages;
           if (use > 0 && !wait_phase(empty0 + 8 * st, (use - 1) & 1u, err, abort_flag)) {
@@ -283,35 +308,42 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp == 1) {
     // ---------------------------------------------------------------- MMA issue
     if (lane == 0) {
-      uint32_t n = 0, i = 0, blocks = 0;
-      int64_t hb_now = -1;
+      static_assert(C::kBlocks == 1 || C::kChunks <= kStages, "every column block reads the tile's resident chunks");
+      const uint64_t adesc0 = sdesc_sw128(base + C::kOffA, 16, 1024), wdesc0 = sdesc_sw128(base, 16, 1024);
+      uint32_t n = 0, slot = 0, heads = 0;
+      int h_now = -1;
       bool ok = true;
-      for (int64_t u = u0; ok && u < u1; ++u, ++i) {
-        const int64_t hb = u / tiles;
-        if (hb != hb_now) {
-          hb_now = hb;
-          ok = wait_phase(w_ready, blocks++ & 1u, err, abort_flag);
+      for (int u = u0; ok && u < u1; ++u, n += C::kChunks) {
+        const bool fresh = u / tiles != h_now;       // the head's first tile: its weights arrive chunk by chunk
+        if (fresh) {
+          h_now = u / tiles;
+          ++heads;
         }
-        if (ok && i > 0) ok = wait_phase(d_free, (i - 1) & 1u, err, abort_flag);
-        for (int kc = 0; ok && kc < C::kChunks; ++kc, ++n) {
-          const uint32_t st = n % kStages;
-          if (!wait_phase(full0 + 8 * st, (n / kStages) & 1u, err, abort_flag)) {
-            ok = false;
-            break;
-          }
-          tc_fence_after();
-          const uint32_t sa = base + C::kOffA + st * kChunkBytes, sb = base + kc * C::kWChunkBytes;
+        for (int nb = 0; ok && nb < C::kBlocks; ++nb) {
+          for (int kc = 0; ok && kc < C::kChunks; ++kc) {
+            const uint32_t c = n + kc, st = c % kStages;
+            if (nb == 0) {
+              ok = (!fresh || wait_phase(w_ready0 + 8 * kc, (heads - 1) & 1u, err, abort_flag)) &&
+                   wait_phase(full0 + 8 * st, (c / kStages) & 1u, err, abort_flag);
+              if (!ok) break;
+            }
+            const uint64_t da = adesc0 + (uint64_t)((st * kChunkBytes) >> 4);
+            const uint64_t db = wdesc0 + (uint64_t)((kc * C::kWChunkBytes + nb * kSlotCols * 128) >> 4);
 #pragma unroll
-          for (int kk = 0; kk < 4; ++kk) {
-            const int k = kc * 64 + kk * 16;
-#pragma unroll
-            for (int nh = 0; nh < C::kNC / C::kMmaN; ++nh)
-              mma_ss(tmem + (k / G) * C::kNC + nh * C::kMmaN, sdesc_sw128(sa + kk * 32, 16, 1024),
-                     sdesc_sw128(sb + nh * C::kMmaN * 128 + kk * 32, 16, 1024), C::kIdesc, k % G ? 1u : 0u);
+            for (int kk = 0; kk < 4; ++kk) {
+              const bool first = G == 128 ? kk == 0 && kc % 2 == 0 : kk % (G / 16) == 0;
+              const bool last = G == 128 ? kk == 3 && kc % 2 == 1 : kk % (G / 16) == G / 16 - 1;
+              if (first && slot >= (uint32_t)kSlots)
+                ok = ok && wait_phase(s_free0 + 8 * (slot % kSlots), (slot / kSlots - 1) & 1u, err, abort_flag);
+              if (!ok) break;
+              if (kk == 0 || first) tc_fence_after();
+              mma_ss(tmem + (slot % kSlots) * kSlotCols, da + (uint64_t)((kk * 32) >> 4), db + (uint64_t)((kk * 32) >> 4),
+                     C::kIdesc, first ? 0u : 1u);
+              if (last) tc_commit(s_full0 + 8 * (slot++ % kSlots));
+            }
+            if (ok && nb == C::kBlocks - 1) tc_commit(empty0 + 8 * st);
           }
-          tc_commit(empty0 + 8 * st);
         }
-        if (ok) tc_commit(d_full);
       }
       tc_commit(drain);  // every MMA has finished before TMEM is released
       wait_phase_drain(drain, 0);
@@ -319,97 +351,108 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncwarp();
   } else {
     // ---------------------------------------------------------------- weights and epilogue
-    const int tid = threadIdx.x - 64;                // 0 .. 255
     const int q4 = warp & 3, half = (warp - 2) >> 2;
-    const uint32_t r = (uint32_t)(q4 * 32 + lane);   // token row = TMEM lane
-    const uint32_t tl = tmem + ((uint32_t)(q4 * 32) << 16);
-    const uint32_t out = base + C::kOffOut + half * kBoxBytes;
-    const bool leader = (warp - 2) % 4 == 0 && lane == 0;
-    int64_t hb_now = -1;
-    uint32_t i = 0;
-    for (int64_t u = u0; u < u1; ++u, ++i) {
-      const int64_t hb = u / tiles;
-      const int h = (int)(hb / C::kBlocks), n0 = (int)(hb % C::kBlocks) * C::kNC, m0 = (int)(u % tiles) * 128;
-      if (hb != hb_now) {
-        // Every MMA of the block before has completed (its last tile's d_full)
-        // and every warp has read that tile's scales: the barrier below.
-        hb_now = hb;
-        constexpr int kPer = C::kNC * (K / 8) / 256, kBatch = kPer < 16 ? kPer : 16;
-        const uint32_t* wp = words + (int64_t)h * (K / 8) * N + n0;
-        named_bar_sync(kEpiBar, 32 * kEpiWarps);
-        for (int s = tid; s < C::kGroups * C::kNC; s += 256)
-          sc[s] = __uint_as_float((uint32_t)__ldg(scales + ((int64_t)h * C::kGroups + s / C::kNC) * N + n0 + s % C::kNC) << 16);
-#pragma unroll 1
-        for (int b = 0; b < kPer; b += kBatch) {
-          uint32_t w[kBatch];
-#pragma unroll
-          for (int j = 0; j < kBatch; ++j) {
-            const int at = (b + j) * 256 + tid;
-            w[j] = __ldg(wp + (int64_t)(at / C::kNC) * N + at % C::kNC);
-          }
-#pragma unroll
-          for (int j = 0; j < kBatch; ++j) {
-            const int at = (b + j) * 256 + tid, n = at % C::kNC, kb = at / C::kNC;
-            const uint4 v = codes_to_bf16(w[j]);
-            st_shared_v4(base + (kb / 8) * C::kWChunkBytes + n * 128 + (((kb & 7) ^ (n & 7)) << 4), v.x, v.y, v.z, v.w);
-          }
+    const uint32_t tl = tmem + ((uint32_t)(q4 * 32) << 16) + half * 64;
+    const uint32_t box = base + C::kOffOut + (warp - 2) * kBoxBytes;
+    int h_now = -1;
+    uint32_t heads = 0, slot = 0;
+    bool ok = true;
+    for (int u = u0; ok && u < u1; ++u) {
+      const int h = u / tiles, m0 = u % tiles * 128 + q4 * 32;
+      if (h != h_now) {
+        // Every MMA of the head before has completed (this warp has seen its
+        // last slot full); its scales may go once every warp is past them.
+        if (h_now >= 0) {
+          if (lane == 0) mbar_arrive(head_done);
+          ok = __all_sync(0xffffffffu, wait_phase<false, true>(head_done, (heads - 1) & 1u, err, abort_flag));
+          if (!ok) break;
         }
-        fence_proxy_async_smem();
+        h_now = h;
+#pragma unroll
+        for (int j = 0; j < C::kScales; ++j) sc[j * kEpiThreads + tid] = __uint_as_float((uint32_t)sv[j] << 16);
         __syncwarp();
-        if (lane == 0) mbar_arrive(w_ready);
+        if (lane == 0) mbar_arrive(sc_ready);
+        constexpr int kPer = C::kWords / C::kChunks;  // words of a chunk
+#pragma unroll
+        for (int kc = 0; kc < C::kChunks; ++kc) {
+#pragma unroll
+          for (int j = kc * kPer; j < (kc + 1) * kPer; ++j) {
+            const int at = j * kEpiThreads + tid, n = at % N, kb = at / N;
+            const uint4 v = codes_to_bf16(w[j]);
+            st_shared_v4(base + kc * C::kWChunkBytes + n * 128 + (((kb & 7) ^ (n & 7)) << 4), v.x, v.y, v.z, v.w);
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(w_ready0 + 8 * kc);
+        }
+        if (h < (u1 - 1) / tiles) request(h + 1);
+        ok = __all_sync(0xffffffffu, wait_phase<false, true>(sc_ready, heads & 1u, err, abort_flag));
+        if (!ok) break;
+        ++heads;
       }
-      const bool w = wait_phase(d_full, i & 1u, err, abort_flag);
-      if (!named_bar_and(kEpiBar, 32 * kEpiWarps, w)) break;
-      tc_fence_after();
 #pragma unroll 1
-      for (int b = half; b < C::kBoxes; b += 2) {
-        float acc[kBoxCols];
+      for (int nb = 0; ok && nb < C::kBlocks; ++nb) {
+        float acc[64];
 #pragma unroll
-        for (int j = 0; j < kBoxCols; ++j) acc[j] = 0.f;
+        for (int j = 0; j < 64; ++j) acc[j] = 0.f;
 #pragma unroll 1
-        for (int g = 0; g < C::kGroups; ++g) {
-          uint32_t d[32];
-          tmem_ld32_sync(tl + g * C::kNC + b * kBoxCols, d);
-          const float4* s4 = reinterpret_cast<const float4*>(sc + g * C::kNC + b * kBoxCols);
+        for (int g = 0; g < C::kGroups; ++g, ++slot) {
+          ok = __all_sync(0xffffffffu, wait_phase<false, true>(s_full0 + 8 * (slot % kSlots), (slot / kSlots) & 1u, err, abort_flag));
+          if (!ok) break;
+          tc_fence_after();
+          const float4* s4 = reinterpret_cast<const float4*>(sc + g * N + nb * kSlotCols + half * 64);
 #pragma unroll
-          for (int j = 0; j < kBoxCols / 4; ++j) {
-            const float4 s = s4[j];
-            acc[4 * j] = fmaf(s.x, __uint_as_float(d[4 * j]), acc[4 * j]);
-            acc[4 * j + 1] = fmaf(s.y, __uint_as_float(d[4 * j + 1]), acc[4 * j + 1]);
-            acc[4 * j + 2] = fmaf(s.z, __uint_as_float(d[4 * j + 2]), acc[4 * j + 2]);
-            acc[4 * j + 3] = fmaf(s.w, __uint_as_float(d[4 * j + 3]), acc[4 * j + 3]);
+          for (int b = 0; b < 2; ++b) {
+            uint32_t d[32];
+            tmem_ld32_sync(tl + (slot % kSlots) * kSlotCols + 32 * b, d);
+            if (b == 1) {
+              tc_fence_before();
+              __syncwarp();
+              if (lane == 0) mbar_arrive(s_free0 + 8 * (slot % kSlots));
+            }
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              const float4 s = s4[8 * b + j];
+              float* v = acc + 32 * b + 4 * j;
+              v[0] = fmaf(s.x, __uint_as_float(d[4 * j]), v[0]);
+              v[1] = fmaf(s.y, __uint_as_float(d[4 * j + 1]), v[1]);
+              v[2] = fmaf(s.z, __uint_as_float(d[4 * j + 2]), v[2]);
+              v[3] = fmaf(s.w, __uint_as_float(d[4 * j + 3]), v[3]);
+            }
           }
         }
-        if (b + 2 >= C::kBoxes) {  // this half's last read of the tile's sums
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(d_free);
-        }
-        if (leader) bulk_wait_all_read();  // the box's previous store has read it
-        named_bar_sync(kHalfBar + half, 128);
-        // 64-byte swizzle: row r at 64 r, 16-byte piece c at c ^ ((r / 2) & 3)
+        if (!ok) break;
+        if (m0 < T) {  // warp-uniform: rows past T are not stored
 #pragma unroll
-        for (int c = 0; c < 4; ++c)
-          st_shared_v4(out + r * 64u + (((uint32_t)c ^ ((r >> 1) & 3u)) << 4), pack_bf16x2(acc[8 * c], acc[8 * c + 1]),
-                       pack_bf16x2(acc[8 * c + 2], acc[8 * c + 3]), pack_bf16x2(acc[8 * c + 4], acc[8 * c + 5]),
-                       pack_bf16x2(acc[8 * c + 6], acc[8 * c + 7]));
-        fence_proxy_async_smem();
-        named_bar_sync(kHalfBar + half, 128);
-        if (leader) {
-          tma_store_3d(&y_map, out, n0 + b * kBoxCols, h, m0);
-          bulk_commit_group();
+          for (int b = 0; b < 2; ++b) {
+            if (lane == 0) bulk_wait_all_read();  // the box's previous store has read it
+            __syncwarp();
+            // 64-byte swizzle: row r at 64 r, 16-byte piece c at c ^ ((r / 2) & 3)
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              const float* v = acc + 32 * b + 8 * c;
+              st_shared_v4(box + lane * 64u + (((uint32_t)c ^ (((uint32_t)lane >> 1) & 3u)) << 4), pack_bf16x2(v[0], v[1]),
+                           pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+              tma_store_3d(&y_map, box, nb * kSlotCols + half * 64 + b * kBoxCols, h, m0);
+              bulk_commit_group();
+            }
+          }
         }
       }
-      if (half >= C::kBoxes && lane == 0) mbar_arrive(d_free);  // a half without boxes
     }
-    if (leader) bulk_wait_all_read();  // the staging boxes are released at exit
+    if (lane == 0) bulk_wait_all_read();  // the staging box is released at exit
+    __syncwarp();
   }
   tc_fence_before();
   __syncthreads();
   if (warp == 1) {
     __syncwarp();
     tc_fence_after();
-    tmem_dealloc(tmem, 512);
+    tmem_dealloc(tmem, kSlots * kSlotCols);
   }
 }
 
@@ -419,10 +462,8 @@ cudaError_t run_gemm(const W4Args& a, const CUtensorMap& x_map, const CUtensorMa
   auto* kern = w4_gemm_kernel<N, K, G>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
   if (e != cudaSuccess) return e;
-  const int32_t tiles = (a.T + 127) / 128;
-  const int64_t units = (int64_t)MLA_NUM_HEADS * C::kBlocks * tiles;
-  kern<<<(unsigned)(units < 152 ? units : 152), kThreads, C::kSmem, stream>>>(x_map, y_map, a.words, a.scales, tiles,
-                                                                              a.dev_err);
+  const int units = MLA_NUM_HEADS * ((a.T + 127) / 128);
+  kern<<<units < 152 ? units : 152, kThreads, C::kSmem, stream>>>(x_map, y_map, a.words, a.scales, a.T, a.dev_err);
   return cudaGetLastError();
 }
 
