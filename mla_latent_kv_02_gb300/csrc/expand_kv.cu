@@ -162,6 +162,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     __syncwarp();
   } else if (warp == 1) {
     if (lane == 0 && even) {
+      // Descriptors of chunk 0 / stage 0; an MMA's are these plus an offset (a
+      // descriptor built per MMA stalls the issue).
+      const uint64_t adesc0 = sdesc_sw128(base, 16, 1024);
+      const uint64_t kdesc0 = sdesc_sw128(base + kOffB, 16, 1024);
+      const uint64_t vdesc0 = sdesc_sw128(base + kOffB + kBHalf, 8192, 1024);
       int g = 0, na = 0, cur = -1, j = 0;
       bool ok = true;
       for (int64_t u = u0; u < u1 && ok; ++u, ++j) {
@@ -176,6 +181,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         if (use > 0 && !wait_phase<true>(BAR(kBarAccEmpty + buf), (uint32_t)((use - 1) & 1), err, abort_flag)) break;
         tc_fence_after();
         const uint32_t d = tmem + 256u * buf;
+#pragma unroll
         for (int kc = 0; kc < kKCh; ++kc, ++g) {
           const int s = g % kStages;
           if (!wait_phase(BAR(kBarFull + s), (uint32_t)((g / kStages) & 1), err, abort_flag)) {
@@ -183,13 +189,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             break;
           }
           tc_fence_after();
-          const uint32_t sa = base + kc * kAChunk, sb = base + kOffB + s * kStage;
+          const uint64_t da = adesc0 + (uint64_t)((kc * kAChunk) >> 4);
+          const uint64_t dk = kdesc0 + (uint64_t)((s * kStage) >> 4), dv = vdesc0 + (uint64_t)((s * kStage) >> 4);
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk) {
             const uint32_t acc = (kc | kk) ? 1u : 0u;
-            const uint64_t a = sdesc_sw128(sa + kk * 32, 16, 1024);
-            mma_ss_pair(d, a, sdesc_sw128(sb + kk * 32, 16, 1024), kIdescK, acc);
-            mma_ss_pair(d + 128, a, sdesc_sw128(sb + kBHalf + kk * 2048, 8192, 1024), kIdescV, acc);
+            mma_ss_pair(d, da + (uint64_t)((kk * 32) >> 4), dk + (uint64_t)((kk * 32) >> 4), kIdescK, acc);
+            mma_ss_pair(d + 128, da + (uint64_t)((kk * 32) >> 4), dv + (uint64_t)((kk * 2048) >> 4), kIdescV, acc);
           }
           tc_commit_pair(BAR(kBarEmpty + s), 3);
         }
