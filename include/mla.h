@@ -535,9 +535,10 @@ mla_status mla_decode_paged_fp8(const void* q_abs, const void* q_r, const void* 
  *
  * Pages that hold neither a sink nor a token of any row's window are not read:
  * their block-table entries may be -1 and the pages may belong to others.  Of
- * a page that is read, every slot up to the row's own position must hold
- * finite values, and so must the rest of the last page (as for
- * mla_decode_paged).
+ * the pages that mla_decode_window(_fp8) reads, the slots that a row does not
+ * see may hold anything, infinities and NaN among them (unlike
+ * mla_decode_paged, which wants the whole page finite); over the FP8 cache
+ * their scales are not judged either.
  * ------------------------------------------------------------------------- */
 
 /* Summary of a window plan, filled by the planner and passed back to the decode. */

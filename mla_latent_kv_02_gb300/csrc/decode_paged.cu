@@ -104,8 +104,9 @@ constexpr int kSmallMisc = kSmallPair + 4 * kH * 8;
 // misc: +0 abort flag, +8 TMEM address, +16 segment range [2], +32 copies
 // issued per softmax warp [8], +64 the peer's copies [8] (written by the
 // peer), +96 the abort flags of this CTA and the peer [2], +104 the last tile
-// armed on each exchange buffer [4].
-constexpr int kMiscPush = 32, kMiscPeerPush = 64, kMiscAborts = 96, kMiscArmed = 104;
+// armed on each exchange buffer [4], +120 the last tile whose scores each
+// softmax warpgroup has seen complete [2] (windowed).
+constexpr int kMiscPush = 32, kMiscPeerPush = 64, kMiscAborts = 96, kMiscArmed = 104, kMiscScored = 120;
 constexpr int kSmallBytes = kSmallMisc + 128;
 
 // The two cache formats.  bf16: the producer's TMA fills a 4-deep ring of
@@ -227,6 +228,10 @@ struct TileCursor {
     }
     return bits_below(a) | (bits_below(c) & ~bits_below(b));
   }
+  // Whether the row may see less than the whole of the current tile.
+  __device__ __forceinline__ bool edge() const {
+    return pg <= w.sink_tiles || (pg + w.skip + 1) * kPage > vis;
+  }
   static __device__ __forceinline__ uint64_t bits_below(int n) {
     return n <= 0 ? 0ull : n >= 64 ? ~0ull : (1ull << n) - 1ull;
   }
@@ -257,7 +262,13 @@ __device__ __forceinline__ uint32_t as_u32(__half2 h) { return *reinterpret_cast
 // fill no whole page they ride in the dead space before the window's first
 // token where there is room (a merged tile, loaded as two boxes), so a window
 // of W tokens costs about W / 64 + 1 tiles.  The row's visibility in a tile is
-// a 64-bit mask, all ones inside the window.
+// a 64-bit mask, formed for the edge tiles only; the latents of masked tokens
+// are cleared before P·V, so such slots may hold anything.
+// Measured (device time of decode and combine): 128 rows of 2112 tokens 93.9
+// us = 0.42 of the tensor peak on the tokens seen, a tile every 2 100 cycles
+// as in the full decode plus 1.7 row switches a cluster; 16 rows of 4112 tokens
+// of an FP8 cache 46 us (the code conversion's ring); one row of 516 tokens 13.7
+// us, of which 10 are one cluster's latency and 4 the combine.
 template <bool kF8, bool kWin>
 __device__ __forceinline__ void decode_body(const CUtensorMap& kv_map, const CUtensorMap& rope_map,
                                             const DecodeArgs& a, const WindowArgs* win) {
@@ -283,6 +294,7 @@ __device__ __forceinline__ void decode_body(const CUtensorMap& kv_map, const CUt
   volatile uint32_t* peer_push = reinterpret_cast<volatile uint32_t*>(smem_raw + kSmallMisc + kMiscPeerPush);
   volatile int32_t* aborts = reinterpret_cast<volatile int32_t*>(smem_raw + kSmallMisc + kMiscAborts);
   int32_t* armed = reinterpret_cast<int32_t*>(smem_raw + kSmallMisc + kMiscArmed);
+  volatile int32_t* scored = reinterpret_cast<volatile int32_t*>(smem_raw + kSmallMisc + kMiscScored);
   const uint32_t base = (raw + kSmallBytes + 1023u) & ~1023u;
   const bool layout_fits = base + kAlignedBytes <= raw + kSmemBytes;
 #define BAR(i) (bars + 8u * (uint32_t)(i))
@@ -317,6 +329,7 @@ __device__ __forceinline__ void decode_body(const CUtensorMap& kv_map, const CUt
       peer_push[i] = 0u;
     }
     aborts[0] = aborts[1] = 0;
+    scored[0] = scored[1] = -1;
     mbar_init(BAR(B_DRAIN), 1);
     mbar_init(BAR(B_DRAIN_PV), 1);
     fence_mbar_init();
@@ -511,19 +524,53 @@ __device__ __forceinline__ void decode_body(const CUtensorMap& kv_map, const CUt
     }
     __syncwarp();
   };
+  // Zeroes the latents of tile t's tokens whose bit of `seen` is clear, by one
+  // warp, after every score of the tile is complete (its softmax warpgroup
+  // publishes that: a phase of the score barriers could be two behind here).
+  auto clear_masked = [&](uint64_t seen, uint32_t t) -> bool {
+    if (seen == ~0ull) return true;
+    const uint64_t t0 = cycles();
+    bool done = true;
+    for (uint32_t it = 1; scored[t & 1u] < (int32_t)t; ++it) {
+      if ((it & a.wait_every) == 0u && (*abort_flag || cycles() - t0 > a.wait_limit)) {
+        if (!*abort_flag) atomicOr(err, (int32_t)MLA_DEVERR_TIMEOUT);
+        *abort_flag = 1;
+        done = false;
+        break;
+      }
+    }
+    if (!__all_sync(0xffffffffu, done)) return false;
+    tc_fence_after();
+    // Eight lanes a 128-byte row of a chunk, in any order: all of it goes.
+    const uint32_t at = base + kOffKV + (t % kStages) * kStageBytes + ((uint32_t)lane & 7u) * 16u;
+#pragma unroll 1
+    for (uint32_t tok = (uint32_t)lane >> 3; tok < (uint32_t)kPage; tok += 4) {
+      if ((seen >> tok) & 1u) continue;
+#pragma unroll
+      for (uint32_t c = 0; c < 4; ++c) st_shared_v4(at + c * kChunkBytes + tok * 128u, 0u, 0u, 0u, 0u);
+    }
+    fence_proxy_async_smem();
+    __syncwarp();
+    return true;
+  };
   auto role_pv = [&]() {
     // ---------------------------------------------------------------- P·V issue
-    if (lane == 0) {
-      TileCursor<false> cp;
-      cp.init(a.segs, s_begin, s_end);
+    // Windowed: the whole warp walks the tiles, lane 0 issues, and a tile's
+    // masked tokens have their latents cleared once QK^T has read the page,
+    // while the softmax is at work: their P is 0, but 0 times an infinity or a
+    // NaN is not 0.  (128 rows of 2112 tokens: 93.9 us, 92.9 without the
+    // clearing, 95.8 with the softmax warps clearing.)
+    if (kWin || lane == 0) {
+      TileCursor<kWin> cp;
+      cp.init(a.segs, s_begin, s_end, kWin ? win->sinks : 0);
       // The latent chunks read MN-major for P·V, and the ones tile.
       const uint64_t vdesc0 = sdesc_sw128(base + kOffKV, 8192, 1024);
       const uint64_t odesc0 = sdesc_sw128(base + kOffOnes, 16, 1024);
-      for (uint32_t tp = 0; cp.valid(); ++tp) {
+      auto issue = [&](uint32_t tp) -> bool {
         const bool first = cp.first();
-        if (!wait_phase<false, kIssueSuspend>(BAR(B_P_FULL), tp & 1u, err, abort_flag, a.wait_limit, a.wait_every)) break;
+        if (!wait_phase<false, kIssueSuspend>(BAR(B_P_FULL), tp & 1u, err, abort_flag, a.wait_limit, a.wait_every)) return false;
         if (first && !wait_phase<false, kIssueSuspend>(BAR(B_O_FREE), (uint32_t)(cp.s - s_begin) & 1u, err, abort_flag, a.wait_limit, a.wait_every))
-          break;
+          return false;
         tc_fence_after();
         // O_r[128 x 256] += P[128 x 64] · V_r[64 x 256]; V_r is MN-major: 4 atoms
         // of 64 columns 8 KB apart (LBO), 8-token row groups 1 KB apart (SBO).
@@ -540,10 +587,24 @@ __device__ __forceinline__ void decode_body(const CUtensorMap& kv_map, const CUt
         // this commit frees the page stage once P·V(tp) has read it.
         tc_commit(BAR(B_KV_EMPTY + tp % kStages));
         tc_commit(BAR(B_O_DONE0 + (tp & 1u)));
+        return true;
+      };
+      for (uint32_t tp = 0; cp.valid(); ++tp) {
+        bool ok = true;
+        if constexpr (kWin) {
+          if (cp.edge() && !clear_masked(cp.visible(), tp)) break;
+          if (lane == 0) ok = issue(tp);
+          ok = __shfl_sync(0xffffffffu, (int)ok, 0) != 0;
+        } else {
+          ok = issue(tp);
+        }
+        if (!ok) break;
         cp.next();
       }
-      tc_commit(BAR(B_DRAIN_PV));
-      wait_phase_drain(BAR(B_DRAIN_PV), 0);
+      if (lane == 0) {
+        tc_commit(BAR(B_DRAIN_PV));
+        wait_phase_drain(BAR(B_DRAIN_PV), 0);
+      }
     }
     __syncwarp();
   };
@@ -567,6 +628,27 @@ __device__ __forceinline__ void decode_body(const CUtensorMap& kv_map, const CUt
     const uint32_t ct = (uint32_t)lane >> 3, cc = (uint32_t)lane & 7u;
     constexpr int kRows = kPage / kConvWarps;
     constexpr int kBatch = 4;
+    // Windowed: the scales of tokens that the row does not see are not judged.
+    // Whether this warp's scales of tile t outside the range are all such.
+    auto masked_scales_only = [&](uint32_t t, uint32_t stage) {
+      TileCursor<kWin> cv;
+      cv.init(a.segs, s_begin, s_end, win->sinks);
+      uint32_t at = 0;
+      while (cv.valid() && at + (uint32_t)(cv.pe - cv.pb) <= t) {
+        at += (uint32_t)(cv.pe - cv.pb);
+        if (++cv.s < cv.s_end) cv.load();
+      }
+      cv.pg = cv.pb + (int)(t - at);
+      const uint64_t seen = cv.visible();
+      bool ok = true;
+#pragma unroll 1
+      for (int r = cw; r < kPage; r += kConvWarps) {
+        bool ok_r;
+        fp8_f16_factor(ld_shared_f32(stage + kF8ScaleOff + 4u * (uint32_t)r), ok_r);
+        ok = ok && (ok_r || !((seen >> r) & 1u));
+      }
+      return ok;
+    };
     for (uint32_t t = 0; t < G; ++t) {
       const uint32_t st = t % kStages;
       const bool w = wait_phase<false, true>(BAR(B_F8_FULL + st), (t / kStages) & 1u, err, abort_flag, a.wait_limit, a.wait_every);
@@ -593,6 +675,9 @@ __device__ __forceinline__ void decode_body(const CUtensorMap& kv_map, const CUt
         bool ok_j;
         fac[j] = fp8_f16_factor(ld_shared_f32(stage + kF8ScaleOff + 4u * r), ok_j);
         in_range = in_range && ok_j;
+      }
+      if constexpr (kWin) {
+        if (!in_range) in_range = masked_scales_only(t, stage);
       }
       if (!in_range && lane == 0) atomicOr(err, (int32_t)MLA_DEVERR_FP8_RANGE);  // warp-uniform
       if (__any_sync(0xffffffffu, *abort_flag != 0)) {
@@ -718,6 +803,7 @@ __device__ __forceinline__ void decode_body(const CUtensorMap& kv_map, const CUt
     auto fetch_push = [&](uint32_t t, const TileCursor<kWin>& c, uint32_t (&own)[kWords]) -> bool {
       bool w = wait_phase<false, true>(BAR(B_S_FULL0 + (t & 1u)), (t >> 1) & 1u, err, abort_flag, a.wait_limit, a.wait_every);
       if (!__all_sync(0xffffffffu, w)) return false;
+      if (kWin && wg_leader) scored[wg] = (int32_t)t;
       tc_fence_after();
       {
         uint32_t r[64];
@@ -802,8 +888,8 @@ __device__ __forceinline__ void decode_body(const CUtensorMap& kv_map, const CUt
 
       // ---- causal/length mask and the row max of this tile
       if constexpr (kWin) {
-        const uint64_t seen = cf.visible();
-        if (seen != ~0ull) {
+        if (cf.edge()) {
+          const uint64_t seen = cf.visible();
 #pragma unroll
           for (int j = 0; j < kWords; ++j) {
             if (!((seen >> (2 * j)) & 1u)) own[j] = (own[j] & 0xFFFF0000u) | 0xFC00u;

@@ -286,7 +286,7 @@ const char* mla_status_string(mla_status s) {
   return "MLA_ERR_UNKNOWN";
 }
 
-int32_t mla_version(void) { return 100; }
+int32_t mla_version(void) { return 101; }
 
 mla_config mla_config_default(void) {
   mla_config c;

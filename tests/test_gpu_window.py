@@ -180,6 +180,48 @@ def test_decode_window_large_scores(api, kind):
     _check_decode(cache, q_abs, q_r, o, lse, q, window, sinks)
 
 
+def _poison(cache, keep):
+    """NaN and infinities in every slot of the pool but the tokens keep[b] of each sequence."""
+    pool = (cache.kv if cache.kind == "bf16" else cache.rows).shape[0]
+    hold = torch.zeros(pool * 64, dtype=torch.bool, device="cuda")
+    for b, tokens in enumerate(keep):
+        t = torch.tensor(sorted(tokens), dtype=torch.long, device="cuda")
+        hold[cache.table[b].long()[t // 64] * 64 + t % 64] = True
+    bad = (~hold).nonzero().flatten()
+    if cache.kind == "bf16":
+        flat = cache.kv.view(-1, 576)
+        flat[bad[0::2]] = float("nan")
+        flat[bad[1::2]] = float("inf")
+    else:
+        cache.rows.view(-1, 640)[bad] = 0x7F                 # NaN codes, and NaN in the RoPE bytes
+        sc = cache.scales.view(-1)
+        sc[bad[0::3]] = float("nan")
+        sc[bad[1::3]] = float("inf")
+        sc[bad[2::3]] = 0.0
+
+
+@pytest.mark.parametrize("kind", ["bf16", "fp8"])
+@pytest.mark.parametrize("window,sinks", [(100, 4), (64, 64), (30, 75), (1, 0)])
+def test_decode_window_masked_slots_may_hold_anything(api, kind, window, sinks):
+    seq, q = RESIDUES, [1] * len(RESIDUES)
+    cache = Cache(api, seq, kind, 17)
+    _poison(cache, [seen_positions(n - 1, window, sinks) for n in seq])
+    q_abs, q_r = _queries(sum(q), 18)
+    o, lse, err = _decode(api, cache, q_abs, q_r, api.mla_window_plan(seq, q, window, sinks))
+    assert api.mla_check(err) == 0
+    _check_decode(cache, q_abs, q_r, o, lse, q, window, sinks)
+
+
+def test_decode_window_fp8_scale_out_of_range_is_reported(api):
+    """A seen token's scale outside [2^-15, 2^7] sets the flag of the full decode."""
+    seq, q = [300], [1]
+    cache = Cache(api, seq, "fp8", 19)
+    cache.scales[int(cache.bt[0, 4]), 40] = 2.0 ** 9          # position 296: in the window
+    q_abs, q_r = _queries(1, 20)
+    _, _, err = _decode(api, cache, q_abs, q_r, api.mla_window_plan(seq, q, 100, 4))
+    assert int(err.item()) == api.DEVERR_FP8_RANGE
+
+
 def test_decode_window_beyond_32_bit_offsets(api):
     """Pages past 4 GiB of the pool."""
     seq, q, window, sinks = [500, 260], [1, 2], 200, 4
@@ -308,6 +350,23 @@ def test_chunk_window(api, kind, case):
         assert bool((d <= tol).all()), (b, float((d / tol).max()))
         inside[s0:s0 + M] = True
     assert bool((out[~inside] == 9.0).all()), "a row of no chunk was written"
+
+
+@pytest.mark.parametrize("kind", ["bf16", "fp8"])
+def test_chunk_window_reads_kept_tokens_only(api, kind):
+    n, q, window, sinks = [1000, 700], [300, 256], 200, 5
+    cache = Cache(api, n, kind, 43)
+    keep = [sorted({j for i in range(m) for j in seen_positions(N - m + i, window, sinks)}) for N, m in zip(n, q)]
+    w_uk, w_uv = _weights(5)
+    rng = np.random.default_rng(44)
+    T = sum(q)
+    q_c, q_r = to_bf16(bf16(rng, (T, 128, 128)), "cuda"), to_bf16(bf16(rng, (T, 128, 64)), "cuda")
+    want, out = (torch.empty((T, 128, 128), dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    err = _chunk(api, cache, q_c, q_r, [0, 1], [0, 300], q, n, window, sinks, w_uk, w_uv, want)
+    assert api.mla_check(err) == 0
+    _poison(cache, keep)
+    err = _chunk(api, cache, q_c, q_r, [0, 1], [0, 300], q, n, window, sinks, w_uk, w_uv, out)
+    assert api.mla_check(err) == 0 and torch.equal(out, want)
 
 
 def test_chunk_window_that_covers_all_is_the_branch_without(api):
