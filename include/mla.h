@@ -576,10 +576,11 @@ mla_status mla_decode_window_fp8(const void* q_abs, const void* q_r, const void*
                                  size_t ws_bytes, void* o_lat, float* lse, int32_t* dev_err, void* stream);
 
 /* Workspace bytes mla_prefill_window_batch needs: the kept tokens' packed
- * rows, K_c and V_c (as mla_prefill_batch_workspace_size over the kept
- * tokens).  A sequence keeps all n_tokens[i] tokens when no token lies
- * between the sinks and its first row's window, else sinks + window +
- * q_lens[i] - 1.  Host int32 [nb], nb <= 64, 1 <= q_lens[i] <= n_tokens[i]. */
+ * rows, K_c and V_c (as mla_prefill_batch_workspace_size over the kept tokens,
+ * each sequence's starting at a multiple of 128).  A sequence keeps all
+ * n_tokens[i] tokens when no token lies between the sinks and its first row's
+ * window, else sinks + window + q_lens[i] - 1.  Host int32 [nb], nb <= 64,
+ * 1 <= q_lens[i] <= n_tokens[i]; at most 2^24 rows in all. */
 mla_status mla_prefill_window_workspace_size(const int32_t* q_lens, const int32_t* n_tokens, int32_t nb,
                                              int32_t window, int32_t sinks, size_t* bytes);
 
@@ -587,9 +588,10 @@ mla_status mla_prefill_window_workspace_size(const int32_t* q_lens, const int32_
  * mla_prefill_decompress_batch with a sliding window and sinks: the same
  * arguments, buffers and errors, window >= 1 and sinks >= 0.  Only the kept
  * tokens (above) are gathered and expanded; pages that hold none of them may
- * be -1 in the block table.  Every slot of a kept token must hold finite
- * values.  K_c and V_c are held in bf16 (one rounding), as in the branch
- * without a window.
+ * be -1 in the block table.  A row's keys of 128 tokens are multiplied at once,
+ * so the kept tokens of a sequence must hold finite values, those that only
+ * some of its rows see included; another sequence's never touch it.  K_c and
+ * V_c are held in bf16 (one rounding), as in the branch without a window.
  */
 mla_status mla_prefill_window_batch(const void* q_c, const void* q_r, const int32_t* seq_ids, const int32_t* q_starts,
                                     const int32_t* q_lens, const int32_t* n_tokens, int32_t nb, int32_t window,

@@ -8,6 +8,7 @@ library's CUDA kernels.
 from __future__ import annotations
 
 import ctypes as C
+import operator
 from dataclasses import dataclass
 from typing import Optional, Sequence
 
@@ -553,18 +554,27 @@ def mla_decode_paged_fp8(q_abs, q_r, rows, scales, block_table, plan: DecodePlan
 
 
 # ------------------------------------------------------------------ sliding window with sinks
+def _window_args(window, sinks):
+    """window and sinks as C int32 values (the library judges their signs)."""
+    w, s = operator.index(window), operator.index(sinks)
+    if max(abs(w), abs(s)) > 2 ** 31 - 1:
+        raise ValueError(f"window = {w}, sinks = {s}: at most 2^31 - 1")
+    return w, s
+
+
 def mla_window_plan_host(seq_lens: Sequence[int], q_lens: Sequence[int], window: int, sinks: int, num_clusters: int):
     """Host planner of the windowed decode only (no GPU): returns (plan int32 array, info)."""
     sl = np.ascontiguousarray(seq_lens, dtype=np.int32)
     ql = np.ascontiguousarray(q_lens, dtype=np.int32)
     if sl.shape != ql.shape or sl.ndim != 1:
         raise ValueError("seq_lens and q_lens must be lists of the same length")
+    window, sinks = _window_args(window, sinks)
     nbytes = mla_decode_plan_bytes(int(ql.sum()) if ql.size else 0, num_clusters)
     buf = np.zeros(nbytes // 4, dtype=np.int32)
     info = mla_window_info()
     P32 = C.POINTER(C.c_int32)
-    _check(lib().mla_window_plan_host(sl.ctypes.data_as(P32), ql.ctypes.data_as(P32), int(sl.size), int(window),
-                                      int(sinks), int(num_clusters), buf.ctypes.data_as(C.c_void_p), nbytes,
+    _check(lib().mla_window_plan_host(sl.ctypes.data_as(P32), ql.ctypes.data_as(P32), int(sl.size), window,
+                                      sinks, int(num_clusters), buf.ctypes.data_as(C.c_void_p), nbytes,
                                       C.byref(info)))
     return buf, info
 
@@ -640,7 +650,7 @@ def _decode_window(call, cache, pages, q_abs, q_r, block_table, plan, o_lat, dev
     ws_bytes = plan.workspace.numel()
     _check(call(_in(q_abs, "q_abs", torch.bfloat16, (T, H, D_C), dev), _in(q_r, "q_r", torch.bfloat16, (T, H, D_R), dev),
                 *cache, pages, _in(block_table, "block_table", torch.int32, (block_table.shape[0], cols), dev), cols,
-                _in(plan.plan, "plan.plan", torch.int32, (plan.plan.numel(),), dev), plan.info, scale,
+                _in(plan.plan, "plan.plan", torch.int32, (plan.plan.numel(),), dev), plan.info, float(scale),
                 _in(plan.workspace, "plan.workspace", torch.uint8, (ws_bytes,), dev), ws_bytes,
                 _in(o_lat, "o_lat", torch.bfloat16, (T, H, D_C), dev),
                 None if lse is None else _in(lse, "lse", torch.float32, (T, H), dev),
@@ -657,10 +667,11 @@ def _host_i32(*lists):
 
 def mla_prefill_window_workspace_size(q_lens: Sequence[int], n_tokens: Sequence[int], window: int, sinks: int) -> int:
     q, n = _host_i32(q_lens, n_tokens)
+    window, sinks = _window_args(window, sinks)
     out = C.c_size_t()
     P32 = C.POINTER(C.c_int32)
     _check(lib().mla_prefill_window_workspace_size(q.ctypes.data_as(P32), n.ctypes.data_as(P32), int(n.size),
-                                                   int(window), int(sinks), C.byref(out)))
+                                                   window, sinks, C.byref(out)))
     return int(out.value)
 
 
@@ -670,6 +681,7 @@ def _prefill_window(call, cache, pages, q_c, q_r, block_table, seq_ids, q_starts
     if block_table.dim() != 2:
         raise ValueError("block_table must be [sequences, pages]")
     batch, cols = block_table.shape
+    window, sinks = _window_args(window, sinks)
     arrs = _host_i32(seq_ids, q_starts, q_lens, n_tokens)
     if arrs[0].size and int((arrs[1].astype(np.int64) + arrs[2]).max()) > rows:
         raise ValueError("a chunk's rows run past q_c")
@@ -679,7 +691,7 @@ def _prefill_window(call, cache, pages, q_c, q_r, block_table, seq_ids, q_starts
                 *[a.ctypes.data_as(P32) for a in arrs], arrs[0].size, window, sinks, *cache, pages,
                 _in(block_table, "block_table", torch.int32, (batch, cols), dev), batch, cols,
                 _in(w_uk, "w_uk", torch.bfloat16, (H, D_HC, D_C), dev),
-                _in(w_uv, "w_uv", torch.bfloat16, (H, D_C, D_HC), dev), scale,
+                _in(w_uv, "w_uv", torch.bfloat16, (H, D_C, D_HC), dev), float(scale),
                 _in(workspace, "workspace", torch.uint8, (ws_bytes,), dev), ws_bytes,
                 _in(out, "out", torch.bfloat16, (rows, H, D_HC), dev), _in(dev_err, "dev_err", torch.int32, (1,), dev),
                 _on(stream, dev)))

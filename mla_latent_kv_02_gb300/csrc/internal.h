@@ -137,11 +137,12 @@ struct GatherBatch {
 };
 
 // The packed gather of windowed sequences: row j of sequence i comes from
-// position j < cut[i] ? j : j + shift[i].
+// position j < cut[i] ? j : j + shift[i], for j < n[i]; the rows from there to
+// the next sequence's first are zeros.
 struct WindowGather {
   int32_t nb;
   int32_t max_pages;
-  int64_t total;        // Σ n[i]
+  int64_t total;        // rows, the zeros between sequences included
   int64_t num_pages;
   const int32_t* block_table;
   int32_t* dev_err;

@@ -12,7 +12,9 @@
 #include <cstdint>
 #include <cstdio>
 #include <cstring>
+#include <memory>
 #include <mutex>
+#include <new>
 #include <string>
 #include <vector>
 
@@ -942,10 +944,15 @@ mla_status mla_prefill_decompress_batch(const void* q_c, const void* q_r, const 
 }
 
 // The tokens of one sequence that a chunk's window and sinks keep, packed:
-// row j holds position j < cut ? j : j + shift.
+// row j holds position j < cut ? j : j + shift.  A sequence's rows start at a
+// multiple of the attention's 128-token key tiles, after rows of zeros, so that
+// no tile of one sequence holds another's tokens: masked there, a NaN of
+// another sequence would still reach this one's output.
+constexpr int64_t kKeyTile = 128;
 struct KeptTokens {
   int32_t n, cut, shift;
 };
+static int64_t packed_start(int64_t total) { return (total + kKeyTile - 1) / kKeyTile * kKeyTile; }
 static KeptTokens kept_tokens(int32_t M, int32_t N, int32_t window, int32_t sinks) {
   const int64_t lo = (int64_t)N - M + 1 - window;  // the first row's window starts here
   if (lo <= sinks) return {N, N, 0};
@@ -967,7 +974,7 @@ mla_status mla_prefill_window_workspace_size(const int32_t* q_lens, const int32_
   for (int32_t i = 0; i < nb; ++i) {
     if (q_lens[i] < 1 || n_tokens[i] < q_lens[i])
       return fail(MLA_ERR_INVALID_ARG, "sequence %d: q_len %d must be in [1, n_tokens = %d]", i, q_lens[i], n_tokens[i]);
-    total += kept_tokens(q_lens[i], n_tokens[i], window, sinks).n;
+    total = packed_start(total) + kept_tokens(q_lens[i], n_tokens[i], window, sinks).n;
   }
   if (total > (1 << 24)) return fail(MLA_ERR_INVALID_ARG, "%lld kept tokens in all: too many", (long long)total);
   *bytes = prefill_ws_bytes(total);
@@ -1025,6 +1032,7 @@ static mla_status prefill_window(const void* q_c, const void* q_r, const int32_t
       return fail(MLA_ERR_INVALID_ARG, "sequence %d: %d tokens need more than max_pages = %d pages", i, N, max_pages);
     if (q0 < 0) return fail(MLA_ERR_INVALID_ARG, "q_starts[%d] = %d < 0", i, q0);
     const KeptTokens k = kept_tokens(M, N, window, sinks);
+    total = packed_start(total);
     g.b[i] = b;
     g.n[i] = k.n;
     g.cut[i] = k.cut;
@@ -1241,7 +1249,11 @@ mla_status mla_window_plan_host(const int32_t* seq_lens, const int32_t* q_lens, 
   if (!aligned(plan_host, 4)) return fail(MLA_ERR_MISALIGNED, "plan_host is not 4-byte aligned");
   mla_status s = window_check(window, sinks);
   if (s != MLA_OK) return s;
-  s = build_plan(seq_lens, q_lens, B, num_clusters, (int32_t*)plan_host, plan_bytes / 4, &info->plan, window, sinks);
+  try {
+    s = build_plan(seq_lens, q_lens, B, num_clusters, (int32_t*)plan_host, plan_bytes / 4, &info->plan, window, sinks);
+  } catch (const std::bad_alloc&) {
+    return fail(MLA_ERR_NO_SPACE, "out of host memory");
+  }
   if (s != MLA_OK) return s;
   info->window = window;
   info->sinks = sinks;
@@ -1254,12 +1266,22 @@ mla_status mla_window_plan(const int32_t* seq_lens_host, const int32_t* q_lens_h
   CHECK_PTR(plan_dev);
   CHECK_PTR(info);
   CHECK_ALIGN16(plan_dev);
-  std::vector<int32_t> host(plan_bytes / 4 + 1);
-  mla_status s = mla_window_plan_host(seq_lens_host, q_lens_host, B, window, sinks, num_clusters, host.data(),
-                                      plan_bytes, info);
+  if (B < 0) return fail(MLA_ERR_INVALID_ARG, "B = %d is negative", B);
+  if (num_clusters < 1) return fail(MLA_ERR_INVALID_ARG, "num_clusters = %d < 1", num_clusters);
+  if (B > 0) CHECK_PTR(q_lens_host);
+  int64_t T = 0;  // the rows bound what a plan can need, however large the buffer
+  for (int32_t b = 0; b < B; ++b) T += q_lens_host[b] > 0 ? q_lens_host[b] : 0;
+  if (T > INT32_MAX / MLA_NUM_HEADS) return fail(MLA_ERR_INVALID_ARG, "too many query rows");
+  size_t need = 0;
+  mla_status s = mla_decode_plan_bytes((int32_t)T, num_clusters, &need);
+  if (s != MLA_OK) return s;
+  std::unique_ptr<int32_t[]> host(new (std::nothrow) int32_t[std::min(plan_bytes, need) / 4 + 1]);
+  if (!host) return fail(MLA_ERR_NO_SPACE, "out of host memory");
+  s = mla_window_plan_host(seq_lens_host, q_lens_host, B, window, sinks, num_clusters, host.get(),
+                           std::min(plan_bytes, need), info);
   if (s != MLA_OK) return s;
   // Pageable source: the call returns once the data is staged, so `host` may go.
-  cudaError_t e = cudaMemcpyAsync(plan_dev, host.data(), info->plan.plan_bytes, cudaMemcpyHostToDevice,
+  cudaError_t e = cudaMemcpyAsync(plan_dev, host.get(), info->plan.plan_bytes, cudaMemcpyHostToDevice,
                                   (cudaStream_t)stream);
   if (e != cudaSuccess) return cuda_fail(e, "plan copy");
   return MLA_OK;

@@ -2,7 +2,8 @@
 // reads: of each sequence its sinks and the tokens from its first query row's
 // window on, one warp per token, from the bf16 or the FP8 cache to bf16 rows
 // (the FP8 latent as code * 2^k, exact in bf16).  HBM-bound: 1152 or 644
-// bytes read and 1152 written per token kept.
+// bytes read and 1152 written per token kept.  Rows between two sequences are
+// zeros.
 #include <cuda_runtime.h>
 
 #include <cstdint>
@@ -32,6 +33,10 @@ __global__ void __launch_bounds__(kWarps * 32)
       else hi = mid - 1;
     }
     int32_t j = (int32_t)(t - g.off[lo]);
+    if (j >= g.n[lo]) {  // between this sequence's rows and the next one's
+      for (int k = lane; k < kRowVec; k += 32) out[t * kRowVec + k] = make_uint4(0u, 0u, 0u, 0u);
+      continue;
+    }
     if (j >= g.cut[lo]) j += g.shift[lo];
     const int32_t pid = __ldg(g.block_table + (int64_t)g.b[lo] * g.max_pages + j / MLA_PAGE_SIZE);
     if (pid < 0 || (int64_t)pid >= g.num_pages) {

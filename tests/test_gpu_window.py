@@ -280,6 +280,26 @@ def test_decode_window_two_streams_and_a_graph(api):
     _check_decode(cache, q_abs, q_r, o, lse, q, window, sinks)
 
 
+@pytest.mark.parametrize("kind", ["bf16", "fp8"])
+@pytest.mark.parametrize("limit", [64, 5000, 12000])
+def test_decode_window_wait_expiry_is_reported(api, kind, limit):
+    """Waits that run out early, at the set-up or among the tiles: reported, drained, and the next call is right."""
+    seq, q, window, sinks = [700, 900, 333], [2, 1, 2], 257, 6
+    cache = Cache(api, seq, kind, 25)
+    q_abs, q_r = _queries(5, 26)
+    plan = api.mla_window_plan(seq, q, window, sinks, num_clusters=3)
+    try:
+        api.mla_debug_set_decode_wait_limit(limit)
+        _, _, err = _decode(api, cache, q_abs, q_r, plan)
+    finally:
+        api.mla_debug_set_decode_wait_limit(0)
+    torch.cuda.synchronize()
+    assert int(err.item()) in ((api.DEVERR_TIMEOUT,) if limit == 64 else (0, api.DEVERR_TIMEOUT))
+    o, lse, err = _decode(api, cache, q_abs, q_r, plan)
+    assert api.mla_check(err) == 0
+    _check_decode(cache, q_abs, q_r, o, lse, q, window, sinks)
+
+
 def test_decode_window_into_reuses_a_plan(api):
     seq, q = [700, 900], [1, 1]
     cache = Cache(api, seq, "bf16", 31)
@@ -308,9 +328,9 @@ CHUNK_CASES = [
 ]
 
 
-def _chunk(api, cache, q_c, q_r, ids, starts, q, n, window, sinks, w_uk, w_uv, out, stream=None):
+def _chunk(api, cache, q_c, q_r, ids, starts, q, n, window, sinks, w_uk, w_uv, out, stream=None, err=None):
     ws = torch.empty(api.mla_prefill_window_workspace_size(q, n, window, sinks), dtype=torch.uint8, device="cuda")
-    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    err = torch.zeros(1, dtype=torch.int32, device="cuda") if err is None else err
     tail = (cache.table, ids, starts, q, n, window, sinks, w_uk, w_uv, ws, out, err)
     if cache.kind == "bf16":
         api.mla_prefill_window_batch(q_c, q_r, cache.kv, *tail, stream=stream)
@@ -367,6 +387,24 @@ def test_chunk_window_reads_kept_tokens_only(api, kind):
     _poison(cache, keep)
     err = _chunk(api, cache, q_c, q_r, [0, 1], [0, 300], q, n, window, sinks, w_uk, w_uv, out)
     assert api.mla_check(err) == 0 and torch.equal(out, want)
+
+
+def test_chunk_window_keeps_sequences_apart(api):
+    """NaN in one sequence's tokens stays in that sequence."""
+    n, q, window, sinks = [500, 610, 430], [300, 256, 257], 200, 5
+    cache = Cache(api, n, "bf16", 45)
+    w_uk, w_uv = _weights(6)
+    rng = np.random.default_rng(46)
+    T = sum(q)
+    q_c, q_r = to_bf16(bf16(rng, (T, 128, 128)), "cuda"), to_bf16(bf16(rng, (T, 128, 64)), "cuda")
+    want, out = (torch.empty((T, 128, 128), dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    starts = [0, 300, 556]
+    err = _chunk(api, cache, q_c, q_r, [0, 1, 2], starts, q, n, window, sinks, w_uk, w_uv, want)
+    cache.kv[cache.table[1, :10].long()] = float("nan")
+    err = _chunk(api, cache, q_c, q_r, [0, 1, 2], starts, q, n, window, sinks, w_uk, w_uv, out, err=err)
+    assert api.mla_check(err) == 0
+    assert torch.equal(out[:300], want[:300]) and torch.equal(out[556:], want[556:])
+    assert bool(torch.isnan(out[300:556]).all())
 
 
 def test_chunk_window_that_covers_all_is_the_branch_without(api):

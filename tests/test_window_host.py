@@ -107,6 +107,24 @@ def test_window_plan_refusals(api, args):
     assert st == 1
 
 
+def test_window_plan_call_bounds_its_buffers(api):
+    """mla_window_plan: refused before anything is copied, whatever the buffer's size is said to be."""
+    lib = _lib.lib()
+    P32 = C.POINTER(C.c_int32)
+    info = _lib.mla_window_info()
+    sl, ql = np.array([500], np.int32), np.array([600], np.int32)
+
+    def call(dev=0x10000, nbytes=1 << 62, B=1, window=5, sinks=0, clusters=4, q=ql):
+        return lib.mla_window_plan(sl.ctypes.data_as(P32), q.ctypes.data_as(P32), B, window, sinks, clusters,
+                                   C.c_void_p(dev), nbytes, C.byref(info), None)
+
+    assert call() == 1                                       # 600 rows of 500 tokens
+    for kw in [dict(dev=0), dict(dev=0x10008), dict(B=-1), dict(clusters=0)]:
+        assert call(**kw) in (1, 2), kw
+    one = np.array([1], np.int32)
+    assert call(q=one, window=0) == 1 and call(q=one, sinks=-1) == 1 and call(q=one, nbytes=16) == 1
+
+
 def _decode_args(info, kv=0x10000, q=0x20000, o=0x30000, bt=0x40000, plan=0x50000, err=0x60000, ws=0x70000, scale=0.07,
                  pages=10, cols=64):
     return [C.c_void_p(q), C.c_void_p(q), C.c_void_p(kv), pages, C.c_void_p(bt), cols, C.c_void_p(plan), C.byref(info),
@@ -140,13 +158,18 @@ def test_chunk_window_workspace_and_refusals(api):
     per = lambda n: (n * 1152 + 15) // 16 * 16 + 2 * n * 128 * 128 * 2  # noqa: E731
     assert size([300], [1000], 511, 4) == per(4 + 511 + 299)
     assert size([300], [1000], 10000, 4) == per(1000) and size([300], [1000], 1, 701) == per(1000)
-    assert size([300, 1], [1000, 77], 1, 0) == per(300 + 1)
+    assert size([300, 1], [1000, 77], 1, 0) == per(384 + 1)      # a sequence starts at a multiple of 128
     assert size([], [], 1, 0) == 0
     for args in [([0], [5], 1, 0), ([6], [5], 1, 0), ([1], [5], 0, 0), ([1], [5], 1, -1), ([1] * 65, [5] * 65, 1, 0)]:
         with pytest.raises(api.MlaError):
             size(*args)
     with pytest.raises(ValueError):
         size([1, 2], [5], 1, 0)
+    for window, sinks in [(2 ** 32 + 1, 0), (1, 2 ** 31)]:   # not cut to 32 bits
+        with pytest.raises(ValueError):
+            size([1], [5], window, sinks)
+        with pytest.raises(ValueError):
+            api.mla_window_plan_host([5], [1], window, sinks, 4)
     lib = _lib.lib()
     P32 = C.POINTER(C.c_int32)
 
