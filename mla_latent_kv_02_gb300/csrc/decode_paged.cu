@@ -385,6 +385,7 @@ __device__ __forceinline__ void decode_body(const CUtensorMap& kv_map, const CUt
   // arrives here, the softmax warps wait before their first push and the
   // others before the exit barrier, so that the loads start at once.
   cluster_arrive();
+  if (threadIdx.x == 0) grid_launch_dependents();  // the combine's blocks may take their places
   const uint32_t tmem = *tmem_slot;
 
   const int s_begin = seg_range[0];

@@ -120,6 +120,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     tmem_alloc_pair(smem_u32(tmem_slot), 512);
     tmem_relinquish_pair();
   }
+  // The gather before this launch may still run, and a windowed attention
+  // after it may take its places as these blocks leave theirs.
+  if (threadIdx.x == 0) grid_launch_dependents();
+  grid_dependency_wait();
   tc_fence_before();
   __syncthreads();
   cluster_sync();  // both CTAs' barriers exist before any copy or arrival targets them
@@ -305,9 +309,8 @@ cudaError_t launch_expand_kv(const CUtensorMap& a_map, const CUtensorMap& k_map,
   }
   const int64_t units = (int64_t)((n + expand::kTokBlock - 1) / expand::kTokBlock) * 128;
   const int pairs = (int)(units < max_pairs ? units : max_pairs);
-  expand::expand_kv_kernel<<<2 * pairs, expand::kThreads, expand::kSmem, stream>>>(a_map, k_map, v_map, kc_map,
-                                                                                   vc_map, n, err);
-  return cudaGetLastError();
+  return launch_dependent(expand::expand_kv_kernel, dim3(2 * pairs), expand::kThreads, expand::kSmem, true, stream, a_map,
+                          k_map, v_map, kc_map, vc_map, n, err);
 }
 
 }  // namespace mla

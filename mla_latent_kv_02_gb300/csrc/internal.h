@@ -174,6 +174,26 @@ struct WindowArgs {
   int32_t split;                     // window_split(sinks)
 };
 
+// Launches `kern` so that its blocks may take their places while the kernel
+// before it on the stream still runs (programmatic: only if that kernel allows
+// it); every block must call grid_dependency_wait before it reads or writes
+// what that kernel does.
+template <typename... Params, typename... Args>
+cudaError_t launch_dependent(void (*kern)(Params...), dim3 grid, int threads, int smem, bool programmatic,
+                             cudaStream_t stream, Args... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = programmatic ? 1 : 0;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, args...);
+}
+
 int decode_smem_bytes();
 int decode_threads();
 cudaError_t decode_max_clusters(int* out);

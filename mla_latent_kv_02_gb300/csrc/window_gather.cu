@@ -10,6 +10,7 @@
 
 #include "fp8.cuh"
 #include "internal.h"
+#include "ptx.cuh"
 
 namespace mla {
 namespace wgather {
@@ -23,6 +24,7 @@ template <bool kF8>
 __global__ void __launch_bounds__(kWarps * 32)
     gather_window_kernel(const uint8_t* __restrict__ cache, const float* __restrict__ scales,
                          const __grid_constant__ WindowGather g, uint4* __restrict__ out) {
+  if (threadIdx.x == 0) grid_launch_dependents();  // the expansion sets itself up meanwhile
   const int lane = threadIdx.x & 31;
   for (int64_t t = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5); t < g.total;
        t += (int64_t)gridDim.x * kWarps) {
