@@ -139,7 +139,7 @@ __device__ __forceinline__ void prefill_body(const CUtensorMap& q_map, const CUt
     skip = max(first - sink_tiles, 0);
     n_tiles -= skip;
   }
-  auto key_tile = [&](int j) { return kWin && j >= sink_tiles ? j + skip : j; };
+  auto key_tile = [=](int j) { if constexpr (kWin) return j >= sink_tiles ? j + skip : j; else return j; };
   int32_t* err = a.dev_err;
 
   if (threadIdx.x == 0) {
@@ -478,31 +478,51 @@ __device__ __forceinline__ void prefill_body(const CUtensorMap& q_map, const CUt
       if (__all_sync(0xffffffffu, w)) {
         tc_fence_after();
         const float inv = 1.f / (xsum[r] + xsum[128 + r]);
-        // Output rows lie 32 KB apart: the warp's 32 half rows of 128 bytes
-        // cross through its 4 KB of the V ring (every P·V has read it), so that
-        // a store covers four whole lines instead of 32 pieces of 16 bytes.
-        const uint32_t box = base + kOffV + (uint32_t)(warp - kSoftWarp0) * 4096u;
+        if constexpr (kWin) {
+          // Output rows lie 32 KB apart: the warp's 32 half rows of 128 bytes
+          // cross through its 4 KB of the V ring (every P·V has read it), so that
+          // a store covers four whole lines instead of 32 pieces of 16 bytes: 1 %
+          // for a 300-row chunk of six tiles, but slower (524 -> 531 us) for the
+          // 130 tiles of the form without a window, which stores directly.
+          const uint32_t box = base + kOffV + (uint32_t)(warp - kSoftWarp0) * 4096u;
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          uint32_t o[32];
-          tmem_ld32_sync(tl + kColO + 64 * half + 32 * c, o);
+          for (int c = 0; c < 2; ++c) {
+            uint32_t o[32];
+            tmem_ld32_sync(tl + kColO + 64 * half + 32 * c, o);
 #pragma unroll
-          for (int v = 0; v < 4; ++v)
-            st_shared_v4(box + (uint32_t)lane * 128u + ((((uint32_t)(4 * c + v)) ^ ((uint32_t)lane & 7u)) << 4),
-                         pack_bf16x2(__uint_as_float(o[8 * v + 0]) * inv, __uint_as_float(o[8 * v + 1]) * inv),
-                         pack_bf16x2(__uint_as_float(o[8 * v + 2]) * inv, __uint_as_float(o[8 * v + 3]) * inv),
-                         pack_bf16x2(__uint_as_float(o[8 * v + 4]) * inv, __uint_as_float(o[8 * v + 5]) * inv),
-                         pack_bf16x2(__uint_as_float(o[8 * v + 6]) * inv, __uint_as_float(o[8 * v + 7]) * inv));
-        }
-        __syncwarp();
-        const uint32_t piece = (uint32_t)lane & 7u;
+            for (int v = 0; v < 4; ++v)
+              st_shared_v4(box + (uint32_t)lane * 128u + ((((uint32_t)(4 * c + v)) ^ ((uint32_t)lane & 7u)) << 4),
+                           pack_bf16x2(__uint_as_float(o[8 * v + 0]) * inv, __uint_as_float(o[8 * v + 1]) * inv),
+                           pack_bf16x2(__uint_as_float(o[8 * v + 2]) * inv, __uint_as_float(o[8 * v + 3]) * inv),
+                           pack_bf16x2(__uint_as_float(o[8 * v + 4]) * inv, __uint_as_float(o[8 * v + 5]) * inv),
+                           pack_bf16x2(__uint_as_float(o[8 * v + 6]) * inv, __uint_as_float(o[8 * v + 7]) * inv));
+          }
+          __syncwarp();
+          const uint32_t piece = (uint32_t)lane & 7u;
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const uint32_t row = 4u * (uint32_t)k + ((uint32_t)lane >> 3);
-          const int ir = i0 + q4 * 32 + (int)row;
-          if (ir < M)
-            *reinterpret_cast<float4*>(a.out + ((size_t)(sq.q_off + ir) * 128 + h) * 128 + 64 * half + piece * 8) =
-                ld_shared_v4(box + row * 128u + ((piece ^ (row & 7u)) << 4));
+          for (int k = 0; k < 8; ++k) {
+            const uint32_t row = 4u * (uint32_t)k + ((uint32_t)lane >> 3);
+            const int ir = i0 + q4 * 32 + (int)row;
+            if (ir < M)
+              *reinterpret_cast<float4*>(a.out + ((size_t)(sq.q_off + ir) * 128 + h) * 128 + 64 * half + piece * 8) =
+                  ld_shared_v4(box + row * 128u + ((piece ^ (row & 7u)) << 4));
+          }
+        } else {
+          uint4* dst = reinterpret_cast<uint4*>(a.out + ((size_t)(sq.q_off + min(i, M - 1)) * 128 + h) * 128);
+#pragma unroll 1
+          for (int c = 64 * half; c < 64 * half + 64; c += 32) {
+            uint32_t o[32];
+            tmem_ld32_sync(tl + kColO + c, o);
+            if (i < M) {
+#pragma unroll
+              for (int v = 0; v < 4; ++v)
+                dst[c / 8 + v] = make_uint4(
+                    pack_bf16x2(__uint_as_float(o[8 * v + 0]) * inv, __uint_as_float(o[8 * v + 1]) * inv),
+                    pack_bf16x2(__uint_as_float(o[8 * v + 2]) * inv, __uint_as_float(o[8 * v + 3]) * inv),
+                    pack_bf16x2(__uint_as_float(o[8 * v + 4]) * inv, __uint_as_float(o[8 * v + 5]) * inv),
+                    pack_bf16x2(__uint_as_float(o[8 * v + 6]) * inv, __uint_as_float(o[8 * v + 7]) * inv));
+            }
+          }
         }
       }
     }
