@@ -230,7 +230,7 @@ struct TileCursor {
   }
   // Whether the row may see less than the whole of the current tile.
   __device__ __forceinline__ bool edge() const {
-    return pg <= w.sink_tiles || (pg + w.skip + 1) * kPage > vis;
+    return pg <= w.sink_tiles || vis - (pg + w.skip) * kPage < kPage;
   }
   static __device__ __forceinline__ uint64_t bits_below(int n) {
     return n <= 0 ? 0ull : n >= 64 ? ~0ull : (1ull << n) - 1ull;

@@ -1057,8 +1057,8 @@ static mla_status prefill_window(const void* q_c, const void* q_r, const int32_t
   a.scale_log2 = (float)((double)scale * 1.4426950408889634);
   a.out = (uint16_t*)out;
   a.dev_err = dev_err;
-  a.window = window;
-  a.sinks = sinks;
+  a.window = std::min(window, 1 << 25);  // past the kept tokens (at most 2^24) a window is all the same; positions minus it stay in 32 bits
+  a.sinks = std::min(sinks, 1 << 25);
   uint8_t* rows = (uint8_t*)workspace;
   uint8_t* k_c = rows + prefill_rows_bytes(total);
   uint8_t* v_c = k_c + (size_t)total * MLA_NUM_HEADS * MLA_HEAD_DIM_C * 2;

@@ -238,6 +238,31 @@ def test_decode_window_beyond_32_bit_offsets(api):
     _check_decode(small, q_abs, q_r, o, lse, q, window, sinks)
 
 
+@pytest.mark.parametrize("n", [2 ** 31 - 1, 2 ** 31 - 63])
+def test_decode_window_of_the_longest_sequence(api, n):
+    """A sequence of 2^31 - 1 positions whose table maps the pages it sees only."""
+    window, sinks = 100, 4
+    first = n - window                                       # the window's first token
+    pages = [0] + list(range(first // 64, (n - 1) // 64 + 1))
+    cols = (n - 1) // 64 + 1
+    table = torch.full((1, cols), -1, dtype=torch.int32, device="cuda")
+    table[0, torch.tensor(pages, device="cuda")] = torch.arange(len(pages), dtype=torch.int32, device="cuda")
+    rng = np.random.default_rng(3)
+    c, r = bf16(rng, (len(pages) * 64, 512)), bf16(rng, (len(pages) * 64, 64))
+    kv = torch.cat([to_bf16(c, "cuda"), to_bf16(r, "cuda")], dim=1).view(len(pages), 64, 576).contiguous()
+    q_abs, q_r = _queries(1, 4)
+    plan = api.mla_window_plan([n], [1], window, sinks)
+    o = torch.empty((1, 128, 512), dtype=torch.bfloat16, device="cuda")
+    lse = torch.empty((1, 128), dtype=torch.float32, device="cuda")
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    api.mla_decode_window(q_abs, q_r, kv, table, plan, o, err, lse=lse)
+    assert api.mla_check(err) == 0
+    at = list(range(sinks)) + [64 * pages.index(j // 64) + j % 64 for j in range(first, n)]
+    wo, wl_, to, tl = decode_row(q_abs[0].double(), q_r[0].double(), torch.from_numpy(c[at].astype(np.float64)).cuda(),
+                                 torch.from_numpy(r[at].astype(np.float64)).cuda())
+    assert bool(((o[0].double() - wo).abs() <= to).all()) and bool(((lse[0].double() - wl_).abs() <= tl).all())
+
+
 def test_decode_window_bad_pages_are_reported(api):
     seq, q, window, sinks = [1000], [1], 200, 4
     cache = Cache(api, seq, "bf16", 14)
