@@ -727,14 +727,14 @@ def mla_pack_w4(w, group: int, stream=None):
     with a bf16 scale per group of the contraction (dim 1); returns (words, scales)."""
     if not isinstance(w, torch.Tensor) or w.dim() != 3:
         raise TypeError("w must be a torch.Tensor [128, K, N]")
-    K, N = w.shape[1], w.shape[2]
-    _need(w, "w", torch.bfloat16, (H, K, N))
-    if group < 8:
+    K, N, group = w.shape[1], w.shape[2], operator.index(group)
+    if not 8 <= group <= D_C:  # beyond 32 bits another size would reach the library
         raise ValueError(f"group = {group}: 32, 64 and 128 are supported")
+    addr = _in(w, "w", torch.bfloat16, (H, K, N), torch.cuda.current_device())
     with torch.cuda.stream(stream):
         words = torch.empty((H, K // 8, N), dtype=torch.int32, device=w.device)
         scales = torch.empty((H, max(K // group, 1), N), dtype=torch.bfloat16, device=w.device)
-    _check(lib().mla_pack_w4(_ptr(w), int(K), int(N), int(group), _ptr(words), _ptr(scales), _stream(stream)))
+    _check(lib().mla_pack_w4(addr, K, N, group, _ptr(words), _ptr(scales), _stream(stream)))
     return words, scales
 
 

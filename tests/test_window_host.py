@@ -220,3 +220,13 @@ def test_w4_refusals(api):
     assert lib.mla_pack_w4(p, 128, 128, 64, p, p, None) == 3 and lib.mla_pack_w4(p, 128, 512, 48, p, p, None) == 3
     assert lib.mla_pack_w4(None, 128, 512, 64, p, p, None) == 1
     assert lib.mla_pack_w4(p, 512, 128, 64, C.c_void_p(0x10004), p, None) == 2
+
+
+def test_pack_w4_group_is_not_cut_to_32_bits(api):
+    torch = pytest.importorskip("torch")
+    w = torch.zeros((128, 128, 512), dtype=torch.bfloat16)
+    for group in (2 ** 32 + 32, 2 ** 33 + 64, -(2 ** 32) + 64, 0, 1024):
+        with pytest.raises(ValueError, match="group"):
+            api.mla_pack_w4(w, group)
+    with pytest.raises(TypeError):
+        api.mla_pack_w4(w, 64.0)
