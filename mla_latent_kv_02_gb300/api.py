@@ -554,6 +554,20 @@ def mla_decode_paged_fp8(q_abs, q_r, rows, scales, block_table, plan: DecodePlan
 
 
 # ------------------------------------------------------------------ sliding window with sinks
+def _host_i32(*lists):
+    """Host lists of sequences as int32 arrays of one length."""
+    arrs = []
+    for x in lists:
+        v = np.asarray(x)
+        a = np.ascontiguousarray(v, dtype=np.int32)
+        if v.ndim != 1 or (a != v).any():
+            raise ValueError("the sequences' lists must be one-dimensional, of values that int32 holds")
+        arrs.append(a)
+    if any(a.size != arrs[0].size for a in arrs):
+        raise ValueError("the sequences' lists must have the same length")
+    return arrs
+
+
 def _window_args(window, sinks):
     """window and sinks as C int32 values (the library judges their signs)."""
     w, s = operator.index(window), operator.index(sinks)
@@ -564,10 +578,7 @@ def _window_args(window, sinks):
 
 def mla_window_plan_host(seq_lens: Sequence[int], q_lens: Sequence[int], window: int, sinks: int, num_clusters: int):
     """Host planner of the windowed decode only (no GPU): returns (plan int32 array, info)."""
-    sl = np.ascontiguousarray(seq_lens, dtype=np.int32)
-    ql = np.ascontiguousarray(q_lens, dtype=np.int32)
-    if sl.shape != ql.shape or sl.ndim != 1:
-        raise ValueError("seq_lens and q_lens must be lists of the same length")
+    sl, ql = _host_i32(seq_lens, q_lens)
     window, sinks = _window_args(window, sinks)
     nbytes = mla_decode_plan_bytes(int(ql.sum()) if ql.size else 0, num_clusters)
     buf = np.zeros(nbytes // 4, dtype=np.int32)
@@ -655,14 +666,6 @@ def _decode_window(call, cache, pages, q_abs, q_r, block_table, plan, o_lat, dev
                 _in(o_lat, "o_lat", torch.bfloat16, (T, H, D_C), dev),
                 None if lse is None else _in(lse, "lse", torch.float32, (T, H), dev),
                 _in(dev_err, "dev_err", torch.int32, (1,), dev), _on(stream, dev)))
-
-
-def _host_i32(*lists):
-    """The host lists as int32 arrays of one length."""
-    arrs = [np.ascontiguousarray(x, dtype=np.int32) for x in lists]
-    if any(a.ndim != 1 or a.size != arrs[0].size for a in arrs):
-        raise ValueError("the sequences' lists must have the same length")
-    return arrs
 
 
 def mla_prefill_window_workspace_size(q_lens: Sequence[int], n_tokens: Sequence[int], window: int, sinks: int) -> int:

@@ -230,3 +230,14 @@ def test_pack_w4_group_is_not_cut_to_32_bits(api):
             api.mla_pack_w4(w, group)
     with pytest.raises(TypeError):
         api.mla_pack_w4(w, 64.0)
+
+
+def test_sequence_lists_are_not_cut_to_32_bits(api):
+    far = np.array([2 ** 32 + 500])                          # int32 would wrap to 500
+    for lists in [(far, [1]), ([500], far), ([500.5], [1]), ([[500]], [[1]]), (500, 1)]:
+        with pytest.raises(ValueError):
+            api.mla_window_plan_host(*lists, 100, 4, 4)
+        with pytest.raises(ValueError):
+            api.mla_prefill_window_workspace_size(lists[1], lists[0], 100, 4)
+    assert api.mla_prefill_window_workspace_size(np.array([1]), (500,), 600, 0) == 500 * 1152 + 2 * 500 * 128 * 128 * 2
+    assert api.mla_window_plan_host([], [], 100, 4, 4)[1].plan.T == 0
