@@ -283,7 +283,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 
 cudaError_t launch_expand_kv(const CUtensorMap& a_map, const CUtensorMap& k_map, const CUtensorMap& v_map,
                              const CUtensorMap& kc_map, const CUtensorMap& vc_map, int32_t n, int32_t* err,
-                             cudaStream_t stream) {
+                             bool early, cudaStream_t stream) {
   if (n <= 0) return cudaSuccess;
   cudaError_t e = cudaFuncSetAttribute(expand::expand_kv_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        expand::kSmem);
@@ -309,7 +309,7 @@ cudaError_t launch_expand_kv(const CUtensorMap& a_map, const CUtensorMap& k_map,
   }
   const int64_t units = (int64_t)((n + expand::kTokBlock - 1) / expand::kTokBlock) * 128;
   const int pairs = (int)(units < max_pairs ? units : max_pairs);
-  return launch_dependent(expand::expand_kv_kernel, dim3(2 * pairs), expand::kThreads, expand::kSmem, true, stream, a_map,
+  return launch_dependent(expand::expand_kv_kernel, dim3(2 * pairs), expand::kThreads, expand::kSmem, early, stream, a_map,
                           k_map, v_map, kc_map, vc_map, n, err);
 }
 

@@ -245,9 +245,10 @@ cudaError_t launch_gather_window(const void* cache, const float* scales, bool fp
                                  uint16_t* out, cudaStream_t stream);
 
 // Decompress-branch expansion: K_c and V_c in one pass (head-major outputs).
+// early: it may start while the kernel before it on the stream still runs.
 cudaError_t launch_expand_kv(const CUtensorMap& a_map, const CUtensorMap& k_map, const CUtensorMap& v_map,
                              const CUtensorMap& kc_map, const CUtensorMap& vc_map, int32_t n, int32_t* err,
-                             cudaStream_t stream);
+                             bool early, cudaStream_t stream);
 int prefill_smem_bytes();
 cudaError_t launch_prefill_attn(const CUtensorMap& q_map, const CUtensorMap& r_map, const CUtensorMap& k_map,
                                 const CUtensorMap& kr_map, const CUtensorMap& v_map, const PrefillArgs& args,

@@ -737,8 +737,8 @@ int32_t mla_prefill_threshold(void) { return MLA_PREFILL_THRESHOLD; }
 
 int32_t mla_branch_for(int32_t q_len) { return q_len >= MLA_PREFILL_THRESHOLD ? MLA_BRANCH_DECOMPRESS : MLA_BRANCH_ABSORB; }
 
-mla_status mla_expand_kv(const void* rows, int32_t n, const void* w_uk, const void* w_uv, void* k_c, void* v_c,
-                         int32_t* dev_err, void* stream) {
+static mla_status expand_kv(const void* rows, int32_t n, const void* w_uk, const void* w_uv, void* k_c, void* v_c,
+                            int32_t* dev_err, bool early, void* stream) {
   if (n < 0) return fail(MLA_ERR_INVALID_ARG, "n = %d < 0", n);
   if (n == 0) return MLA_OK;
   CHECK_PTR(rows);
@@ -782,9 +782,14 @@ mla_status mla_expand_kv(const void* rows, int32_t n, const void* w_uk, const vo
   if (s != MLA_OK) return s;
   s = make_map(&vcmap, v_c, 3, odims, ostr, obox, "V_c");
   if (s != MLA_OK) return s;
-  cudaError_t e = mla::launch_expand_kv(amap, kmap, vmap, kcmap, vcmap, n, dev_err, (cudaStream_t)stream);
+  cudaError_t e = mla::launch_expand_kv(amap, kmap, vmap, kcmap, vcmap, n, dev_err, early, (cudaStream_t)stream);
   if (e != cudaSuccess) return cuda_fail(e, "expand_kv launch");
   return MLA_OK;
+}
+
+mla_status mla_expand_kv(const void* rows, int32_t n, const void* w_uk, const void* w_uv, void* k_c, void* v_c,
+                         int32_t* dev_err, void* stream) {
+  return expand_kv(rows, n, w_uk, w_uv, k_c, v_c, dev_err, false, stream);
 }
 
 // Tensor maps over the packed arrays of a batch (T rows of queries, N cached
@@ -1064,7 +1069,7 @@ static mla_status prefill_window(const void* q_c, const void* q_r, const int32_t
   uint8_t* v_c = k_c + (size_t)total * MLA_NUM_HEADS * MLA_HEAD_DIM_C * 2;
   cudaError_t e = mla::launch_gather_window(cache, scales, fp8, g, (uint16_t*)rows, (cudaStream_t)stream);
   if (e != cudaSuccess) return cuda_fail(e, "window gather launch");
-  s = mla_expand_kv(rows, (int32_t)total, w_uk, w_uv, k_c, v_c, dev_err, stream);
+  s = expand_kv(rows, (int32_t)total, w_uk, w_uv, k_c, v_c, dev_err, true, stream);
   if (s != MLA_OK) return s;
   return prefill_attention_launch(q_c, q_r, rows_end, rows, k_c, v_c, total, a, stream);
 }
