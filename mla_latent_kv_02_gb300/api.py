@@ -9,7 +9,7 @@ from __future__ import annotations
 
 import ctypes as C
 import operator
-from dataclasses import dataclass
+from dataclasses import dataclass, field, replace
 from typing import Optional, Sequence
 
 import numpy as np
@@ -448,19 +448,57 @@ class DecodePlan:
     info: mla_plan_info
     workspace: torch.Tensor     # uint8 device buffer
     host: Optional[torch.Tensor] = None   # pinned int32 staging of the plan (reused by `into=`)
+    streams: set = field(default_factory=set, repr=False, compare=False)  # raw handles of the streams that use the buffers
 
     @property
     def num_clusters(self) -> int:
         return int(self.info.num_clusters)
 
 
+def _use(plan, stream, dev: int) -> int:
+    """The raw handle of the stream that a call reads or writes a plan's buffers
+    on.  The allocator learns of every such stream: a plan may be dropped as soon
+    as its last call is queued, and its blocks are handed out again only after
+    the work queued there."""
+    raw = _on(stream, dev)
+    if raw not in plan.streams:
+        if stream is None:
+            on = torch.cuda.current_stream(dev)
+        elif isinstance(stream, torch.cuda.Stream):
+            on = stream
+        else:  # any object with a `cuda_stream`
+            on = torch.cuda.ExternalStream(raw, device=dev) if raw else torch.cuda.default_stream(dev)
+        plan.plan.record_stream(on)
+        plan.workspace.record_stream(on)
+        plan.streams.add(raw)
+    return raw
+
+
+def _plan_buffers(cls, words: int, ws_bytes: int, device):
+    """A plan without contents.  The blocks are those of the stream that is
+    current, the one that uploads: a block that work queued on another stream
+    still uses is never overwritten by the upload."""
+    plan = torch.empty(words, dtype=torch.int32, device=device)
+    ws = torch.empty(ws_bytes, dtype=torch.uint8, device=device)
+    host = torch.zeros(words, dtype=torch.int32).pin_memory()
+    return cls(plan=plan, info=None, workspace=ws, host=host, streams={_on(None, plan.get_device())})
+
+
+def _upload(plan, words: int, stream) -> None:
+    with torch.cuda.stream(stream):
+        _use(plan, None, plan.plan.get_device())
+        plan.plan[:words].copy_(plan.host[:words], non_blocking=True)
+
+
 def mla_decode_plan(seq_lens: Sequence[int], q_lens: Sequence[int], device=None, num_clusters: Optional[int] = None,
                     stream=None, into: Optional[DecodePlan] = None) -> DecodePlan:
     """Plan on the host into a pinned buffer and upload it with an
     asynchronous copy on `stream` (a copy from pageable memory would make
-    the host wait for the stream).  `into` reuses a previous plan's buffers
-    when they are large enough; the caller must not reuse a plan whose
-    previous upload or decode may still be running."""
+    the host wait for the stream).  A decode on another stream has to wait
+    for the upload (an event); the plan may be dropped once its last decode is
+    queued.  `into` reuses a previous plan's buffers when they are large
+    enough; the caller must not reuse a plan whose previous upload or decode
+    may still be running."""
     sl = np.ascontiguousarray(seq_lens, dtype=np.int32)
     ql = np.ascontiguousarray(q_lens, dtype=np.int32)
     T = int(ql.sum()) if ql.size else 0
@@ -472,21 +510,16 @@ def mla_decode_plan(seq_lens: Sequence[int], q_lens: Sequence[int], device=None,
     ws_bytes = max(mla_decode_workspace_size(num_clusters), 16)
     if (into is not None and into.host is not None and into.plan.numel() >= words
             and into.workspace.numel() >= ws_bytes and into.plan.device == torch.device(device)):
-        plan, ws, host = into.plan, into.workspace, into.host
-    else:
-        plan = torch.empty(words, dtype=torch.int32, device=device)
-        ws = torch.empty(ws_bytes, dtype=torch.uint8, device=device)
-        host = torch.zeros(words, dtype=torch.int32).pin_memory()
-    info = mla_plan_info()
-    P32 = C.POINTER(C.c_int32)
-    _check(lib().mla_decode_plan_host(sl.ctypes.data_as(P32), ql.ctypes.data_as(P32), int(sl.size),
-                                      int(num_clusters), C.c_void_p(host.data_ptr()), nbytes, C.byref(info)))
-    if stream is None:
-        plan[:words].copy_(host[:words], non_blocking=True)
+        plan = replace(into)
     else:
         with torch.cuda.stream(stream):
-            plan[:words].copy_(host[:words], non_blocking=True)
-    return DecodePlan(plan=plan, info=info, workspace=ws, host=host)
+            plan = _plan_buffers(DecodePlan, words, ws_bytes, device)
+    plan.info = mla_plan_info()
+    P32 = C.POINTER(C.c_int32)
+    _check(lib().mla_decode_plan_host(sl.ctypes.data_as(P32), ql.ctypes.data_as(P32), int(sl.size),
+                                      int(num_clusters), C.c_void_p(plan.host.data_ptr()), nbytes, C.byref(plan.info)))
+    _upload(plan, words, stream)
+    return plan
 
 
 def plan_rows(plan: DecodePlan) -> dict:
@@ -529,7 +562,7 @@ def mla_decode_paged(q_abs, q_r, kv_cache, block_table, plan: DecodePlan, o_lat,
     _check(lib().mla_decode_paged(_ptr(q_abs), _ptr(q_r), _ptr(kv_cache), kv_cache.shape[0], _ptr(block_table),
                                   block_table.shape[1], _ptr(plan.plan), C.byref(plan.info), float(scale),
                                   _ptr(plan.workspace), plan.workspace.numel(), _ptr(o_lat), _ptr(lse),
-                                  _ptr(dev_err), _stream(stream)))
+                                  _ptr(dev_err), _use(plan, stream, torch.cuda.current_device())))
 
 
 def mla_decode_paged_fp8(q_abs, q_r, rows, scales, block_table, plan: DecodePlan, o_lat, dev_err, lse=None,
@@ -550,7 +583,7 @@ def mla_decode_paged_fp8(q_abs, q_r, rows, scales, block_table, plan: DecodePlan
     _check(lib().mla_decode_paged_fp8(_ptr(q_abs), _ptr(q_r), _ptr(rows), _ptr(scales), rows.shape[0],
                                       _ptr(block_table), block_table.shape[1], _ptr(plan.plan), C.byref(plan.info),
                                       float(scale), _ptr(plan.workspace), plan.workspace.numel(), _ptr(o_lat),
-                                      _ptr(lse), _ptr(dev_err), _stream(stream)))
+                                      _ptr(lse), _ptr(dev_err), _use(plan, stream, torch.cuda.current_device())))
 
 
 # ------------------------------------------------------------------ sliding window with sinks
@@ -597,6 +630,7 @@ class WindowPlan:
     info: mla_window_info
     workspace: torch.Tensor     # uint8 device buffer
     host: torch.Tensor          # pinned int32 staging of the plan (reused by `into=`)
+    streams: set = field(default_factory=set, repr=False, compare=False)  # raw handles of the streams that use the buffers
 
     @property
     def num_clusters(self) -> int:
@@ -606,9 +640,11 @@ class WindowPlan:
 def mla_window_plan(seq_lens: Sequence[int], q_lens: Sequence[int], window: int, sinks: int, device=None,
                     num_clusters: Optional[int] = None, stream=None, into: Optional[WindowPlan] = None) -> WindowPlan:
     """mla_decode_plan for a sliding window with sinks: one plan serves every
-    layer of a step.  A plan holds one workspace, so decodes that share it must
-    not overlap on the GPU; `into` reuses a previous plan's buffers when they
-    are large enough and nothing that reads them may still be running."""
+    layer of a step.  The upload runs on `stream`; a decode on another stream has
+    to wait for it (an event), and the plan may be dropped once its last decode
+    is queued.  A plan holds one workspace, so decodes that share it must not
+    overlap on the GPU; `into` reuses a previous plan's buffers when they are
+    large enough and nothing that reads them may still be running."""
     if num_clusters is None:
         num_clusters = mla_decode_max_clusters()
     buf, info = mla_window_plan_host(seq_lens, q_lens, window, sinks, num_clusters)
@@ -617,15 +653,14 @@ def mla_window_plan(seq_lens: Sequence[int], q_lens: Sequence[int], window: int,
     ws_bytes = max(mla_decode_workspace_size(num_clusters), 16)
     if (into is not None and into.plan.numel() >= words and into.workspace.numel() >= ws_bytes
             and into.plan.device == device):
-        plan, ws, host = into.plan, into.workspace, into.host
+        plan = replace(into)
     else:
-        plan = torch.empty(words, dtype=torch.int32, device=device)
-        ws = torch.empty(ws_bytes, dtype=torch.uint8, device=device)
-        host = torch.zeros(words, dtype=torch.int32).pin_memory()
-    host[:buf.size] = torch.from_numpy(buf)
-    with torch.cuda.stream(stream):
-        plan[:words].copy_(host[:words], non_blocking=True)
-    return WindowPlan(plan=plan, info=info, workspace=ws, host=host)
+        with torch.cuda.stream(stream):
+            plan = _plan_buffers(WindowPlan, words, ws_bytes, device)
+    plan.info = info
+    plan.host[:buf.size] = torch.from_numpy(buf)
+    _upload(plan, words, stream)
+    return plan
 
 
 def mla_decode_window(q_abs, q_r, kv_cache, block_table, plan: WindowPlan, o_lat, dev_err, lse=None,
@@ -665,7 +700,7 @@ def _decode_window(call, cache, pages, q_abs, q_r, block_table, plan, o_lat, dev
                 _in(plan.workspace, "plan.workspace", torch.uint8, (ws_bytes,), dev), ws_bytes,
                 _in(o_lat, "o_lat", torch.bfloat16, (T, H, D_C), dev),
                 None if lse is None else _in(lse, "lse", torch.float32, (T, H), dev),
-                _in(dev_err, "dev_err", torch.int32, (1,), dev), _on(stream, dev)))
+                _in(dev_err, "dev_err", torch.int32, (1,), dev), _use(plan, stream, dev)))
 
 
 def mla_prefill_window_workspace_size(q_lens: Sequence[int], n_tokens: Sequence[int], window: int, sinks: int) -> int:
