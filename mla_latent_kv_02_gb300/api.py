@@ -61,7 +61,11 @@ def _need(t: torch.Tensor, name: str, dtype, shape=None, cuda: bool = True):
 
 
 _Tensor = torch.Tensor
-_raw_stream = torch._C._cuda_getCurrentRawStream
+
+
+def _raw_stream(dev: int) -> int:
+    # looked up at a call: a PyTorch without CUDA lacks the name, and the host-only calls serve there too
+    return torch._C._cuda_getCurrentRawStream(dev)
 
 
 def _in(t, name: str, dtype, shape, dev: int) -> int:
