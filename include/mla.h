@@ -237,7 +237,9 @@ mla_status mla_decode_plan_host(const int32_t* seq_lens, const int32_t* q_lens, 
                                 int32_t num_clusters, void* plan_host, size_t plan_bytes,
                                 mla_plan_info* info);
 
-/* As mla_decode_plan_host, then copies the plan to plan_dev on `stream`. */
+/* As mla_decode_plan_host, then copies the plan to plan_dev on `stream`.  A
+ * stream that is being captured is MLA_ERR_UNSUPPORTED: the copy's source does
+ * not outlive the call. */
 mla_status mla_decode_plan(const int32_t* seq_lens_host, const int32_t* q_lens_host, int32_t B,
                            int32_t num_clusters, void* plan_dev, size_t plan_bytes,
                            mla_plan_info* info, void* stream);
@@ -560,7 +562,8 @@ mla_status mla_window_plan_host(const int32_t* seq_lens, const int32_t* q_lens, 
                                 int32_t sinks, int32_t num_clusters, void* plan_host, size_t plan_bytes,
                                 mla_window_info* info);
 
-/* As mla_window_plan_host, then copies the plan to plan_dev on `stream`. */
+/* As mla_window_plan_host, then copies the plan to plan_dev on `stream` (as
+ * mla_decode_plan, not into a capture). */
 mla_status mla_window_plan(const int32_t* seq_lens_host, const int32_t* q_lens_host, int32_t B, int32_t window,
                            int32_t sinks, int32_t num_clusters, void* plan_dev, size_t plan_bytes,
                            mla_window_info* info, void* stream);

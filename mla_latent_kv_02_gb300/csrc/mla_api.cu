@@ -1231,6 +1231,20 @@ mla_status mla_decode_plan_host(const int32_t* seq_lens, const int32_t* q_lens, 
   return build_plan(seq_lens, q_lens, B, num_clusters, (int32_t*)plan_host, plan_bytes / 4, info);
 }
 
+// The uploads copy from memory of the call's own: a captured copy would read it
+// again at every replay, long after it is gone.
+static mla_status not_captured(void* stream) {
+  cudaStreamCaptureStatus st = cudaStreamCaptureStatusNone;
+  const cudaError_t e = cudaStreamIsCapturing((cudaStream_t)stream, &st);
+  if (e != cudaSuccess) {
+    cudaGetLastError();  // not left for a later launch to find
+    return cuda_fail(e, "stream capture query");
+  }
+  if (st != cudaStreamCaptureStatusNone)
+    return fail(MLA_ERR_UNSUPPORTED, "a plan cannot be uploaded into a stream capture: plan before it, or use the host planner");
+  return MLA_OK;
+}
+
 mla_status mla_decode_plan(const int32_t* seq_lens_host, const int32_t* q_lens_host, int32_t B, int32_t num_clusters,
                            void* plan_dev, size_t plan_bytes, mla_plan_info* info, void* stream) {
   CHECK_PTR(plan_dev);
@@ -1238,6 +1252,7 @@ mla_status mla_decode_plan(const int32_t* seq_lens_host, const int32_t* q_lens_h
   CHECK_ALIGN16(plan_dev);
   std::vector<int32_t> host(plan_bytes / 4);
   mla_status s = build_plan(seq_lens_host, q_lens_host, B, num_clusters, host.data(), host.size(), info);
+  if (s == MLA_OK) s = not_captured(stream);
   if (s != MLA_OK) return s;
   // Pageable source: the call returns once the data is staged, so `host` may go.
   cudaError_t e = cudaMemcpyAsync(plan_dev, host.data(), info->plan_bytes, cudaMemcpyHostToDevice,
@@ -1284,6 +1299,7 @@ mla_status mla_window_plan(const int32_t* seq_lens_host, const int32_t* q_lens_h
   if (!host) return fail(MLA_ERR_NO_SPACE, "out of host memory");
   s = mla_window_plan_host(seq_lens_host, q_lens_host, B, window, sinks, num_clusters, host.get(),
                            std::min(plan_bytes, need), info);
+  if (s == MLA_OK) s = not_captured(stream);
   if (s != MLA_OK) return s;
   // Pageable source: the call returns once the data is staged, so `host` may go.
   cudaError_t e = cudaMemcpyAsync(plan_dev, host.get(), info->plan.plan_bytes, cudaMemcpyHostToDevice,

@@ -71,3 +71,22 @@ def test_decode_with_an_uploaded_plan(api, kind):
     o, lse, err = _decode(api, cache, q_abs, q_r, py)
     assert api.mla_check(err) == 0
     _check_decode(cache, q_abs, q_r, o, lse, q, window, sinks)
+
+
+@pytest.mark.parametrize("case", [0, 3])
+def test_upload_into_a_capture_is_refused(api, case):
+    """The copy's source is the call's own memory, gone when a captured copy is replayed."""
+    seq, q, window, sinks, clusters = CASES[case]
+    want, winfo = _host(api, seq, q, window, sinks, clusters)
+    plan = torch.full((want.size,), -7, dtype=torch.int32, device="cuda")
+    x = torch.zeros(4, device="cuda")
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        x.add_(1)
+        status, _ = _upload(seq, q, window, sinks, clusters, plan, torch.cuda.current_stream())
+    assert status == 3 and b"capture" in _lib.lib().mla_last_error()
+    g.replay()                                               # the capture itself goes on
+    torch.cuda.synchronize()
+    assert x.tolist() == [1.0] * 4 and bool((plan == -7).all())
+    assert _upload(seq, q, window, sinks, clusters, plan, torch.cuda.current_stream())[0] == 0
