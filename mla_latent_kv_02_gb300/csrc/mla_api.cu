@@ -1223,12 +1223,22 @@ mla_status mla_decode_workspace_size(int32_t num_clusters, size_t* bytes) {
   return MLA_OK;
 }
 
+// build_plan where an exception may not pass.
+static mla_status plan_checked(const int32_t* seq_lens, const int32_t* q_lens, int32_t B, int32_t num_clusters,
+                               int32_t* out, size_t out_words, mla_plan_info* info, int32_t window = 0, int32_t sinks = 0) {
+  try {
+    return build_plan(seq_lens, q_lens, B, num_clusters, out, out_words, info, window, sinks);
+  } catch (const std::bad_alloc&) {
+    return fail(MLA_ERR_NO_SPACE, "out of host memory");
+  }
+}
+
 mla_status mla_decode_plan_host(const int32_t* seq_lens, const int32_t* q_lens, int32_t B, int32_t num_clusters,
                                 void* plan_host, size_t plan_bytes, mla_plan_info* info) {
   CHECK_PTR(plan_host);
   CHECK_PTR(info);
   if (!aligned(plan_host, 4)) return fail(MLA_ERR_MISALIGNED, "plan_host is not 4-byte aligned");
-  return build_plan(seq_lens, q_lens, B, num_clusters, (int32_t*)plan_host, plan_bytes / 4, info);
+  return plan_checked(seq_lens, q_lens, B, num_clusters, (int32_t*)plan_host, plan_bytes / 4, info);
 }
 
 // The uploads copy from memory of the call's own: a captured copy would read it
@@ -1245,46 +1255,11 @@ static mla_status not_captured(void* stream) {
   return MLA_OK;
 }
 
-mla_status mla_decode_plan(const int32_t* seq_lens_host, const int32_t* q_lens_host, int32_t B, int32_t num_clusters,
-                           void* plan_dev, size_t plan_bytes, mla_plan_info* info, void* stream) {
+// A plan built in memory of the call's own and copied to plan_dev.
+static mla_status plan_upload(const int32_t* seq_lens_host, const int32_t* q_lens_host, int32_t B, int32_t num_clusters,
+                              void* plan_dev, size_t plan_bytes, mla_plan_info* info, void* stream, int32_t window = 0,
+                              int32_t sinks = 0) {
   CHECK_PTR(plan_dev);
-  CHECK_PTR(info);
-  CHECK_ALIGN16(plan_dev);
-  std::vector<int32_t> host(plan_bytes / 4);
-  mla_status s = build_plan(seq_lens_host, q_lens_host, B, num_clusters, host.data(), host.size(), info);
-  if (s == MLA_OK) s = not_captured(stream);
-  if (s != MLA_OK) return s;
-  // Pageable source: the call returns once the data is staged, so `host` may go.
-  cudaError_t e = cudaMemcpyAsync(plan_dev, host.data(), info->plan_bytes, cudaMemcpyHostToDevice,
-                                  (cudaStream_t)stream);
-  if (e != cudaSuccess) return cuda_fail(e, "plan copy");
-  return MLA_OK;
-}
-
-mla_status mla_window_plan_host(const int32_t* seq_lens, const int32_t* q_lens, int32_t B, int32_t window,
-                                int32_t sinks, int32_t num_clusters, void* plan_host, size_t plan_bytes,
-                                mla_window_info* info) {
-  CHECK_PTR(plan_host);
-  CHECK_PTR(info);
-  if (!aligned(plan_host, 4)) return fail(MLA_ERR_MISALIGNED, "plan_host is not 4-byte aligned");
-  mla_status s = window_check(window, sinks);
-  if (s != MLA_OK) return s;
-  try {
-    s = build_plan(seq_lens, q_lens, B, num_clusters, (int32_t*)plan_host, plan_bytes / 4, &info->plan, window, sinks);
-  } catch (const std::bad_alloc&) {
-    return fail(MLA_ERR_NO_SPACE, "out of host memory");
-  }
-  if (s != MLA_OK) return s;
-  info->window = window;
-  info->sinks = sinks;
-  return MLA_OK;
-}
-
-mla_status mla_window_plan(const int32_t* seq_lens_host, const int32_t* q_lens_host, int32_t B, int32_t window,
-                           int32_t sinks, int32_t num_clusters, void* plan_dev, size_t plan_bytes,
-                           mla_window_info* info, void* stream) {
-  CHECK_PTR(plan_dev);
-  CHECK_PTR(info);
   CHECK_ALIGN16(plan_dev);
   if (B < 0) return fail(MLA_ERR_INVALID_ARG, "B = %d is negative", B);
   if (num_clusters < 1) return fail(MLA_ERR_INVALID_ARG, "num_clusters = %d < 1", num_clusters);
@@ -1295,16 +1270,49 @@ mla_status mla_window_plan(const int32_t* seq_lens_host, const int32_t* q_lens_h
   size_t need = 0;
   mla_status s = mla_decode_plan_bytes((int32_t)T, num_clusters, &need);
   if (s != MLA_OK) return s;
-  std::unique_ptr<int32_t[]> host(new (std::nothrow) int32_t[std::min(plan_bytes, need) / 4 + 1]);
+  const size_t words = std::min(plan_bytes, need) / 4;
+  std::unique_ptr<int32_t[]> host(new (std::nothrow) int32_t[words + 1]);
   if (!host) return fail(MLA_ERR_NO_SPACE, "out of host memory");
-  s = mla_window_plan_host(seq_lens_host, q_lens_host, B, window, sinks, num_clusters, host.get(),
-                           std::min(plan_bytes, need), info);
+  s = plan_checked(seq_lens_host, q_lens_host, B, num_clusters, host.get(), words, info, window, sinks);
   if (s == MLA_OK) s = not_captured(stream);
   if (s != MLA_OK) return s;
   // Pageable source: the call returns once the data is staged, so `host` may go.
-  cudaError_t e = cudaMemcpyAsync(plan_dev, host.get(), info->plan.plan_bytes, cudaMemcpyHostToDevice,
-                                  (cudaStream_t)stream);
+  cudaError_t e = cudaMemcpyAsync(plan_dev, host.get(), info->plan_bytes, cudaMemcpyHostToDevice, (cudaStream_t)stream);
   if (e != cudaSuccess) return cuda_fail(e, "plan copy");
+  return MLA_OK;
+}
+
+mla_status mla_decode_plan(const int32_t* seq_lens_host, const int32_t* q_lens_host, int32_t B, int32_t num_clusters,
+                           void* plan_dev, size_t plan_bytes, mla_plan_info* info, void* stream) {
+  CHECK_PTR(info);
+  return plan_upload(seq_lens_host, q_lens_host, B, num_clusters, plan_dev, plan_bytes, info, stream);
+}
+
+mla_status mla_window_plan_host(const int32_t* seq_lens, const int32_t* q_lens, int32_t B, int32_t window,
+                                int32_t sinks, int32_t num_clusters, void* plan_host, size_t plan_bytes,
+                                mla_window_info* info) {
+  CHECK_PTR(plan_host);
+  CHECK_PTR(info);
+  if (!aligned(plan_host, 4)) return fail(MLA_ERR_MISALIGNED, "plan_host is not 4-byte aligned");
+  mla_status s = window_check(window, sinks);
+  if (s != MLA_OK) return s;
+  s = plan_checked(seq_lens, q_lens, B, num_clusters, (int32_t*)plan_host, plan_bytes / 4, &info->plan, window, sinks);
+  if (s != MLA_OK) return s;
+  info->window = window;
+  info->sinks = sinks;
+  return MLA_OK;
+}
+
+mla_status mla_window_plan(const int32_t* seq_lens_host, const int32_t* q_lens_host, int32_t B, int32_t window,
+                           int32_t sinks, int32_t num_clusters, void* plan_dev, size_t plan_bytes,
+                           mla_window_info* info, void* stream) {
+  CHECK_PTR(info);
+  mla_status s = window_check(window, sinks);
+  if (s == MLA_OK)
+    s = plan_upload(seq_lens_host, q_lens_host, B, num_clusters, plan_dev, plan_bytes, &info->plan, stream, window, sinks);
+  if (s != MLA_OK) return s;
+  info->window = window;
+  info->sinks = sinks;
   return MLA_OK;
 }
 
