@@ -541,6 +541,21 @@ mla_status mla_decode_paged_fp8(const void* q_abs, const void* q_r, const void* 
  * see may hold anything, infinities and NaN among them (unlike
  * mla_decode_paged, which wants the whole page finite); over the FP8 cache
  * their scales are not judged either.
+ *
+ * What is held in 16 bits (the same in mla_decode_paged(_fp8); sums of
+ * products, softmax sums, accumulators and lse are fp32):
+ *   - scores, before the scale, in fp16: each half of a score's 576 products
+ *     and the sum of the two halves, every rounding 2^-11 of its value.  With
+ *     the exponent formed in fp16 a token's weight is off by a factor of up to
+ *     about e^(4 S 2^-11), S the largest |score| of the row after the scale:
+ *     0.2 % of itself for S = 1, 14 % for S = 72 (1 000 before the default
+ *     scale).  A score past 65 504 before the scale (4 700 after it) does not
+ *     fit: the row's result is then wrong or NaN, and no error is set;
+ *   - the weights 2^x: fp16, and bf16 on their way into P.V over the bf16 cache;
+ *   - over the FP8 cache also q_abs, q_r and the cached RoPE keys, rounded from
+ *     bf16 to f16: exact for magnitudes in [2^-17, 65 280], saturating at
+ *     65 504, smaller values to a multiple of 2^-24;
+ *   - o_lat: bf16, one rounding.
  * ------------------------------------------------------------------------- */
 
 /* Summary of a window plan, filled by the planner and passed back to the decode. */
@@ -593,8 +608,11 @@ mla_status mla_prefill_window_workspace_size(const int32_t* q_lens, const int32_
  * tokens (above) are gathered and expanded; pages that hold none of them may
  * be -1 in the block table.  A row's keys of 128 tokens are multiplied at once,
  * so the kept tokens of a sequence must hold finite values, those that only
- * some of its rows see included; another sequence's never touch it.  K_c and
- * V_c are held in bf16 (one rounding), as in the branch without a window.
+ * some of its rows see included; another sequence's never touch it.
+ * In 16 bits, as in the branch without a window: K_c and V_c in bf16 (one
+ * rounding), the scores before the scale in fp16 (one rounding; past 65 504 they
+ * saturate and the row's result is wrong, with no error set), the exponent and
+ * 2^x in fp16, P and out in bf16; row sums and accumulators are fp32.
  */
 mla_status mla_prefill_window_batch(const void* q_c, const void* q_r, const int32_t* seq_ids, const int32_t* q_starts,
                                     const int32_t* q_lens, const int32_t* n_tokens, int32_t nb, int32_t window,
@@ -662,7 +680,7 @@ mla_status mla_gather_paged_nvfp4_batch(const void* rows, float tensor_scale, in
 /* ---------------------------------------------------------------------------
  * Steps A2 and A5 with 4-bit weights: W_UK and W_UV held as signed 4-bit codes
  * with one bf16 scale per group of `group` consecutive contraction values of a
- * column (4.25 to 4.5 bits a weight against 16),
+ * column (4.125 to 4.5 bits a weight against 16),
  *   W[h, k, n] = scales[h, k / group, n] * code[h, k, n],  code in [-8, 7].
  * words uint32 [128, K/8, N]: the code of k = 8 kb + i is the two's-complement
  * nibble in bits [4i, 4i + 4) of words[h, kb, n]; scales bf16 [128, K/group, N].
