@@ -161,12 +161,13 @@ inline int blocks_for(int64_t items) {
 }
 
 // Blocks of the rotating append: one token a warp while that fills the GPU,
-// then about six, in whole waves of eight blocks an SM.  On 2^20 tokens of 1.8
-// KB each: 54 tokens a warp 321 us, 8 309, 6 302 (6.3 TB/s), 4 315, one 368;
-// two tokens of a warp in flight at once 355 (fewer warps fit).
+// then about six, in steps of eight blocks an SM (six are resident: 40 registers
+// a thread).  Found by trial on 2^20 tokens of 1.8 KB each: 54 tokens a warp 321
+// us, 8 309, 6 302 (6.3 TB/s), 4 315, one 368; two tokens of a warp in flight at
+// once 355 (fewer warps fit).
 inline int append_blocks(int64_t n) {
-  constexpr int64_t kWave = 152 * 8;
-  const int64_t few = n / (6 * kWarps) / kWave * kWave;
+  constexpr int64_t kStep = 152 * 8;
+  const int64_t few = n / (6 * kWarps) / kStep * kStep;
   const int64_t b = few > blocks_for(n) ? few : blocks_for(n);
   return (int)b;
 }

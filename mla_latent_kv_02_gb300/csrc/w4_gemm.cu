@@ -41,7 +41,13 @@ using namespace mla::dev;
 constexpr int kSlice = 128;         // values of k a warp sums
 constexpr int kSteps = kSlice / 32; // words of a column in a slice, four lanes each one
 constexpr int kRowThreads = 256;
-constexpr int32_t kRowsMax = 32;    // more tokens go to tcgen05
+// More tokens go to tcgen05.  Device us with cold weights, this kernel against
+// the 128-token tiles at the same count (absorb, then up; groups of 128 / 64 / 32):
+//   16 tokens 5.7 / 5.6 / 6.3 against 8.1 / 10.2 / 12.7; 4.8 / 6.1 / 6.2 against 8.6 / 8.9 / 10.6
+//   32 tokens 7.5 / 7.9 / 8.8 against 8.6 / 10.3 / 12.7; 7.1 / 7.5 / 7.5 against 8.6 / 9.0 / 10.6
+// The tiles take 8.8 / 10.5 / 13.0 and 8.7 / 9.0 / 10.8 at 33 tokens and up to
+// 0.8 us more at 128; this kernel holds at most four token tiles in registers.
+constexpr int32_t kRowsMax = 32;
 
 // Pair i of a word (offset binary: sign bits flipped) as bf16: 0x4300 | v is 128 + v.
 __device__ __forceinline__ uint32_t code_pair(uint32_t w, int i) {
