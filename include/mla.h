@@ -604,7 +604,8 @@ mla_status mla_prefill_window_workspace_size(const int32_t* q_lens, const int32_
 
 /*
  * mla_prefill_decompress_batch with a sliding window and sinks: the same
- * arguments, buffers and errors, window >= 1 and sinks >= 0.  Only the kept
+ * arguments, buffers and errors, window >= 1 and sinks >= 0; chunks whose query
+ * rows overlap are MLA_ERR_INVALID_ARG.  Only the kept
  * tokens (above) are gathered and expanded; pages that hold none of them may
  * be -1 in the block table.  A row's keys of 128 tokens are multiplied at once,
  * so the kept tokens of a sequence must hold finite values, those that only

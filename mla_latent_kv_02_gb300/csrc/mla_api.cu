@@ -1049,6 +1049,14 @@ static mla_status prefill_window(const void* q_c, const void* q_r, const int32_t
     if (total > (1 << 24)) return fail(MLA_ERR_INVALID_ARG, "%lld kept tokens in all: too many", (long long)total);
   }
   if (rows_end > (1 << 24)) return fail(MLA_ERR_INVALID_ARG, "query rows past 2^24");
+  int32_t order[mla::kPrefillMaxSeqs];  // by first row: two chunks on one row of the output would race for it
+  for (int32_t i = 0; i < nb; ++i) order[i] = i;
+  std::sort(order, order + nb, [=](int32_t x, int32_t y) { return q_starts[x] < q_starts[y]; });
+  for (int32_t i = 1; i < nb; ++i) {
+    const int32_t x = order[i - 1], y = order[i];
+    if (q_starts[y] - q_starts[x] < q_lens[x])
+      return fail(MLA_ERR_INVALID_ARG, "the query rows of sequences %d and %d overlap", x, y);
+  }
   if (ws_bytes < prefill_ws_bytes(total))
     return fail(MLA_ERR_INVALID_ARG, "workspace holds %zu bytes, %lld kept tokens need %zu", ws_bytes,
                 (long long)total, prefill_ws_bytes(total));
