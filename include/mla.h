@@ -74,6 +74,7 @@ typedef enum mla_status {
 #define MLA_DEVERR_POS_OOB 16u /* RoPE position outside [0, max_pos): that token / row skipped */
 #define MLA_DEVERR_FP8_RANGE 32u /* FP8 decode: a token scale outside [2^-15, 2^7]; that row was clamped */
 #define MLA_DEVERR_BATCH 64u   /* batched gather: a sequence id, offset or length out of range; those rows skipped */
+#define MLA_DEVERR_TREE 128u   /* tree: an offset, length or accepted node out of range (sequence skipped), or a parent (a root then) */
 
 /* Thread-local message of the last failing call (never NULL). */
 const char* mla_last_error(void);
@@ -118,11 +119,53 @@ mla_status mla_pool_create(int32_t num_pages, mla_pool** out);
 /* Take `n` free page ids (lowest first) into page_ids_out[n].  MLA_ERR_NO_SPACE
  * (nothing taken) if fewer than n are free. */
 mla_status mla_pool_alloc(mla_pool* pool, int32_t n, int32_t* page_ids_out);
-/* Return ids to the pool.  MLA_ERR_INVALID_ARG (nothing returned) if an id is
- * out of range, not allocated, or repeated. */
+/* Give up one hold of each id; a page that nobody holds any more is free.
+ * MLA_ERR_INVALID_ARG (nothing returned) if an id is out of range, not
+ * allocated, or repeated. */
 mla_status mla_pool_free(mla_pool* pool, const int32_t* ids, int32_t n);
 mla_status mla_pool_available(const mla_pool* pool, int32_t* out);
 void mla_pool_destroy(mla_pool* pool);
+
+/*
+ * Pages held by several sequences.  mla_pool_alloc gives a page one holder;
+ * mla_pool_retain adds one to each of the n ids (an id may be repeated) and
+ * mla_pool_free takes one away.  MLA_ERR_INVALID_ARG (nothing changed) if an id
+ * is out of range or not allocated.  mla_pool_refs: the number of holders.
+ */
+mla_status mla_pool_retain(mla_pool* pool, const int32_t* ids, int32_t n);
+mla_status mla_pool_refs(const mla_pool* pool, int32_t id, int32_t* out);
+
+/*
+ * n_children sequences that continue a parent of n_tokens tokens: beams,
+ * samples of one prompt.  parent: its block-table row (the first
+ * ceil(n_tokens / 64) entries are read).  children int32 [n_children,
+ * max_pages] receives their rows: the parent's full pages, which gain n_children
+ * holders, then for a partly filled last page a fresh page of each child's own,
+ * then -1.  The fresh pages' contents are the caller's to copy: src[i] -> dst[i]
+ * for i < *n_copies (n_children, or 0 when n_tokens is a multiple of 64), as
+ * mla_copy_pages takes them.  The parent keeps its hold of all its pages; a
+ * child gives its pages back with mla_pool_free.  src and dst hold n_children
+ * entries.  MLA_ERR_NO_SPACE or MLA_ERR_INVALID_ARG (a page that is not
+ * allocated or repeated, too few columns): nothing changed.
+ */
+mla_status mla_pool_fork(mla_pool* pool, const int32_t* parent, int32_t n_tokens, int32_t n_children,
+                         int32_t max_pages, int32_t* children, int32_t* src, int32_t* dst, int32_t* n_copies);
+
+/*
+ * Bring the pool's allocated pages together at its low end, at most max_moves
+ * of them: the highest allocated page moves, with its holders, to the lowest
+ * free one until no free page lies below an allocated one.  src[i] -> dst[i],
+ * i < *n_moves, are the copies to make (mla_copy_pages) and the entries to
+ * replace (mla_remap_pages) before the tables are used again; in the pool the
+ * moves are done when the call returns, so what is written to a page allocated
+ * afterwards has to be queued behind the copies.
+ */
+mla_status mla_pool_compact(mla_pool* pool, int32_t max_moves, int32_t* src, int32_t* dst, int32_t* n_moves);
+
+/* Replace every entry src[i] of a host block table (`entries` values) by
+ * dst[i].  MLA_ERR_INVALID_ARG (nothing changed) if an id is negative or a
+ * source is repeated. */
+mla_status mla_remap_pages(int32_t* block_table, int64_t entries, const int32_t* src, const int32_t* dst, int32_t n);
 
 /*
  * Physical slot of token (seq_ids[i], positions[i]):
@@ -709,6 +752,132 @@ mla_status mla_absorb_q_w4(const void* q_c, const void* words, const void* scale
                            int32_t T, int32_t* dev_err, void* stream);
 mla_status mla_up_v_w4(const void* o_lat, const void* words, const void* scales, int32_t group, void* out, int32_t T,
                        int32_t* dev_err, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * Copies of whole pages in every layer's cache: a fork's last page, the moves
+ * of mla_pool_compact, pages kept aside.  For each layer l < layers and i < n,
+ *   page dst[i] of layer l = page src[i] of layer l    (bit for bit).
+ * src and dst are host int32 [n], read before the call returns (they ride in
+ * the launch parameters: the call can be captured, and a replay copies the same
+ * pages); 3 840 pairs a launch.  The cache of layer l starts layer_stride bytes
+ * after that of layer l - 1 (a multiple of 16, at least a layer's pages; not
+ * read for one layer).  A source may be repeated; a page written twice, or both
+ * read and written, an id outside the pool, layers < 1: MLA_ERR_INVALID_ARG,
+ * and nothing is enqueued.  n == 0 is a no-op.  The FP8 cache's scales go with
+ * its rows.
+ * ------------------------------------------------------------------------- */
+mla_status mla_copy_pages(void* kv_cache, int64_t num_pages, int32_t layers, int64_t layer_stride, const int32_t* src,
+                          const int32_t* dst, int32_t n, void* stream);
+mla_status mla_copy_pages_fp8(void* rows, float* scales, int64_t num_pages, int32_t layers, int64_t row_stride,
+                              int64_t scale_stride, const int32_t* src, const int32_t* dst, int32_t n, void* stream);
+mla_status mla_copy_pages_nvfp4(void* rows, int64_t num_pages, int32_t layers, int64_t layer_stride, const int32_t* src,
+                                const int32_t* dst, int32_t n, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * Trees of drafted tokens ([P2] MTP section drafts a chain of tokens for a
+ * step; a tree holds alternatives as well).  Sequence b has n0 = seq_lens[b] -
+ * q_lens[b] tokens and then the q_lens[b] nodes of its tree, at most
+ * MLA_TREE_MAX_NODES, node i appended at slot position n0 + i.  Nodes are in
+ * topological order: a parent before its children.  Row t = q_starts[b] + i is
+ * node i of sequence b.  A step:
+ *   mla_tree_layout   masks, RoPE positions and slots of the nodes;
+ *   mla_kv_append_... and, in every layer, mla_decode_tree(_fp8);
+ *   mla_tree_compact  once a path is accepted: its rows to positions n0, n0 + 1, ...
+ * Everything between the draft and the accepted nodes stays on the device, so
+ * the whole step can be captured.
+ * ------------------------------------------------------------------------- */
+#define MLA_TREE_MAX_NODES 256
+#define MLA_TREE_PLAN_MAGIC 0x544C4D41u /* "AMLT" */
+
+/*
+ * The nodes' ancestors.  parents int32 [T]: a node's parent as a node number
+ * within its own tree, -1 for a root (a node that follows token n0 - 1);
+ * q_starts int32 [B + 1] (first row of each sequence, q_starts[B] = T) and
+ * seq_lens int32 [B]; all device.  Writes
+ *   masks uint64 [T, words]: bit k of a row's words (bit k % 64 of word k / 64)
+ *     is set for the node itself and its ancestors k;
+ *   positions int32 [T] (or NULL): n0 + the node's depth, its RoPE position;
+ *   slots int64 [T] (or NULL): the cache slot of position n0 + i by block_table
+ *     int32 [B, max_pages] (read with slots only); a table entry outside
+ *     [0, num_pages) or past max_pages gives slot -1 and MLA_DEVERR_PAGE_OOB.
+ * words in [1, 4], 64 * words >= a tree's nodes.  A sequence whose offsets or
+ * lengths do not fit (or with more nodes) sets MLA_DEVERR_TREE and is skipped; a
+ * parent outside [-1, i) sets it and counts as -1.
+ */
+mla_status mla_tree_layout(const int32_t* parents, const int32_t* q_starts, const int32_t* seq_lens, int32_t B,
+                           int32_t T, int32_t words, const int32_t* block_table, int32_t max_pages, int64_t num_pages,
+                           uint64_t* masks, int32_t* positions, int64_t* slots, int32_t* dev_err, void* stream);
+
+/* Summary of a tree plan, filled by the planner and passed back to the decode. */
+typedef struct mla_tree_info {
+  mla_plan_info plan; /* plan.magic == MLA_TREE_PLAN_MAGIC */
+  int32_t max_nodes;  /* the largest tree */
+} mla_tree_info;
+
+/*
+ * The split schedule of mla_decode_plan_host for trees: the same arguments
+ * (q_lens[b] nodes, at most MLA_TREE_MAX_NODES, else MLA_ERR_UNSUPPORTED),
+ * buffers (mla_decode_plan_bytes, mla_decode_workspace_size) and errors.  It
+ * depends on the lengths alone, not on the trees' shapes.  A plan of one kind
+ * passed to the other kind's decode is MLA_ERR_INVALID_ARG.
+ */
+mla_status mla_tree_plan_host(const int32_t* seq_lens, const int32_t* q_lens, int32_t B, int32_t num_clusters,
+                              void* plan_host, size_t plan_bytes, mla_tree_info* info);
+/* As mla_tree_plan_host, then copies the plan to plan_dev on `stream` (as
+ * mla_decode_plan, not into a capture). */
+mla_status mla_tree_plan(const int32_t* seq_lens_host, const int32_t* q_lens_host, int32_t B, int32_t num_clusters,
+                         void* plan_dev, size_t plan_bytes, mla_tree_info* info, void* stream);
+
+/*
+ * Steps A3 and A4 for the nodes of trees: mla_decode_paged(_fp8) in which row t,
+ * node i of sequence b, sees the tokens [0, n0) and each node k <= i whose bit
+ * is set in masks[t] (its own bit included; bits above i are not read).  masks
+ * uint64 [T, words], device, 8-byte aligned, 64 * words >= the plan's largest
+ * tree.  Any mask of such bits will do, a tree's or not.  A row that sees
+ * nothing (n0 = 0 and no bit set) has o_lat = 0 and lse = -infinity.  Of the
+ * pages that are read, slots that a row does not see may hold anything,
+ * infinities and NaN among them; over the FP8 cache their scales are not judged.
+ * What is held in 16 bits is as for the windowed decode.
+ */
+mla_status mla_decode_tree(const void* q_abs, const void* q_r, const void* kv_cache, int64_t num_pages,
+                           const int32_t* block_table, int32_t max_pages, const uint64_t* masks, int32_t words,
+                           const void* plan_dev, const mla_tree_info* info, float scale, void* workspace,
+                           size_t ws_bytes, void* o_lat, float* lse, int32_t* dev_err, void* stream);
+mla_status mla_decode_tree_fp8(const void* q_abs, const void* q_r, const void* rows, const float* scales,
+                               int64_t num_pages, const int32_t* block_table, int32_t max_pages,
+                               const uint64_t* masks, int32_t words, const void* plan_dev, const mla_tree_info* info,
+                               float scale, void* workspace, size_t ws_bytes, void* o_lat, float* lse,
+                               int32_t* dev_err, void* stream);
+
+/*
+ * Keep the accepted path of each tree.  accepted int32 [B] (device): the last
+ * accepted node of sequence b, -1 for none; the kept nodes k_0 < k_1 < ... are
+ * the bits up to that node in its mask row.  In each of `layers` caches the row
+ * at position n0 + k_r moves to n0 + r (bit for bit, the FP8 scale with it), and
+ * new_lens[b] = n0 + the number of kept nodes (device int32 [B], not one of the
+ * inputs' memory: MLA_ERR_INVALID_ARG).  RoPE keys stay as they are: a kept
+ * node's position n0 + depth is the one it moves to.  The pages that hold the
+ * nodes must belong to the sequence alone (a fork's shared pages are full, and
+ * nodes are never in them).  Slots after new_lens[b] keep what they held; pages
+ * past it are the caller's to free.  A page id outside the pool
+ * sets MLA_DEVERR_PAGE_OOB, and a row from or to such a page does not move.  A
+ * sequence whose offsets or lengths do not fit, or with an accepted node outside
+ * [-1, q_lens[b]), sets MLA_DEVERR_TREE and is left as it was, its new_lens[b]
+ * too.  Layer strides as for mla_copy_pages.
+ */
+mla_status mla_tree_compact(void* kv_cache, int64_t num_pages, int32_t layers, int64_t layer_stride,
+                            const int32_t* block_table, int32_t max_pages, const uint64_t* masks, int32_t words,
+                            const int32_t* q_starts, const int32_t* seq_lens, const int32_t* accepted, int32_t B,
+                            int32_t T, int32_t* new_lens, int32_t* dev_err, void* stream);
+mla_status mla_tree_compact_fp8(void* rows, float* scales, int64_t num_pages, int32_t layers, int64_t row_stride,
+                                int64_t scale_stride, const int32_t* block_table, int32_t max_pages,
+                                const uint64_t* masks, int32_t words, const int32_t* q_starts, const int32_t* seq_lens,
+                                const int32_t* accepted, int32_t B, int32_t T, int32_t* new_lens, int32_t* dev_err,
+                                void* stream);
+mla_status mla_tree_compact_nvfp4(void* rows, int64_t num_pages, int32_t layers, int64_t layer_stride,
+                                  const int32_t* block_table, int32_t max_pages, const uint64_t* masks, int32_t words,
+                                  const int32_t* q_starts, const int32_t* seq_lens, const int32_t* accepted, int32_t B,
+                                  int32_t T, int32_t* new_lens, int32_t* dev_err, void* stream);
 
 /*
  * Synchronise `stream`, read the device error word into *word_out (may be

@@ -29,6 +29,10 @@ class mla_window_info(C.Structure):
     _fields_ = [("plan", mla_plan_info), ("window", C.c_int32), ("sinks", C.c_int32)]
 
 
+class mla_tree_info(C.Structure):
+    _fields_ = [("plan", mla_plan_info), ("max_nodes", C.c_int32)]
+
+
 P = C.c_void_p
 I32 = C.c_int32
 I64 = C.c_int64
@@ -48,6 +52,11 @@ SIGNATURES = {
     "mla_pool_free": (C.c_int, [P, PI32, I32]),
     "mla_pool_available": (C.c_int, [P, PI32]),
     "mla_pool_destroy": (None, [P]),
+    "mla_pool_retain": (C.c_int, [P, PI32, I32]),
+    "mla_pool_refs": (C.c_int, [P, I32, PI32]),
+    "mla_pool_fork": (C.c_int, [P, PI32, I32, I32, I32, PI32, PI32, PI32, PI32]),
+    "mla_pool_compact": (C.c_int, [P, I32, PI32, PI32, PI32]),
+    "mla_remap_pages": (C.c_int, [PI32, I64, PI32, PI32, I32]),
     "mla_slot_mapping": (C.c_int, [PI32, I32, I32, PI32, PI32, I32, PI64]),
     "mla_cache_init": (C.c_int, [P, I64, P]),
     "mla_kv_append": (C.c_int, [P, P, P, I32, P, I64, P, P]),
@@ -93,6 +102,18 @@ SIGNATURES = {
     "mla_pack_w4": (C.c_int, [P, I32, I32, I32, P, P, P]),
     "mla_absorb_q_w4": (C.c_int, [P, P, P, I32, P, I32, P, P]),
     "mla_up_v_w4": (C.c_int, [P, P, P, I32, P, I32, P, P]),
+    "mla_copy_pages": (C.c_int, [P, I64, I32, I64, P, P, I32, P]),
+    "mla_copy_pages_fp8": (C.c_int, [P, P, I64, I32, I64, I64, P, P, I32, P]),
+    "mla_copy_pages_nvfp4": (C.c_int, [P, I64, I32, I64, P, P, I32, P]),
+    "mla_tree_layout": (C.c_int, [P, P, P, I32, I32, I32, P, I32, I64, P, P, P, P, P]),
+    "mla_tree_plan_host": (C.c_int, [PI32, PI32, I32, I32, P, SZ, C.POINTER(mla_tree_info)]),
+    "mla_tree_plan": (C.c_int, [PI32, PI32, I32, I32, P, SZ, C.POINTER(mla_tree_info), P]),
+    "mla_decode_tree": (C.c_int, [P, P, P, I64, P, I32, P, I32, P, C.POINTER(mla_tree_info), C.c_float, P, SZ, P, P, P, P]),
+    "mla_decode_tree_fp8": (C.c_int, [P, P, P, P, I64, P, I32, P, I32, P, C.POINTER(mla_tree_info), C.c_float, P, SZ, P,
+                                      P, P, P]),
+    "mla_tree_compact": (C.c_int, [P, I64, I32, I64, P, I32, P, I32, P, P, P, I32, I32, P, P, P]),
+    "mla_tree_compact_fp8": (C.c_int, [P, P, I64, I32, I64, I64, P, I32, P, I32, P, P, P, I32, I32, P, P, P]),
+    "mla_tree_compact_nvfp4": (C.c_int, [P, I64, I32, I64, P, I32, P, I32, P, P, P, I32, I32, P, P, P]),
     "mla_check": (C.c_int, [P, P, PI32]),
     "mla_debug_set_decode_wait_limit": (C.c_int, [C.c_uint64]),
     "mla_decode_paged_noalloc": (C.c_int, [P, P, P, I64, P, I32, PI32, PI32, I32, C.c_float, P, P, P, P]),

@@ -15,7 +15,7 @@ from typing import Optional, Sequence
 import numpy as np
 import torch
 
-from ._lib import lib, mla_plan_info, mla_window_info
+from ._lib import lib, mla_plan_info, mla_tree_info, mla_window_info
 
 H, D_HC, D_C, D_R, PAGE = 128, 128, 512, 64, 64
 D_QK = D_C + D_R
@@ -23,7 +23,7 @@ D_QK = D_C + D_R
 STATUS = {0: "MLA_OK", 1: "MLA_ERR_INVALID_ARG", 2: "MLA_ERR_MISALIGNED", 3: "MLA_ERR_UNSUPPORTED",
           4: "MLA_ERR_CUDA", 5: "MLA_ERR_DEVICE", 6: "MLA_ERR_TIMEOUT", 7: "MLA_ERR_NO_SPACE"}
 DEVERR_PAGE_OOB, DEVERR_SLOT_OOB, DEVERR_TIMEOUT, DEVERR_PLAN, DEVERR_POS_OOB, DEVERR_FP8_RANGE = 1, 2, 4, 8, 16, 32
-DEVERR_BATCH = 64
+DEVERR_BATCH, DEVERR_TREE = 64, 128
 
 
 class MlaError(RuntimeError):
@@ -99,8 +99,23 @@ def mla_kv_bytes(layers: int, dc: int, dr: int, elem_bytes: int, tokens: int, se
     return int(out.value)
 
 
+_P32 = C.POINTER(C.c_int32)
+
+
+def _i32(x, name: str) -> np.ndarray:
+    """Host values as a contiguous int32 array; what int32 does not hold is refused."""
+    v = np.asarray(x)
+    if type(x) is not np.ndarray or v.dtype != np.int32:
+        a = np.ascontiguousarray(v, dtype=np.int32)
+        if (a != v).any():
+            raise ValueError(f"{name} must be whole numbers that int32 holds")
+        return a
+    return np.ascontiguousarray(v)
+
+
 class MlaPool:
-    """Host page pool (mla_pool_*)."""
+    """Host page pool (mla_pool_*).  A page may have several holders: `retain`
+    and `fork` add them, `free` takes one away from each id."""
 
     def __init__(self, num_pages: int):
         self._h = C.c_void_p()
@@ -120,6 +135,43 @@ class MlaPool:
         _check(lib().mla_pool_available(self._h, C.byref(out)))
         return int(out.value)
 
+    def retain(self, ids) -> None:
+        ids = _i32(ids, "ids").reshape(-1)
+        _check(lib().mla_pool_retain(self._h, ids.ctypes.data_as(_P32), int(ids.size)))
+
+    def refs(self, page: int) -> int:
+        out = C.c_int32()
+        _check(lib().mla_pool_refs(self._h, operator.index(page), C.byref(out)))
+        return int(out.value)
+
+    def fork(self, parent, n_tokens: int, n_children: int, max_pages: Optional[int] = None):
+        """Children of a parent of n_tokens tokens (parent: its block-table row):
+        returns (rows int32 [n_children, max_pages], src, dst), the copies that
+        give each child its own last page (mla_copy_pages)."""
+        parent = _i32(parent, "parent").reshape(-1)
+        cols, k = parent.size if max_pages is None else operator.index(max_pages), operator.index(n_children)
+        if not 0 <= n_tokens <= PAGE * parent.size:
+            raise ValueError(f"n_tokens = {n_tokens}: the parent has {parent.size} pages")
+        if not (0 <= k < 2 ** 31 and 0 <= cols < 2 ** 31):
+            raise ValueError(f"n_children = {k}, max_pages = {cols}: out of range")
+        rows = np.full((k, cols), -1, dtype=np.int32)
+        src, dst, n = np.zeros(max(k, 1), dtype=np.int32), np.zeros(max(k, 1), dtype=np.int32), C.c_int32()
+        _check(lib().mla_pool_fork(self._h, parent.ctypes.data_as(_P32), operator.index(n_tokens), k, cols,
+                                   rows.ctypes.data_as(_P32), src.ctypes.data_as(_P32), dst.ctypes.data_as(_P32),
+                                   C.byref(n)))
+        return rows, src[:n.value], dst[:n.value]
+
+    def compact(self, max_moves: int):
+        """Brings the allocated pages together at the pool's low end, at most
+        max_moves of them: returns (src, dst), the copies to make
+        (mla_copy_pages) and the table entries to replace (mla_remap_pages)."""
+        k = operator.index(max_moves)
+        if not 0 <= k < 2 ** 31:
+            raise ValueError(f"max_moves = {k}: out of range")
+        src, dst, n = np.zeros(max(k, 1), dtype=np.int32), np.zeros(max(k, 1), dtype=np.int32), C.c_int32()
+        _check(lib().mla_pool_compact(self._h, k, src.ctypes.data_as(_P32), dst.ctypes.data_as(_P32), C.byref(n)))
+        return src[:n.value].copy(), dst[:n.value].copy()
+
     def close(self) -> None:
         if self._h:
             lib().mla_pool_destroy(self._h)
@@ -130,6 +182,17 @@ class MlaPool:
             self.close()
         except Exception:
             pass
+
+
+def mla_remap_pages(block_table: np.ndarray, src, dst) -> np.ndarray:
+    """A host block table with every entry src[i] replaced by dst[i] (a new array)."""
+    bt = _i32(block_table, "block_table").copy()
+    src, dst = _i32(src, "src").reshape(-1), _i32(dst, "dst").reshape(-1)
+    if src.size != dst.size:
+        raise ValueError(f"{src.size} sources and {dst.size} destinations")
+    _check(lib().mla_remap_pages(bt.ctypes.data_as(_P32), int(bt.size), src.ctypes.data_as(_P32),
+                                 dst.ctypes.data_as(_P32), int(src.size)))
+    return bt
 
 
 def mla_slot_mapping(block_table: np.ndarray, seq_ids: np.ndarray, positions: np.ndarray) -> np.ndarray:
@@ -652,6 +715,11 @@ def mla_window_plan(seq_lens: Sequence[int], q_lens: Sequence[int], window: int,
     if num_clusters is None:
         num_clusters = mla_decode_max_clusters()
     buf, info = mla_window_plan_host(seq_lens, q_lens, window, sinks, num_clusters)
+    return _planned(WindowPlan, buf, info, num_clusters, device, stream, into)
+
+
+def _planned(cls, buf, info, num_clusters: int, device, stream, into):
+    """A host plan in device buffers, `into`'s where they are large enough."""
     words = (buf.size + 3) // 4 * 4
     device = torch.device(device) if device is not None else torch.device("cuda", torch.cuda.current_device())
     ws_bytes = max(mla_decode_workspace_size(num_clusters), 16)
@@ -660,7 +728,7 @@ def mla_window_plan(seq_lens: Sequence[int], q_lens: Sequence[int], window: int,
         plan = replace(into)
     else:
         with torch.cuda.stream(stream):
-            plan = _plan_buffers(WindowPlan, words, ws_bytes, device)
+            plan = _plan_buffers(cls, words, ws_bytes, device)
     plan.info = info
     plan.host[:buf.size] = torch.from_numpy(buf)
     _upload(plan, words, stream)
@@ -705,6 +773,209 @@ def _decode_window(call, cache, pages, q_abs, q_r, block_table, plan, o_lat, dev
                 _in(o_lat, "o_lat", torch.bfloat16, (T, H, D_C), dev),
                 None if lse is None else _in(lse, "lse", torch.float32, (T, H), dev),
                 _in(dev_err, "dev_err", torch.int32, (1,), dev), _use(plan, stream, dev)))
+
+
+# ------------------------------------------------------------------ pages of all layers
+def _layers(t, name: str, dtype, page, dev: int):
+    """A cache [pages, *page], or that of a model's layers [layers, pages, *page]
+    (each layer contiguous, any stride between layers): (address, pages, layers,
+    bytes from a layer to the next)."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on {t.device}, the current device is cuda:{dev}")
+    shape = t.shape
+    if len(shape) not in (len(page) + 1, len(page) + 2) or shape[-len(page):] != page:
+        raise ValueError(f"{name} has shape {tuple(shape)}, expected ([layers,] pages, {', '.join(map(str, page))})")
+    layers, stride = (shape[0], t.stride(0) * t.element_size()) if len(shape) > len(page) + 1 else (1, 0)
+    if not (t.is_contiguous() or (len(shape) > len(page) + 1 and layers > 0 and t[0].is_contiguous())):
+        raise ValueError(f"{name}: a layer's pages must be contiguous")
+    return t.data_ptr(), shape[-len(page) - 1], layers, stride
+
+
+def _fp8_layers(rows, scales, dev: int):
+    r, pages, layers, row_stride = _layers(rows, "rows", torch.uint8, (PAGE, FP8_ROW_BYTES), dev)
+    s, s_pages, s_layers, scale_stride = _layers(scales, "scales", torch.float32, (PAGE,), dev)
+    if (s_pages, s_layers, scales.dim()) != (pages, layers, rows.dim() - 1):
+        raise ValueError(f"rows has shape {tuple(rows.shape)}, scales {tuple(scales.shape)}")
+    return r, s, pages, layers, row_stride, scale_stride
+
+
+def _copy_pages(call, cache, src, dst, stream, dev: int) -> None:
+    src, dst = _i32(src, "src"), _i32(dst, "dst")
+    if src.ndim != 1 or src.shape != dst.shape:
+        raise ValueError(f"src and dst must be lists of one length, got shapes {src.shape} and {dst.shape}")
+    _check(call(*cache, src.ctypes.data, dst.ctypes.data, src.size, _on(stream, dev)))
+
+
+def mla_copy_pages(kv_cache, src, dst, stream=None) -> None:
+    """Page dst[i] = page src[i] in every layer of kv_cache bf16 [[layers,]
+    pages, 64, 576] (host lists of page ids; no page written twice, none both
+    read and written)."""
+    dev = torch.cuda.current_device()
+    _copy_pages(lib().mla_copy_pages, _layers(kv_cache, "kv_cache", torch.bfloat16, (PAGE, D_QK), dev), src, dst, stream, dev)
+
+
+def mla_copy_pages_fp8(rows, scales, src, dst, stream=None) -> None:
+    """mla_copy_pages over the FP8 cache: rows uint8 [[layers,] pages, 64, 640],
+    scales fp32 [[layers,] pages, 64]."""
+    dev = torch.cuda.current_device()
+    _copy_pages(lib().mla_copy_pages_fp8, _fp8_layers(rows, scales, dev), src, dst, stream, dev)
+
+
+def mla_copy_pages_nvfp4(rows, src, dst, stream=None) -> None:
+    """mla_copy_pages over the NVFP4 cache: rows uint8 [[layers,] pages, 64, 416]."""
+    dev = torch.cuda.current_device()
+    _copy_pages(lib().mla_copy_pages_nvfp4, _layers(rows, "rows", torch.uint8, (PAGE, NVFP4_ROW_BYTES), dev), src, dst,
+                stream, dev)
+
+
+# ------------------------------------------------------------------ trees of drafted tokens
+def _table(block_table, B: int, dev: int):
+    if not isinstance(block_table, torch.Tensor) or block_table.dim() != 2 or block_table.shape[0] < B:
+        raise ValueError(f"block_table must be [sequences, pages] of at least {B} sequences")
+    return _in(block_table, "block_table", torch.int32, tuple(block_table.shape), dev), block_table.shape[1]
+
+
+def _masks(masks, T: int, dev: int):
+    if not isinstance(masks, torch.Tensor) or masks.dim() != 2:
+        raise ValueError("masks must be a tensor [nodes, words]")
+    words = masks.shape[1]
+    return _in(masks, "masks", torch.int64, (T, words), dev), words
+
+
+def mla_tree_layout(parents, q_starts, seq_lens, masks, dev_err, positions=None, slots=None, block_table=None,
+                    num_pages: int = 0, stream=None) -> None:
+    """The ancestors' masks of drafted nodes: parents int32 [T] (within each tree,
+    -1 for a root, a parent before its children), q_starts int32 [B + 1],
+    seq_lens int32 [B] (nodes included) into masks int64 [T, words], and where
+    wanted positions int32 [T] and slots int64 [T] (by block_table [B, pages] of a
+    pool of num_pages).  All tensors on the device."""
+    dev = torch.cuda.current_device()
+    T, B = parents.shape[0], seq_lens.shape[0]
+    m, words = _masks(masks, T, dev)
+    if slots is not None and block_table is None:
+        raise ValueError("slots need a block_table")
+    table, cols = (None, 0) if slots is None else _table(block_table, B, dev)
+    _check(lib().mla_tree_layout(
+        _in(parents, "parents", torch.int32, (T,), dev), _in(q_starts, "q_starts", torch.int32, (B + 1,), dev),
+        _in(seq_lens, "seq_lens", torch.int32, (B,), dev), B, T, words, table, cols, num_pages, m,
+        None if positions is None else _in(positions, "positions", torch.int32, (T,), dev),
+        None if slots is None else _in(slots, "slots", torch.int64, (T,), dev),
+        _in(dev_err, "dev_err", torch.int32, (1,), dev), _on(stream, dev)))
+
+
+def mla_tree_plan_host(seq_lens: Sequence[int], q_lens: Sequence[int], num_clusters: int):
+    """Host planner of the tree decode only (no GPU): returns (plan int32 array, info)."""
+    sl, ql = _host_i32(seq_lens, q_lens)
+    nbytes = mla_decode_plan_bytes(int(ql.sum()) if ql.size else 0, num_clusters)
+    buf = np.zeros(nbytes // 4, dtype=np.int32)
+    info = mla_tree_info()
+    _check(lib().mla_tree_plan_host(sl.ctypes.data_as(_P32), ql.ctypes.data_as(_P32), int(sl.size), int(num_clusters),
+                                    buf.ctypes.data_as(C.c_void_p), nbytes, C.byref(info)))
+    return buf, info
+
+
+@dataclass
+class TreePlan:
+    """A tree plan on the device plus its host summary (mla_tree_plan)."""
+    plan: torch.Tensor          # int32 device buffer
+    info: mla_tree_info
+    workspace: torch.Tensor     # uint8 device buffer
+    host: torch.Tensor          # pinned int32 staging of the plan (reused by `into=`)
+    streams: set = field(default_factory=set, repr=False, compare=False)  # raw handles of the streams that use the buffers
+
+    @property
+    def num_clusters(self) -> int:
+        return int(self.info.plan.num_clusters)
+
+
+def mla_tree_plan(seq_lens: Sequence[int], q_lens: Sequence[int], device=None, num_clusters: Optional[int] = None,
+                  stream=None, into: Optional[TreePlan] = None) -> TreePlan:
+    """mla_decode_plan for trees of drafted nodes (q_lens[b] of them, the last of
+    seq_lens[b] tokens): one plan serves every layer of a step, whatever the
+    trees' shapes.  Uploads, streams, sharing and `into` as for mla_window_plan."""
+    if num_clusters is None:
+        num_clusters = mla_decode_max_clusters()
+    buf, info = mla_tree_plan_host(seq_lens, q_lens, num_clusters)
+    return _planned(TreePlan, buf, info, num_clusters, device, stream, into)
+
+
+def mla_decode_tree(q_abs, q_r, kv_cache, block_table, masks, plan: TreePlan, o_lat, dev_err, lse=None,
+                    scale: float = 1.0 / (192 ** 0.5), stream=None) -> None:
+    """mla_decode_paged for the nodes of trees: a row sees the tokens before its
+    tree and the nodes of its mask (masks int64 [T, words], mla_tree_layout)."""
+    dev = torch.cuda.current_device()
+    pages = kv_cache.shape[0]
+    cache = (_in(kv_cache, "kv_cache", torch.bfloat16, (pages, PAGE, D_QK), dev),)
+    _decode_tree(lib().mla_decode_tree, cache, pages, q_abs, q_r, block_table, masks, plan, o_lat, dev_err, lse, scale,
+                 stream, dev)
+
+
+def mla_decode_tree_fp8(q_abs, q_r, rows, scales, block_table, masks, plan: TreePlan, o_lat, dev_err, lse=None,
+                        scale: float = 1.0 / (192 ** 0.5), stream=None) -> None:
+    """mla_decode_tree over the FP8 cache."""
+    dev = torch.cuda.current_device()
+    pages = rows.shape[0]
+    cache = (_in(rows, "rows", torch.uint8, (pages, PAGE, FP8_ROW_BYTES), dev),
+             _in(scales, "scales", torch.float32, (pages, PAGE), dev))
+    _decode_tree(lib().mla_decode_tree_fp8, cache, pages, q_abs, q_r, block_table, masks, plan, o_lat, dev_err, lse, scale,
+                 stream, dev)
+
+
+def _decode_tree(call, cache, pages, q_abs, q_r, block_table, masks, plan, o_lat, dev_err, lse, scale, stream, dev) -> None:
+    if not isinstance(plan, TreePlan):
+        raise TypeError("plan must come from mla_tree_plan")
+    T, sums = q_abs.shape[0], plan.info.plan
+    if sums.T != T:
+        raise ValueError(f"plan has {sums.T} rows, q_abs has {T}")
+    m, words = _masks(masks, T, dev)
+    table, cols = _table(block_table, sums.B, dev)
+    ws_bytes = plan.workspace.numel()
+    _check(call(_in(q_abs, "q_abs", torch.bfloat16, (T, H, D_C), dev), _in(q_r, "q_r", torch.bfloat16, (T, H, D_R), dev),
+                *cache, pages, table, cols, m, words, _in(plan.plan, "plan.plan", torch.int32, (plan.plan.numel(),), dev),
+                plan.info, float(scale), _in(plan.workspace, "plan.workspace", torch.uint8, (ws_bytes,), dev), ws_bytes,
+                _in(o_lat, "o_lat", torch.bfloat16, (T, H, D_C), dev),
+                None if lse is None else _in(lse, "lse", torch.float32, (T, H), dev),
+                _in(dev_err, "dev_err", torch.int32, (1,), dev), _use(plan, stream, dev)))
+
+
+def _tree_compact(call, cache, block_table, masks, q_starts, seq_lens, accepted, new_lens, dev_err, stream, dev) -> None:
+    T, B = masks.shape[0], seq_lens.shape[0]
+    m, words = _masks(masks, T, dev)
+    table, cols = _table(block_table, B, dev)
+    _check(call(*cache, table, cols, m, words, _in(q_starts, "q_starts", torch.int32, (B + 1,), dev),
+                _in(seq_lens, "seq_lens", torch.int32, (B,), dev), _in(accepted, "accepted", torch.int32, (B,), dev), B, T,
+                _in(new_lens, "new_lens", torch.int32, (B,), dev), _in(dev_err, "dev_err", torch.int32, (1,), dev),
+                _on(stream, dev)))
+
+
+def mla_tree_compact(kv_cache, block_table, masks, q_starts, seq_lens, accepted, new_lens, dev_err, stream=None) -> None:
+    """Keep each tree's accepted path: in every layer of kv_cache bf16 [[layers,]
+    pages, 64, 576] the rows of node accepted[b] and the nodes of its mask move
+    to the places after the sequence (-1: none is kept), and new_lens[b] becomes
+    the sequence's length.  All tensors on the device."""
+    dev = torch.cuda.current_device()
+    _tree_compact(lib().mla_tree_compact, _layers(kv_cache, "kv_cache", torch.bfloat16, (PAGE, D_QK), dev), block_table,
+                  masks, q_starts, seq_lens, accepted, new_lens, dev_err, stream, dev)
+
+
+def mla_tree_compact_fp8(rows, scales, block_table, masks, q_starts, seq_lens, accepted, new_lens, dev_err,
+                         stream=None) -> None:
+    """mla_tree_compact over the FP8 cache: rows uint8 [[layers,] pages, 64, 640],
+    scales fp32 [[layers,] pages, 64]."""
+    dev = torch.cuda.current_device()
+    _tree_compact(lib().mla_tree_compact_fp8, _fp8_layers(rows, scales, dev), block_table, masks, q_starts, seq_lens,
+                  accepted, new_lens, dev_err, stream, dev)
+
+
+def mla_tree_compact_nvfp4(rows, block_table, masks, q_starts, seq_lens, accepted, new_lens, dev_err, stream=None) -> None:
+    """mla_tree_compact over the NVFP4 cache: rows uint8 [[layers,] pages, 64, 416]."""
+    dev = torch.cuda.current_device()
+    _tree_compact(lib().mla_tree_compact_nvfp4, _layers(rows, "rows", torch.uint8, (PAGE, NVFP4_ROW_BYTES), dev),
+                  block_table, masks, q_starts, seq_lens, accepted, new_lens, dev_err, stream, dev)
 
 
 def mla_prefill_window_workspace_size(q_lens: Sequence[int], n_tokens: Sequence[int], window: int, sinks: int) -> int:

@@ -4,7 +4,8 @@
 // pieces is the log-sum-exp weighted mean of the pieces' normalised outputs:
 //   o_lat = Σ_i 2^(lse_i - m) o_i / Σ_i 2^(lse_i - m),   lse = (m + log2 Σ_i 2^(lse_i - m)) ln 2,
 // with o_i the fp32 normalised partial of piece i, lse_i its log2-sum-exp
-// and m = max_i lse_i.
+// and m = max_i lse_i.  A piece of which the row sees nothing has lse_i =
+// -infinity and weight 0; a row of only such pieces is 0, its lse -infinity.
 //
 // One CTA = one split row and HPC heads; TPH threads per head, each with QPT
 // of the head's 128 column quads (float4), loaded for two pieces at once.
@@ -63,7 +64,8 @@ __global__ void __launch_bounds__(HPC * 128 / QPT) combine_kernel(const CombineA
       for (int k = 0; k < QPT; ++k) vb[k] = make_float4(0.f, 0.f, 0.f, 0.f);
     }
     const float mn = fmaxf(mx, fmaxf(la, lb));
-    const float sc = exp2f(mx - mn), wa = exp2f(la - mn), wb = two ? exp2f(lb - mn) : 0.f;
+    const float ref = mn == -INFINITY ? 0.f : mn;
+    const float sc = exp2f(mx - ref), wa = exp2f(la - ref), wb = two ? exp2f(lb - ref) : 0.f;
     mx = mn;
     wsum = wsum * sc + wa + wb;
 #pragma unroll
@@ -74,7 +76,7 @@ __global__ void __launch_bounds__(HPC * 128 / QPT) combine_kernel(const CombineA
       acc[k].w = acc[k].w * sc + wa * va[k].w + wb * vb[k].w;
     }
   }
-  const float inv = 1.f / wsum;
+  const float inv = wsum == 0.f ? 0.f : 1.f / wsum;
   uint2* dst = reinterpret_cast<uint2*>(a.o_lat + ((size_t)row * kH + h) * kDC) + q0;
 #pragma unroll
   for (int k = 0; k < QPT; ++k)

@@ -184,20 +184,34 @@ struct Idesc {
   static constexpr uint32_t kSum = kF8 ? idesc_f16_f32(128, 16, false, false) : idesc_bf16_f32(128, 16, false, false);
 };
 
+// What a row sees: every token up to its own; a sliding window and sinks; or
+// the tokens before a tree of drafted nodes and the nodes of the row's mask.
+enum class Sees { kAll, kWindow, kTree };
+
 // Walks the 64-token tiles of a cluster's segments in order; a segment's
 // fields are read from the plan once, when the cursor enters it.
-template <bool kWin>
+template <Sees kSees>
 struct TileCursor {
+  static constexpr bool kWin = kSees == Sees::kWindow, kTree = kSees == Sees::kTree;
   const int32_t* segs;
   int s, s_end, pg, pb, pe, row, vis, slot;
-  int sinks, wlo;  // windowed: the segment's window starts at wlo
+  int sinks, wlo;  // windowed: the segment's window starts at wlo; tree: its nodes start at wlo
   WindowTiles w;
+  const uint64_t* masks;  // tree: `words` words of each row
+  int words;
   __device__ __forceinline__ void init(const int32_t* sg, int sb, int se, int sinks_ = 0) {
     segs = sg;
     s = sb;
     s_end = se;
     sinks = sinks_;
     if (s < s_end) load();
+  }
+  __device__ __forceinline__ void init(const int32_t* sg, int sb, int se, const WindowArgs* win, const TreeArgs* tree) {
+    if (kTree) {
+      masks = tree->masks;
+      words = tree->words;
+    }
+    init(sg, sb, se, kWin ? win->sinks : 0);
   }
   __device__ __forceinline__ void load() {
     // {row, b, page_begin, page_end} and {visible, out_slot, 0, 0}: 16-byte aligned
@@ -209,14 +223,29 @@ struct TileCursor {
     vis = hi.x;
     slot = hi.y;
     pg = pb;
-    if (kWin) {
-      wlo = hi.z;
-      w = window_tiles(wlo, sinks);
-    }
+    if (kWin || kTree) wlo = hi.z;
+    if (kWin) w = window_tiles(wlo, sinks);
   }
-  // Windowed: which of the current tile's 64 tokens the row sees, a bit each.
-  // [0, a) are sinks, [b, c) lie in the window.
+  __device__ __forceinline__ uint64_t mask_word(int i) const {
+    return i < words ? __ldg(reinterpret_cast<const unsigned long long*>(masks) + (int64_t)row * words + i) : 0ull;
+  }
+  // Windowed and tree: which of the current tile's 64 tokens the row sees, a
+  // bit each.  Windowed: [0, a) are sinks, [b, c) lie in the window.  Tree:
+  // the tokens before wlo, and node k at token wlo + k where bit k of the
+  // row's mask is set, up to the row's own node (token vis - 1).
   __device__ __forceinline__ uint64_t visible() const {
+    if constexpr (kTree) {
+      const int p0 = pg * kPage, k0 = p0 - wlo;  // the node of the tile's first token
+      uint64_t m;
+      if (k0 < 0) {
+        m = bits_below(-k0) | (k0 > -kPage ? mask_word(0) << -k0 : 0ull);
+      } else {
+        const int r = k0 & 63;
+        m = mask_word(k0 >> 6) >> r;
+        if (r) m |= mask_word((k0 >> 6) + 1) << (64 - r);
+      }
+      return m & bits_below(vis - p0);
+    }
     int a, b = 0, c = 0;
     if (pg < w.sink_tiles) {
       a = sinks - pg * kPage;
@@ -230,6 +259,7 @@ struct TileCursor {
   }
   // Whether the row may see less than the whole of the current tile.
   __device__ __forceinline__ bool edge() const {
+    if constexpr (kTree) return (pg + 1) * kPage > wlo;
     return pg <= w.sink_tiles || vis - (pg + w.skip) * kPage < kPage;
   }
   static __device__ __forceinline__ uint64_t bits_below(int n) {
@@ -269,9 +299,17 @@ __device__ __forceinline__ uint32_t as_u32(__half2 h) { return *reinterpret_cast
 // as in the full decode plus 1.7 row switches a cluster; 16 rows of 4112 tokens
 // of an FP8 cache 46 us (the code conversion's ring); one row of 516 tokens 13.7
 // us, of which 10 are one cluster's latency and 4 the combine.
-template <bool kF8, bool kWin>
+//
+// Sees::kTree: the rows are the nodes of drafted trees.  A tile that holds
+// nodes, or slots past the row's own, is an edge tile of the same kind: a
+// 64-bit mask of it is cut from the row's words, the scores that it hides are
+// set to -infinity and their latents cleared before P.V.  A row may see nothing
+// of a tile, and nothing at all: its maximum is then -infinity, its weights and
+// its sum 0, its output 0.
+template <bool kF8, Sees kSees>
 __device__ __forceinline__ void decode_body(const CUtensorMap& kv_map, const CUtensorMap& rope_map,
-                                            const DecodeArgs& a, const WindowArgs* win) {
+                                            const DecodeArgs& a, const WindowArgs* win, const TreeArgs* tree) {
+  constexpr bool kWin = kSees == Sees::kWindow, kTree = kSees == Sees::kTree, kMasked = kWin || kTree;
   using L = Layout<kF8>;
   constexpr int kStages = L::kStages, kStageBytes = L::kStageBytes, kThreads = L::kThreads;
   constexpr int kPvWarp = L::kPvWarp, kSoftWarp0 = L::kSoftWarp0, kConvWarp0 = L::kConvWarp0;
@@ -351,6 +389,10 @@ __device__ __forceinline__ void decode_body(const CUtensorMap& kv_map, const CUt
         const int64_t last = pe - 1 + (int64_t)(pe > w.sink_tiles ? w.skip : 0);
         good = lo >= 0 && (lo == 0 || (lo > win->sinks && lo < vis)) && last < a.max_pages &&
                last * kPage < (int64_t)vis;
+      }
+      if (kTree && good) {
+        const int32_t first = sg[6];  // the row's node is number vis - 1 - first of its tree
+        good = first >= 0 && first < vis && vis - first <= 64 * tree->words;
       }
     }
     if (!good) {
@@ -485,7 +527,7 @@ __device__ __forceinline__ void decode_body(const CUtensorMap& kv_map, const CUt
     // QK^T issue (the tensor pipe throttles it) never delays P·V, nor the
     // other way round; the two streams share only the tensor pipe.
     if (lane == 0) {
-      TileCursor<false> cq;
+      TileCursor<Sees::kAll> cq;
       cq.init(a.segs, s_begin, s_end);
       // Stage-0 descriptors: latent chunks (K-major) and the RoPE half,
       // advanced by adding the byte offset >> 4 to the start-address field
@@ -556,14 +598,14 @@ __device__ __forceinline__ void decode_body(const CUtensorMap& kv_map, const CUt
   };
   auto role_pv = [&]() {
     // ---------------------------------------------------------------- P·V issue
-    // Windowed: the whole warp walks the tiles, lane 0 issues, and a tile's
+    // Masked: the whole warp walks the tiles, lane 0 issues, and a tile's
     // masked tokens have their latents cleared once QK^T has read the page,
     // while the softmax is at work: their P is 0, but 0 times an infinity or a
     // NaN is not 0.  (128 rows of 2112 tokens: 93.9 us, 92.9 without the
     // clearing, 95.8 with the softmax warps clearing.)
-    if (kWin || lane == 0) {
-      TileCursor<kWin> cp;
-      cp.init(a.segs, s_begin, s_end, kWin ? win->sinks : 0);
+    if (kMasked || lane == 0) {
+      TileCursor<kSees> cp;
+      cp.init(a.segs, s_begin, s_end, win, tree);
       // The latent chunks read MN-major for P·V, and the ones tile.
       const uint64_t vdesc0 = sdesc_sw128(base + kOffKV, 8192, 1024);
       const uint64_t odesc0 = sdesc_sw128(base + kOffOnes, 16, 1024);
@@ -592,7 +634,7 @@ __device__ __forceinline__ void decode_body(const CUtensorMap& kv_map, const CUt
       };
       for (uint32_t tp = 0; cp.valid(); ++tp) {
         bool ok = true;
-        if constexpr (kWin) {
+        if constexpr (kMasked) {
           if (cp.edge() && !clear_masked(cp.visible(), tp)) break;
           if (lane == 0) ok = issue(tp);
           ok = __shfl_sync(0xffffffffu, (int)ok, 0) != 0;
@@ -629,11 +671,11 @@ __device__ __forceinline__ void decode_body(const CUtensorMap& kv_map, const CUt
     const uint32_t ct = (uint32_t)lane >> 3, cc = (uint32_t)lane & 7u;
     constexpr int kRows = kPage / kConvWarps;
     constexpr int kBatch = 4;
-    // Windowed: the scales of tokens that the row does not see are not judged.
+    // Masked: the scales of tokens that the row does not see are not judged.
     // Whether this warp's scales of tile t outside the range are all such.
     auto masked_scales_only = [&](uint32_t t, uint32_t stage) {
-      TileCursor<kWin> cv;
-      cv.init(a.segs, s_begin, s_end, win->sinks);
+      TileCursor<kSees> cv;
+      cv.init(a.segs, s_begin, s_end, win, tree);
       uint32_t at = 0;
       while (cv.valid() && at + (uint32_t)(cv.pe - cv.pb) <= t) {
         at += (uint32_t)(cv.pe - cv.pb);
@@ -677,7 +719,7 @@ __device__ __forceinline__ void decode_body(const CUtensorMap& kv_map, const CUt
         fac[j] = fp8_f16_factor(ld_shared_f32(stage + kF8ScaleOff + 4u * r), ok_j);
         in_range = in_range && ok_j;
       }
-      if constexpr (kWin) {
+      if constexpr (kMasked) {
         if (!in_range) in_range = masked_scales_only(t, stage);
       }
       if (!in_range && lane == 0) atomicOr(err, (int32_t)MLA_DEVERR_FP8_RANGE);  // warp-uniform
@@ -801,10 +843,10 @@ __device__ __forceinline__ void decode_body(const CUtensorMap& kv_map, const CUt
     // partial to the peer, and load the next segment's Q if tile
     // t ends a segment (its QK^T was the segment's last).  `own` keeps the
     // rounded values.
-    auto fetch_push = [&](uint32_t t, const TileCursor<kWin>& c, uint32_t (&own)[kWords]) -> bool {
+    auto fetch_push = [&](uint32_t t, const TileCursor<kSees>& c, uint32_t (&own)[kWords]) -> bool {
       bool w = wait_phase<false, true>(BAR(B_S_FULL0 + (t & 1u)), (t >> 1) & 1u, err, abort_flag, a.wait_limit, a.wait_every);
       if (!__all_sync(0xffffffffu, w)) return false;
-      if (kWin && wg_leader) scored[wg] = (int32_t)t;
+      if (kMasked && wg_leader) scored[wg] = (int32_t)t;
       tc_fence_after();
       {
         uint32_t r[64];
@@ -852,8 +894,8 @@ __device__ __forceinline__ void decode_body(const CUtensorMap& kv_map, const CUt
         mbar_arrive_expect_tx(BAR(B_X_FULL0 + t), (uint32_t)kXBytes);
         armed[t] = (int32_t)t;
       }
-    TileCursor<kWin> cf;  // this warpgroup's tile
-    cf.init(a.segs, s_begin, s_end, kWin ? win->sinks : 0);
+    TileCursor<kSees> cf;  // this warpgroup's tile
+    cf.init(a.segs, s_begin, s_end, win, tree);
     if (wg == 1 && cf.valid()) cf.next();
     if (wg == 0 && G > 0) load_q(s_begin);
     uint32_t own[kWords];
@@ -888,7 +930,7 @@ __device__ __forceinline__ void decode_body(const CUtensorMap& kv_map, const CUt
       }
 
       // ---- causal/length mask and the row max of this tile
-      if constexpr (kWin) {
+      if constexpr (kMasked) {
         if (cf.edge()) {
           const uint64_t seen = cf.visible();
 #pragma unroll
@@ -952,7 +994,9 @@ __device__ __forceinline__ void decode_body(const CUtensorMap& kv_map, const CUt
       // ---- P = 2^(c2 (s - m)) in fp16 pairs (one fused multiply-add for the
       //      exponent), stored as bf16 for the tensor core (the FP8 cache's
       //      f16 operands take the fp16 P as it is)
-      const __half2 mc2 = __float2half2_rn(-m * c2);
+      // Tree: with nothing seen so far m is -infinity, and every exponent is
+      // -infinity - 0.
+      const __half2 mc2 = __float2half2_rn(kTree && m == -INFINITY ? 0.f : -m * c2);
 #pragma unroll
       for (int j = 0; j < kWords; ++j) {
         const uint32_t p16 = ex2_f16x2(as_u32(__hfma2(as_h2(own[j]), c2h, mc2)));
@@ -999,7 +1043,7 @@ __device__ __forceinline__ void decode_body(const CUtensorMap& kv_map, const CUt
         }
         tc_fence_after();
         const float lt = __uint_as_float(tmem_ld1_sync(tl + kColSum));
-        const float inv = 1.f / lt;
+        const float inv = kTree && lt == 0.f ? 0.f : 1.f / lt;
         // The rows lie 1 KB (partials 2 KB) apart, so a thread's own stores
         // would write 32 lines an instruction: the warp's rows cross through
         // its part of tile g's exchange buffer, 128 bytes of each row a round,
@@ -1148,14 +1192,21 @@ template <bool kF8>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<kF8>::kThreads, 1)
     decode_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constant__ CUtensorMap rope_map,
                   const DecodeArgs a) {
-  decode_body<kF8, false>(kv_map, rope_map, a, nullptr);
+  decode_body<kF8, Sees::kAll>(kv_map, rope_map, a, nullptr, nullptr);
 }
 
 template <bool kF8>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<kF8>::kThreads, 1)
     decode_window_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constant__ CUtensorMap rope_map,
                          const DecodeArgs a, const __grid_constant__ WindowArgs win) {
-  decode_body<kF8, true>(kv_map, rope_map, a, &win);
+  decode_body<kF8, Sees::kWindow>(kv_map, rope_map, a, &win, nullptr);
+}
+
+template <bool kF8>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<kF8>::kThreads, 1)
+    decode_tree_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constant__ CUtensorMap rope_map,
+                       const DecodeArgs a, const TreeArgs tree) {
+  decode_body<kF8, Sees::kTree>(kv_map, rope_map, a, nullptr, &tree);
 }
 
 }  // namespace decode
@@ -1177,6 +1228,17 @@ static cudaError_t run_window(const CUtensorMap& kv_map, const CUtensorMap& rope
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
   kern<<<2 * num_clusters, decode::Layout<kF8>::kThreads, smem, stream>>>(kv_map, rope_map, args, window);
+  return cudaGetLastError();
+}
+
+template <bool kF8>
+static cudaError_t run_tree(const CUtensorMap& kv_map, const CUtensorMap& rope_map, const DecodeArgs& args,
+                            const TreeArgs& tree, int num_clusters, cudaStream_t stream) {
+  auto* kern = decode::decode_tree_kernel<kF8>;
+  constexpr int smem = decode::Layout<kF8>::kSmemBytes;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  kern<<<2 * num_clusters, decode::Layout<kF8>::kThreads, smem, stream>>>(kv_map, rope_map, args, tree);
   return cudaGetLastError();
 }
 
@@ -1214,6 +1276,12 @@ cudaError_t launch_decode_window(const CUtensorMap& kv_map, const CUtensorMap& r
                                  const WindowArgs& window, int num_clusters, bool fp8, cudaStream_t stream) {
   return fp8 ? run_window<true>(kv_map, rope_map, args, window, num_clusters, stream)
              : run_window<false>(kv_map, rope_map, args, window, num_clusters, stream);
+}
+
+cudaError_t launch_decode_tree(const CUtensorMap& kv_map, const CUtensorMap& rope_map, const DecodeArgs& args,
+                               const TreeArgs& tree, int num_clusters, bool fp8, cudaStream_t stream) {
+  return fp8 ? run_tree<true>(kv_map, rope_map, args, tree, num_clusters, stream)
+             : run_tree<false>(kv_map, rope_map, args, tree, num_clusters, stream);
 }
 
 }  // namespace mla

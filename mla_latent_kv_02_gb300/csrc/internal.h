@@ -21,7 +21,7 @@ mla_status set_last_error(mla_status s, const char* message);
 //   [8..15] reserved
 //   seg_off   at kPlanHeader, num_clusters + 1 entries
 //   segments  at seg_base, num_segments x 8: {row, b, page_begin, page_end,
-//             visible, out_slot (-1 = final), window's first token, 0}
+//             visible, out_slot (-1 = final), window's or tree's first token, 0}
 //   split rows at split_base, num_split_rows x 4: {row, slot_begin, n_slots, 0}
 constexpr int kPlanHeader = 16;
 constexpr int kSegWords = 8;
@@ -174,6 +174,55 @@ struct WindowArgs {
   int32_t split;                     // window_split(sinks)
 };
 
+// What the tree decode takes beside DecodeArgs: `words` 64-bit words of mask
+// for each row.  A plan segment carries the tree's first token in word 6.
+struct TreeArgs {
+  const uint64_t* masks;
+  int32_t words;
+};
+
+// Trees of drafted nodes, a sequence each (tree.cu): sequence b's nodes are
+// rows [q_starts[b], q_starts[b + 1]) of T, its last ones of seq_lens[b] tokens.
+struct TreeLayoutArgs {
+  const int32_t* parents;
+  const int32_t* q_starts;
+  const int32_t* seq_lens;
+  const int32_t* block_table;  // with slots
+  int64_t num_pages;
+  int32_t max_pages;
+  int32_t B;
+  int32_t T;
+  int32_t words;
+  uint64_t* masks;
+  int32_t* positions;          // or null
+  int64_t* slots;              // or null
+  int32_t* dev_err;
+};
+// The caches of a model's layers as 16-byte pieces of a token's row, and for
+// the FP8 cache a scale beside each row (else null).  Strides in bytes.
+struct LayerCaches {
+  uint8_t* rows;
+  float* scales;
+  int64_t row_stride;
+  int64_t scale_stride;
+  int64_t num_pages;
+  int32_t layers;
+};
+struct TreeCompactArgs {
+  LayerCaches c;
+  const int32_t* block_table;
+  const uint64_t* masks;
+  const int32_t* q_starts;
+  const int32_t* seq_lens;
+  const int32_t* accepted;
+  int32_t max_pages;
+  int32_t B;
+  int32_t T;
+  int32_t words;
+  int32_t* new_lens;
+  int32_t* dev_err;
+};
+
 // Launches `kern` so that its blocks may take their places while the kernel
 // before it on the stream still runs (programmatic: only if that kernel allows
 // it); every block must call grid_dependency_wait before it reads or writes
@@ -205,6 +254,8 @@ cudaError_t launch_decode(const CUtensorMap& kv_map, const CUtensorMap& rope_map
                           int num_clusters, bool fp8, cudaStream_t stream);
 cudaError_t launch_decode_window(const CUtensorMap& kv_map, const CUtensorMap& rope_map, const DecodeArgs& args,
                                  const WindowArgs& window, int num_clusters, bool fp8, cudaStream_t stream);
+cudaError_t launch_decode_tree(const CUtensorMap& kv_map, const CUtensorMap& rope_map, const DecodeArgs& args,
+                               const TreeArgs& tree, int num_clusters, bool fp8, cudaStream_t stream);
 cudaError_t launch_combine(const CombineArgs& args, int num_split_rows, cudaStream_t stream);
 
 cudaError_t launch_kv_append(const uint16_t* c_kv_new, const uint16_t* k_r_new, const int64_t* slots, int32_t n,
@@ -243,6 +294,13 @@ cudaError_t launch_gather_batch(const uint16_t* kv_cache, int64_t num_pages, con
 
 cudaError_t launch_gather_window(const void* cache, const float* scales, bool fp8, const WindowGather& g,
                                  uint16_t* out, cudaStream_t stream);
+
+cudaError_t launch_tree_layout(const TreeLayoutArgs& args, cudaStream_t stream);
+// row_bytes: 1152, 640 or 416
+cudaError_t launch_tree_compact(const TreeCompactArgs& args, int row_bytes, cudaStream_t stream);
+// Pages src[i] to dst[i] in every layer (host arrays of n, read before the call returns).
+cudaError_t launch_copy_pages(const LayerCaches& c, int row_bytes, const int32_t* src, const int32_t* dst, int32_t n,
+                              cudaStream_t stream);
 
 // Decompress-branch expansion: K_c and V_c in one pass (head-major outputs).
 // early: it may start while the kernel before it on the stream still runs.

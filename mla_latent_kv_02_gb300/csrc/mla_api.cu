@@ -95,16 +95,26 @@ struct PlanRow {
   int32_t b;
   int32_t visible;
   int32_t npages;  // tiles the row reads
-  int32_t lo;      // the window's first token; 0: the row sees every token up to its own
+  int32_t lo;      // the window's first token (0: the row sees every token up to its own), or the tree's
 };
 
 // Minimum 64-token tiles per cluster: below it, the per-range fixed costs
 // (query load, epilogue, a combine partial) outweigh the added parallelism.
 constexpr int64_t kMinTilesPerCluster = 2;
 
-// window == 0: full attention; otherwise a sliding window with sinks.
+// What the planned rows see.  window == 0: every token up to the row's own;
+// otherwise a sliding window with sinks.  tree: the rows are the nodes of
+// trees, masked within them.
+struct PlanKind {
+  int32_t window = 0;
+  int32_t sinks = 0;
+  bool tree = false;
+  uint32_t magic() const { return tree ? MLA_TREE_PLAN_MAGIC : window > 0 ? MLA_WINDOW_PLAN_MAGIC : MLA_PLAN_MAGIC; }
+};
+
 mla_status build_plan(const int32_t* seq_lens, const int32_t* q_lens, int32_t B, int32_t num_clusters,
-                      int32_t* out, size_t out_words, mla_plan_info* info, int32_t window = 0, int32_t sinks = 0) {
+                      int32_t* out, size_t out_words, mla_plan_info* info, const PlanKind& kind = {}) {
+  const int32_t window = kind.window, sinks = kind.sinks;
   if (B < 0) return fail(MLA_ERR_INVALID_ARG, "B = %d is negative", B);
   if (B > 0) {
     CHECK_PTR(seq_lens);
@@ -118,10 +128,12 @@ mla_status build_plan(const int32_t* seq_lens, const int32_t* q_lens, int32_t B,
     const int32_t n = seq_lens[b], q = q_lens[b];
     if (n < 1) return fail(MLA_ERR_INVALID_ARG, "seq_lens[%d] = %d < 1", b, n);
     if (q < 0 || q > n) return fail(MLA_ERR_INVALID_ARG, "q_lens[%d] = %d outside [0, seq_len = %d]", b, q, n);
+    if (kind.tree && q > MLA_TREE_MAX_NODES)
+      return fail(MLA_ERR_UNSUPPORTED, "q_lens[%d] = %d: a tree has at most %d nodes", b, q, MLA_TREE_MAX_NODES);
     max_pages = std::max<int32_t>(max_pages, (n - 1) / MLA_PAGE_SIZE + 1);
     for (int32_t i = 0; i < q; ++i) {
       const int32_t vis = n - q + i + 1;
-      int32_t np = (vis - 1) / MLA_PAGE_SIZE + 1, lo = 0;
+      int32_t np = (vis - 1) / MLA_PAGE_SIZE + 1, lo = kind.tree ? n - q : 0;
       if (window > 0 && vis - (int64_t)window > (int64_t)sinks) {  // tokens between the sinks and the window
         lo = vis - window;
         np -= mla::window_tiles(lo, sinks).skip;
@@ -210,7 +222,7 @@ mla_status build_plan(const int32_t* seq_lens, const int32_t* q_lens, int32_t B,
     return fail(MLA_ERR_INVALID_ARG, "plan buffer holds %zu bytes, %lld needed", out_words * 4,
                 (long long)L.words * 4);
   std::fill(out, out + L.words, 0);
-  const uint32_t magic = window > 0 ? MLA_WINDOW_PLAN_MAGIC : MLA_PLAN_MAGIC;
+  const uint32_t magic = kind.magic();
   out[0] = (int32_t)magic;
   out[1] = (int32_t)T;
   out[2] = B;
@@ -246,6 +258,16 @@ mla_status build_plan(const int32_t* seq_lens, const int32_t* q_lens, int32_t B,
   return MLA_OK;
 }
 
+// A call whose body may run out of host memory: no exception passes.
+template <typename F>
+mla_status no_throw(F&& body) {
+  try {
+    return body();
+  } catch (const std::bad_alloc&) {
+    return fail(MLA_ERR_NO_SPACE, "out of host memory");
+  }
+}
+
 size_t workspace_bytes_for(int64_t partials) {
   return (size_t)partials * (MLA_NUM_HEADS * MLA_LATENT_DIM * 4 + MLA_NUM_HEADS * 4);
 }
@@ -266,7 +288,7 @@ PlanLayout plan_layout(int64_t num_clusters, int64_t num_segments, int64_t num_s
 }  // namespace mla
 
 struct mla_pool {
-  std::vector<uint8_t> used;
+  std::vector<int32_t> refs;  // holders of each page, 0: free
   int32_t free_count = 0;
 };
 
@@ -329,11 +351,29 @@ mla_status mla_kv_bytes(int64_t layers, int64_t dc, int64_t dr, int64_t elem_byt
 mla_status mla_pool_create(int32_t num_pages, mla_pool** out) {
   CHECK_PTR(out);
   if (num_pages < 1) return fail(MLA_ERR_INVALID_ARG, "num_pages = %d < 1", num_pages);
-  auto* p = new (std::nothrow) mla_pool();
-  if (!p) return fail(MLA_ERR_NO_SPACE, "out of host memory");
-  p->used.assign((size_t)num_pages, 0);
-  p->free_count = num_pages;
-  *out = p;
+  return no_throw([&] {
+    auto p = std::make_unique<mla_pool>();
+    p->refs.assign((size_t)num_pages, 0);
+    p->free_count = num_pages;
+    *out = p.release();
+    return MLA_OK;
+  });
+}
+
+// Takes n free pages, lowest first; the caller has seen that there are so many.
+static void pool_take(mla_pool* pool, int32_t n, int32_t* ids) {
+  int32_t k = 0;
+  for (size_t i = 0; i < pool->refs.size() && k < n; ++i)
+    if (!pool->refs[i]) {
+      pool->refs[i] = 1;
+      ids[k++] = (int32_t)i;
+    }
+  pool->free_count -= n;
+}
+
+static mla_status pool_held(const mla_pool* pool, int32_t id) {
+  if (id < 0 || (size_t)id >= pool->refs.size()) return fail(MLA_ERR_INVALID_ARG, "page id %d out of range", id);
+  if (!pool->refs[id]) return fail(MLA_ERR_INVALID_ARG, "page id %d is not allocated", id);
   return MLA_OK;
 }
 
@@ -344,13 +384,7 @@ mla_status mla_pool_alloc(mla_pool* pool, int32_t n, int32_t* ids) {
   CHECK_PTR(ids);
   if (n > pool->free_count)
     return fail(MLA_ERR_NO_SPACE, "%d pages requested, %d free", n, pool->free_count);
-  int32_t k = 0;
-  for (size_t i = 0; i < pool->used.size() && k < n; ++i)
-    if (!pool->used[i]) {
-      pool->used[i] = 1;
-      ids[k++] = (int32_t)i;
-    }
-  pool->free_count -= n;
+  pool_take(pool, n, ids);
   return MLA_OK;
 }
 
@@ -359,17 +393,136 @@ mla_status mla_pool_free(mla_pool* pool, const int32_t* ids, int32_t n) {
   if (n < 0) return fail(MLA_ERR_INVALID_ARG, "n = %d < 0", n);
   if (n == 0) return MLA_OK;
   CHECK_PTR(ids);
-  std::vector<uint8_t> seen(pool->used.size(), 0);
+  return no_throw([&] {
+    std::vector<uint8_t> seen(pool->refs.size(), 0);
+    for (int32_t i = 0; i < n; ++i) {
+      const mla_status s = pool_held(pool, ids[i]);
+      if (s != MLA_OK) return s;
+      if (seen[ids[i]]) return fail(MLA_ERR_INVALID_ARG, "page id %d repeated", ids[i]);
+      seen[ids[i]] = 1;
+    }
+    for (int32_t i = 0; i < n; ++i)
+      if (--pool->refs[ids[i]] == 0) ++pool->free_count;
+    return MLA_OK;
+  });
+}
+
+mla_status mla_pool_retain(mla_pool* pool, const int32_t* ids, int32_t n) {
+  CHECK_PTR(pool);
+  if (n < 0) return fail(MLA_ERR_INVALID_ARG, "n = %d < 0", n);
+  if (n == 0) return MLA_OK;
+  CHECK_PTR(ids);
   for (int32_t i = 0; i < n; ++i) {
-    const int32_t id = ids[i];
-    if (id < 0 || (size_t)id >= pool->used.size()) return fail(MLA_ERR_INVALID_ARG, "page id %d out of range", id);
-    if (!pool->used[id]) return fail(MLA_ERR_INVALID_ARG, "page id %d is not allocated", id);
-    if (seen[id]) return fail(MLA_ERR_INVALID_ARG, "page id %d repeated", id);
-    seen[id] = 1;
+    const mla_status s = pool_held(pool, ids[i]);
+    if (s != MLA_OK) return s;
+    if (pool->refs[ids[i]] > INT32_MAX - n) return fail(MLA_ERR_INVALID_ARG, "page id %d has too many holders", ids[i]);
   }
-  for (int32_t i = 0; i < n; ++i) pool->used[ids[i]] = 0;
-  pool->free_count += n;
+  for (int32_t i = 0; i < n; ++i) ++pool->refs[ids[i]];
   return MLA_OK;
+}
+
+mla_status mla_pool_refs(const mla_pool* pool, int32_t id, int32_t* out) {
+  CHECK_PTR(pool);
+  CHECK_PTR(out);
+  if (id < 0 || (size_t)id >= pool->refs.size()) return fail(MLA_ERR_INVALID_ARG, "page id %d out of range", id);
+  *out = pool->refs[id];
+  return MLA_OK;
+}
+
+mla_status mla_pool_fork(mla_pool* pool, const int32_t* parent, int32_t n_tokens, int32_t n_children,
+                         int32_t max_pages, int32_t* children, int32_t* src, int32_t* dst, int32_t* n_copies) {
+  CHECK_PTR(pool);
+  CHECK_PTR(n_copies);
+  if (n_tokens < 0 || n_children < 0 || max_pages < 0)
+    return fail(MLA_ERR_INVALID_ARG, "n_tokens = %d, n_children = %d, max_pages = %d: negative", n_tokens, n_children,
+                max_pages);
+  const int32_t full = n_tokens / MLA_PAGE_SIZE, pages = full + (n_tokens % MLA_PAGE_SIZE != 0);
+  if (pages > max_pages)
+    return fail(MLA_ERR_INVALID_ARG, "n_tokens = %d needs more than max_pages = %d pages", n_tokens, max_pages);
+  *n_copies = 0;
+  if (n_children == 0) return MLA_OK;
+  const int32_t copies = pages > full ? n_children : 0;
+  if (max_pages > 0) CHECK_PTR(children);
+  if (pages > 0) CHECK_PTR(parent);
+  if (copies) {
+    CHECK_PTR(src);
+    CHECK_PTR(dst);
+  }
+  return no_throw([&] {
+    const std::vector<int32_t> held(parent, parent + pages);  // `children` may hold the parent's row
+    std::vector<int32_t> sorted(held);
+    std::sort(sorted.begin(), sorted.end());
+    for (int32_t k = 0; k < pages; ++k) {
+      const mla_status s = pool_held(pool, held[k]);
+      if (s != MLA_OK) return s;
+      if (k && sorted[k] == sorted[k - 1]) return fail(MLA_ERR_INVALID_ARG, "page id %d repeated", sorted[k]);
+      if (pool->refs[held[k]] > INT32_MAX - n_children)
+        return fail(MLA_ERR_INVALID_ARG, "page id %d has too many holders", held[k]);
+    }
+    if (copies > pool->free_count)
+      return fail(MLA_ERR_NO_SPACE, "%d pages requested, %d free", copies, pool->free_count);
+    std::vector<int32_t> fresh((size_t)copies);
+    if (copies) pool_take(pool, copies, fresh.data());
+    for (int32_t i = 0; i < n_children; ++i) {
+      int32_t* row = children + (int64_t)i * max_pages;
+      std::fill(row, row + max_pages, -1);
+      for (int32_t k = 0; k < full; ++k) row[k] = held[k];
+      if (copies) {
+        row[full] = fresh[i];
+        src[i] = held[full];
+        dst[i] = fresh[i];
+      }
+    }
+    for (int32_t k = 0; k < full; ++k) pool->refs[held[k]] += n_children;
+    *n_copies = copies;
+    return MLA_OK;
+  });
+}
+
+mla_status mla_pool_compact(mla_pool* pool, int32_t max_moves, int32_t* src, int32_t* dst, int32_t* n_moves) {
+  CHECK_PTR(pool);
+  CHECK_PTR(n_moves);
+  if (max_moves < 0) return fail(MLA_ERR_INVALID_ARG, "max_moves = %d < 0", max_moves);
+  if (max_moves > 0) {
+    CHECK_PTR(src);
+    CHECK_PTR(dst);
+  }
+  int32_t n = 0;
+  int64_t lo = 0, hi = (int64_t)pool->refs.size() - 1;
+  while (n < max_moves) {
+    while (lo < hi && pool->refs[lo]) ++lo;
+    while (lo < hi && !pool->refs[hi]) --hi;
+    if (lo >= hi) break;
+    std::swap(pool->refs[lo], pool->refs[hi]);
+    src[n] = (int32_t)hi;
+    dst[n++] = (int32_t)lo;
+  }
+  *n_moves = n;
+  return MLA_OK;
+}
+
+mla_status mla_remap_pages(int32_t* block_table, int64_t entries, const int32_t* src, const int32_t* dst, int32_t n) {
+  if (n < 0 || entries < 0)
+    return fail(MLA_ERR_INVALID_ARG, "n = %d, entries = %lld: negative", n, (long long)entries);
+  if (n == 0 || entries == 0) return MLA_OK;
+  CHECK_PTR(block_table);
+  CHECK_PTR(src);
+  CHECK_PTR(dst);
+  return no_throw([&] {
+    std::vector<std::pair<int32_t, int32_t>> moves((size_t)n);
+    for (int32_t i = 0; i < n; ++i) {
+      if (src[i] < 0 || dst[i] < 0) return fail(MLA_ERR_INVALID_ARG, "move %d: a page id is negative", i);
+      moves[i] = {src[i], dst[i]};
+    }
+    std::sort(moves.begin(), moves.end());
+    for (int32_t i = 1; i < n; ++i)
+      if (moves[i].first == moves[i - 1].first) return fail(MLA_ERR_INVALID_ARG, "page id %d repeated", moves[i].first);
+    for (int64_t i = 0; i < entries; ++i) {
+      const auto at = std::lower_bound(moves.begin(), moves.end(), std::make_pair(block_table[i], INT32_MIN));
+      if (at != moves.end() && at->first == block_table[i]) block_table[i] = at->second;
+    }
+    return MLA_OK;
+  });
 }
 
 mla_status mla_pool_available(const mla_pool* pool, int32_t* out) {
@@ -1204,6 +1357,167 @@ mla_status mla_pack_w4(const void* w, int32_t K, int32_t N, int32_t group, void*
   return MLA_OK;
 }
 
+// ------------------------------------------------------------------ pages and trees
+// The caches of `layers` layers: pointers, strides and sizes.
+static mla_status check_layers(const mla::LayerCaches& c, int row_bytes, bool fp8) {
+  CHECK_PTR(c.rows);
+  CHECK_ALIGN16(c.rows);
+  if (c.num_pages < 1 || c.num_pages * MLA_PAGE_SIZE > (int64_t)INT32_MAX)
+    return fail(MLA_ERR_INVALID_ARG, "num_pages = %lld outside [1, 2^31/64)", (long long)c.num_pages);
+  if (c.layers < 1 || c.layers > 65535) return fail(MLA_ERR_INVALID_ARG, "layers = %d outside [1, 65535]", c.layers);
+  if (fp8) {
+    CHECK_PTR(c.scales);
+    CHECK_ALIGN16(c.scales);
+  }
+  for (int i = 0; i < (fp8 ? 2 : 1) && c.layers > 1; ++i) {
+    const int64_t stride = i ? c.scale_stride : c.row_stride;
+    const int64_t least = c.num_pages * MLA_PAGE_SIZE * (i ? 4 : row_bytes);
+    if (stride % 16) return fail(MLA_ERR_MISALIGNED, "a layer stride of %lld bytes is not a multiple of 16", (long long)stride);
+    if (stride < least || stride > INT64_MAX / c.layers)
+      return fail(MLA_ERR_INVALID_ARG, "a layer stride of %lld bytes: a layer's pages take %lld", (long long)stride,
+                  (long long)least);
+  }
+  return MLA_OK;
+}
+
+static mla_status copy_pages(const mla::LayerCaches& c, int row_bytes, bool fp8, const int32_t* src, const int32_t* dst,
+                             int32_t n, void* stream) {
+  if (n < 0) return fail(MLA_ERR_INVALID_ARG, "n = %d < 0", n);
+  if (n == 0) return MLA_OK;
+  CHECK_PTR(src);
+  CHECK_PTR(dst);
+  mla_status s = check_layers(c, row_bytes, fp8);
+  if (s != MLA_OK) return s;
+  return no_throw([&] {
+    std::vector<uint8_t> role((size_t)c.num_pages, 0);  // 1: read, 2: written
+    for (int32_t i = 0; i < n; ++i) {
+      for (const int32_t id : {src[i], dst[i]})
+        if (id < 0 || id >= c.num_pages) return fail(MLA_ERR_INVALID_ARG, "copy %d: page id %d out of range", i, id);
+      role[src[i]] |= 1;
+      if (role[dst[i]] & 2) return fail(MLA_ERR_INVALID_ARG, "copy %d: page %d is written twice", i, dst[i]);
+      role[dst[i]] |= 2;
+    }
+    for (int32_t i = 0; i < n; ++i)
+      if (role[src[i]] == 3) return fail(MLA_ERR_INVALID_ARG, "copy %d: page %d is read and written", i, src[i]);
+    cudaError_t e = mla::launch_copy_pages(c, row_bytes, src, dst, n, (cudaStream_t)stream);
+    if (e != cudaSuccess) return cuda_fail(e, "copy_pages launch");
+    return MLA_OK;
+  });
+}
+
+mla_status mla_copy_pages(void* kv_cache, int64_t num_pages, int32_t layers, int64_t layer_stride, const int32_t* src,
+                          const int32_t* dst, int32_t n, void* stream) {
+  return copy_pages({(uint8_t*)kv_cache, nullptr, layer_stride, 0, num_pages, layers}, (int)kRowBytes, false, src, dst, n,
+                    stream);
+}
+
+mla_status mla_copy_pages_fp8(void* rows, float* scales, int64_t num_pages, int32_t layers, int64_t row_stride,
+                              int64_t scale_stride, const int32_t* src, const int32_t* dst, int32_t n, void* stream) {
+  return copy_pages({(uint8_t*)rows, scales, row_stride, scale_stride, num_pages, layers}, MLA_FP8_ROW_BYTES, true, src,
+                    dst, n, stream);
+}
+
+mla_status mla_copy_pages_nvfp4(void* rows, int64_t num_pages, int32_t layers, int64_t layer_stride, const int32_t* src,
+                                const int32_t* dst, int32_t n, void* stream) {
+  return copy_pages({(uint8_t*)rows, nullptr, layer_stride, 0, num_pages, layers}, MLA_NVFP4_ROW_BYTES, false, src, dst,
+                    n, stream);
+}
+
+static mla_status tree_sizes(int32_t B, int32_t T, int32_t words) {
+  if (B < 0 || T < 0 || T > INT32_MAX / MLA_NUM_HEADS) return fail(MLA_ERR_INVALID_ARG, "B = %d, T = %d: out of range", B, T);
+  if (words < 1 || words > MLA_TREE_MAX_NODES / 64)
+    return fail(MLA_ERR_INVALID_ARG, "words = %d outside [1, %d]", words, MLA_TREE_MAX_NODES / 64);
+  return MLA_OK;
+}
+
+mla_status mla_tree_layout(const int32_t* parents, const int32_t* q_starts, const int32_t* seq_lens, int32_t B,
+                           int32_t T, int32_t words, const int32_t* block_table, int32_t max_pages, int64_t num_pages,
+                           uint64_t* masks, int32_t* positions, int64_t* slots, int32_t* dev_err, void* stream) {
+  mla_status s = tree_sizes(B, T, words);
+  if (s != MLA_OK) return s;
+  if (B == 0 || T == 0) return MLA_OK;
+  CHECK_PTR(parents);
+  CHECK_PTR(q_starts);
+  CHECK_PTR(seq_lens);
+  CHECK_PTR(masks);
+  CHECK_PTR(dev_err);
+  if (slots) {
+    CHECK_PTR(block_table);
+    if (num_pages < 1 || max_pages < 1) return fail(MLA_ERR_INVALID_ARG, "bad pool/table sizes");
+  }
+  if (!aligned(masks, 8) || !aligned(slots, 8)) return fail(MLA_ERR_MISALIGNED, "masks and slots must be 8-byte aligned");
+  if (!aligned(parents, 4) || !aligned(q_starts, 4) || !aligned(seq_lens, 4) || !aligned(block_table, 4) ||
+      !aligned(positions, 4) || !aligned(dev_err, 4))
+    return fail(MLA_ERR_MISALIGNED, "parents, q_starts, seq_lens, block_table, positions and dev_err must be 4-byte aligned");
+  const mla::TreeLayoutArgs a = {parents, q_starts, seq_lens, block_table, num_pages, max_pages, B, T, words,
+                                 masks, positions, slots, dev_err};
+  cudaError_t e = mla::launch_tree_layout(a, (cudaStream_t)stream);
+  if (e != cudaSuccess) return cuda_fail(e, "tree_layout launch");
+  return MLA_OK;
+}
+
+static mla_status tree_compact(const mla::LayerCaches& c, int row_bytes, bool fp8, const int32_t* block_table,
+                               int32_t max_pages, const uint64_t* masks, int32_t words, const int32_t* q_starts,
+                               const int32_t* seq_lens, const int32_t* accepted, int32_t B, int32_t T,
+                               int32_t* new_lens, int32_t* dev_err, void* stream) {
+  mla_status s = tree_sizes(B, T, words);
+  if (s != MLA_OK) return s;
+  if (B == 0) return MLA_OK;
+  s = check_layers(c, row_bytes, fp8);
+  if (s != MLA_OK) return s;
+  CHECK_PTR(block_table);
+  if (T > 0) CHECK_PTR(masks);
+  CHECK_PTR(q_starts);
+  CHECK_PTR(seq_lens);
+  CHECK_PTR(accepted);
+  CHECK_PTR(new_lens);
+  CHECK_PTR(dev_err);
+  if (max_pages < 1) return fail(MLA_ERR_INVALID_ARG, "max_pages = %d < 1", max_pages);
+  if (!aligned(masks, 8)) return fail(MLA_ERR_MISALIGNED, "masks is not 8-byte aligned");
+  if (!aligned(block_table, 4) || !aligned(q_starts, 4) || !aligned(seq_lens, 4) || !aligned(accepted, 4) ||
+      !aligned(new_lens, 4) || !aligned(dev_err, 4))
+    return fail(MLA_ERR_MISALIGNED, "block_table, q_starts, seq_lens, accepted, new_lens and dev_err must be 4-byte aligned");
+  const uintptr_t out = (uintptr_t)new_lens, len = (uintptr_t)B * 4;
+  const struct {
+    const void* p;
+    uintptr_t bytes;
+    const char* what;
+  } in[] = {{seq_lens, len, "seq_lens"}, {accepted, len, "accepted"}, {q_starts, len + 4, "q_starts"}};
+  for (const auto& x : in)
+    if (out < (uintptr_t)x.p + x.bytes && (uintptr_t)x.p < out + len)
+      return fail(MLA_ERR_INVALID_ARG, "new_lens and %s overlap", x.what);
+  const mla::TreeCompactArgs a = {c, block_table, masks, q_starts, seq_lens, accepted, max_pages, B, T, words,
+                                  new_lens, dev_err};
+  cudaError_t e = mla::launch_tree_compact(a, row_bytes, (cudaStream_t)stream);
+  if (e != cudaSuccess) return cuda_fail(e, "tree_compact launch");
+  return MLA_OK;
+}
+
+mla_status mla_tree_compact(void* kv_cache, int64_t num_pages, int32_t layers, int64_t layer_stride,
+                            const int32_t* block_table, int32_t max_pages, const uint64_t* masks, int32_t words,
+                            const int32_t* q_starts, const int32_t* seq_lens, const int32_t* accepted, int32_t B,
+                            int32_t T, int32_t* new_lens, int32_t* dev_err, void* stream) {
+  return tree_compact({(uint8_t*)kv_cache, nullptr, layer_stride, 0, num_pages, layers}, (int)kRowBytes, false, block_table,
+                      max_pages, masks, words, q_starts, seq_lens, accepted, B, T, new_lens, dev_err, stream);
+}
+
+mla_status mla_tree_compact_fp8(void* rows, float* scales, int64_t num_pages, int32_t layers, int64_t row_stride,
+                                int64_t scale_stride, const int32_t* block_table, int32_t max_pages,
+                                const uint64_t* masks, int32_t words, const int32_t* q_starts, const int32_t* seq_lens,
+                                const int32_t* accepted, int32_t B, int32_t T, int32_t* new_lens, int32_t* dev_err,
+                                void* stream) {
+  return tree_compact({(uint8_t*)rows, scales, row_stride, scale_stride, num_pages, layers}, MLA_FP8_ROW_BYTES, true,
+                      block_table, max_pages, masks, words, q_starts, seq_lens, accepted, B, T, new_lens, dev_err, stream);
+}
+
+mla_status mla_tree_compact_nvfp4(void* rows, int64_t num_pages, int32_t layers, int64_t layer_stride,
+                                  const int32_t* block_table, int32_t max_pages, const uint64_t* masks, int32_t words,
+                                  const int32_t* q_starts, const int32_t* seq_lens, const int32_t* accepted, int32_t B,
+                                  int32_t T, int32_t* new_lens, int32_t* dev_err, void* stream) {
+  return tree_compact({(uint8_t*)rows, nullptr, layer_stride, 0, num_pages, layers}, MLA_NVFP4_ROW_BYTES, false,
+                      block_table, max_pages, masks, words, q_starts, seq_lens, accepted, B, T, new_lens, dev_err, stream);
+}
+
 // ------------------------------------------------------------------ decode
 mla_status mla_decode_max_clusters(int32_t* out) {
   CHECK_PTR(out);
@@ -1233,9 +1547,9 @@ mla_status mla_decode_workspace_size(int32_t num_clusters, size_t* bytes) {
 
 // build_plan where an exception may not pass.
 static mla_status plan_checked(const int32_t* seq_lens, const int32_t* q_lens, int32_t B, int32_t num_clusters,
-                               int32_t* out, size_t out_words, mla_plan_info* info, int32_t window = 0, int32_t sinks = 0) {
+                               int32_t* out, size_t out_words, mla_plan_info* info, const PlanKind& kind = {}) {
   try {
-    return build_plan(seq_lens, q_lens, B, num_clusters, out, out_words, info, window, sinks);
+    return build_plan(seq_lens, q_lens, B, num_clusters, out, out_words, info, kind);
   } catch (const std::bad_alloc&) {
     return fail(MLA_ERR_NO_SPACE, "out of host memory");
   }
@@ -1265,8 +1579,8 @@ static mla_status not_captured(void* stream) {
 
 // A plan built in memory of the call's own and copied to plan_dev.
 static mla_status plan_upload(const int32_t* seq_lens_host, const int32_t* q_lens_host, int32_t B, int32_t num_clusters,
-                              void* plan_dev, size_t plan_bytes, mla_plan_info* info, void* stream, int32_t window = 0,
-                              int32_t sinks = 0) {
+                              void* plan_dev, size_t plan_bytes, mla_plan_info* info, void* stream,
+                              const PlanKind& kind = {}) {
   CHECK_PTR(plan_dev);
   CHECK_ALIGN16(plan_dev);
   if (B < 0) return fail(MLA_ERR_INVALID_ARG, "B = %d is negative", B);
@@ -1281,7 +1595,7 @@ static mla_status plan_upload(const int32_t* seq_lens_host, const int32_t* q_len
   const size_t words = std::min(plan_bytes, need) / 4;
   std::unique_ptr<int32_t[]> host(new (std::nothrow) int32_t[words + 1]);
   if (!host) return fail(MLA_ERR_NO_SPACE, "out of host memory");
-  s = plan_checked(seq_lens_host, q_lens_host, B, num_clusters, host.get(), words, info, window, sinks);
+  s = plan_checked(seq_lens_host, q_lens_host, B, num_clusters, host.get(), words, info, kind);
   if (s == MLA_OK) s = not_captured(stream);
   if (s != MLA_OK) return s;
   // Pageable source: the call returns once the data is staged, so `host` may go.
@@ -1304,7 +1618,8 @@ mla_status mla_window_plan_host(const int32_t* seq_lens, const int32_t* q_lens, 
   if (!aligned(plan_host, 4)) return fail(MLA_ERR_MISALIGNED, "plan_host is not 4-byte aligned");
   mla_status s = window_check(window, sinks);
   if (s != MLA_OK) return s;
-  s = plan_checked(seq_lens, q_lens, B, num_clusters, (int32_t*)plan_host, plan_bytes / 4, &info->plan, window, sinks);
+  s = plan_checked(seq_lens, q_lens, B, num_clusters, (int32_t*)plan_host, plan_bytes / 4, &info->plan,
+                   {window, sinks});
   if (s != MLA_OK) return s;
   info->window = window;
   info->sinks = sinks;
@@ -1317,22 +1632,51 @@ mla_status mla_window_plan(const int32_t* seq_lens_host, const int32_t* q_lens_h
   CHECK_PTR(info);
   mla_status s = window_check(window, sinks);
   if (s == MLA_OK)
-    s = plan_upload(seq_lens_host, q_lens_host, B, num_clusters, plan_dev, plan_bytes, &info->plan, stream, window, sinks);
+    s = plan_upload(seq_lens_host, q_lens_host, B, num_clusters, plan_dev, plan_bytes, &info->plan, stream,
+                    {window, sinks});
   if (s != MLA_OK) return s;
   info->window = window;
   info->sinks = sinks;
   return MLA_OK;
 }
 
-// window: the windowed decode's parameters, null for full attention.
+static int32_t most_nodes(const int32_t* q_lens, int32_t B) {
+  int32_t most = 0;
+  for (int32_t b = 0; b < B; ++b) most = std::max(most, q_lens[b]);
+  return most;
+}
+
+mla_status mla_tree_plan_host(const int32_t* seq_lens, const int32_t* q_lens, int32_t B, int32_t num_clusters,
+                              void* plan_host, size_t plan_bytes, mla_tree_info* info) {
+  CHECK_PTR(plan_host);
+  CHECK_PTR(info);
+  if (!aligned(plan_host, 4)) return fail(MLA_ERR_MISALIGNED, "plan_host is not 4-byte aligned");
+  mla_status s = plan_checked(seq_lens, q_lens, B, num_clusters, (int32_t*)plan_host, plan_bytes / 4, &info->plan,
+                              {0, 0, true});
+  if (s == MLA_OK) info->max_nodes = most_nodes(q_lens, B);
+  return s;
+}
+
+mla_status mla_tree_plan(const int32_t* seq_lens_host, const int32_t* q_lens_host, int32_t B, int32_t num_clusters,
+                         void* plan_dev, size_t plan_bytes, mla_tree_info* info, void* stream) {
+  CHECK_PTR(info);
+  mla_status s = plan_upload(seq_lens_host, q_lens_host, B, num_clusters, plan_dev, plan_bytes, &info->plan, stream,
+                             {0, 0, true});
+  if (s == MLA_OK) info->max_nodes = most_nodes(q_lens_host, B);
+  return s;
+}
+
+// window: the windowed decode's parameters; tree: the tree decode's; both null
+// for full attention.
 static mla_status decode_common(const void* q_abs, const void* q_r, const void* kv_cache, const float* kv_scales,
                                 int64_t num_pages, const int32_t* block_table, int32_t max_pages,
                                 const void* plan_dev, const mla_plan_info* info, float scale, void* workspace,
                                 size_t ws_bytes, void* o_lat, float* lse, int32_t* dev_err, void* stream,
-                                bool fp8, const mla_window_info* window = nullptr) {
+                                bool fp8, const mla_window_info* window = nullptr,
+                                const mla::TreeArgs* tree = nullptr) {
   CHECK_PTR(info);
-  if (info->magic != (window ? MLA_WINDOW_PLAN_MAGIC : MLA_PLAN_MAGIC))
-    return fail(MLA_ERR_INVALID_ARG, "info is not a %s plan summary", window ? "window" : "decode");
+  if (info->magic != (tree ? MLA_TREE_PLAN_MAGIC : window ? MLA_WINDOW_PLAN_MAGIC : MLA_PLAN_MAGIC))
+    return fail(MLA_ERR_INVALID_ARG, "info is not a %s plan summary", tree ? "tree" : window ? "window" : "decode");
   if (window) {
     const mla_status ws = window_check(window->window, window->sinks);
     if (ws != MLA_OK) return ws;
@@ -1345,6 +1689,10 @@ static mla_status decode_common(const void* q_abs, const void* q_r, const void* 
   CHECK_PTR(plan_dev);
   CHECK_PTR(o_lat);
   CHECK_PTR(dev_err);
+  if (tree) {
+    CHECK_PTR(tree->masks);
+    if (!aligned(tree->masks, 8)) return fail(MLA_ERR_MISALIGNED, "masks is not 8-byte aligned");
+  }
   CHECK_ALIGN16(q_abs);
   CHECK_ALIGN16(q_r);
   CHECK_ALIGN16(kv_cache);
@@ -1459,8 +1807,9 @@ static mla_status decode_common(const void* q_abs, const void* q_r, const void* 
   a.kv_scales = fp8 ? kv_scales : nullptr;
   a.wait_limit = g_decode_wait_limit.load(std::memory_order_relaxed);
   a.wait_every = a.wait_limit < (1ull << 20) ? 0u : 255u;
-  cudaError_t e = window ? mla::launch_decode_window(kv_map, rope_map, a, win, info->num_clusters, fp8, (cudaStream_t)stream)
-                         : mla::launch_decode(kv_map, rope_map, a, info->num_clusters, fp8, (cudaStream_t)stream);
+  cudaError_t e = tree     ? mla::launch_decode_tree(kv_map, rope_map, a, *tree, info->num_clusters, fp8, (cudaStream_t)stream)
+                  : window ? mla::launch_decode_window(kv_map, rope_map, a, win, info->num_clusters, fp8, (cudaStream_t)stream)
+                           : mla::launch_decode(kv_map, rope_map, a, info->num_clusters, fp8, (cudaStream_t)stream);
   if (e != cudaSuccess) return cuda_fail(e, "decode launch");
   if (info->num_split_rows > 0) {
     mla::CombineArgs c = {};
@@ -1510,6 +1859,39 @@ mla_status mla_decode_window_fp8(const void* q_abs, const void* q_r, const void*
   CHECK_PTR(info);
   return decode_common(q_abs, q_r, rows, scales, num_pages, block_table, max_pages, plan_dev, &info->plan, scale,
                        workspace, ws_bytes, o_lat, lse, dev_err, stream, true, info);
+}
+
+static mla_status decode_tree(const void* q_abs, const void* q_r, const void* kv_cache, const float* kv_scales,
+                              int64_t num_pages, const int32_t* block_table, int32_t max_pages, const uint64_t* masks,
+                              int32_t words, const void* plan_dev, const mla_tree_info* info, float scale,
+                              void* workspace, size_t ws_bytes, void* o_lat, float* lse, int32_t* dev_err, void* stream,
+                              bool fp8) {
+  CHECK_PTR(info);
+  if (words < 1 || words > MLA_TREE_MAX_NODES / 64)
+    return fail(MLA_ERR_INVALID_ARG, "words = %d outside [1, %d]", words, MLA_TREE_MAX_NODES / 64);
+  if (info->max_nodes > 64 * words)
+    return fail(MLA_ERR_INVALID_ARG, "the plan has a tree of %d nodes, a mask of %d words holds %d", info->max_nodes,
+                words, 64 * words);
+  const mla::TreeArgs tree = {masks, words};
+  return decode_common(q_abs, q_r, kv_cache, kv_scales, num_pages, block_table, max_pages, plan_dev, &info->plan,
+                       scale, workspace, ws_bytes, o_lat, lse, dev_err, stream, fp8, nullptr, &tree);
+}
+
+mla_status mla_decode_tree(const void* q_abs, const void* q_r, const void* kv_cache, int64_t num_pages,
+                           const int32_t* block_table, int32_t max_pages, const uint64_t* masks, int32_t words,
+                           const void* plan_dev, const mla_tree_info* info, float scale, void* workspace,
+                           size_t ws_bytes, void* o_lat, float* lse, int32_t* dev_err, void* stream) {
+  return decode_tree(q_abs, q_r, kv_cache, nullptr, num_pages, block_table, max_pages, masks, words, plan_dev, info,
+                     scale, workspace, ws_bytes, o_lat, lse, dev_err, stream, false);
+}
+
+mla_status mla_decode_tree_fp8(const void* q_abs, const void* q_r, const void* rows, const float* scales,
+                               int64_t num_pages, const int32_t* block_table, int32_t max_pages,
+                               const uint64_t* masks, int32_t words, const void* plan_dev, const mla_tree_info* info,
+                               float scale, void* workspace, size_t ws_bytes, void* o_lat, float* lse,
+                               int32_t* dev_err, void* stream) {
+  return decode_tree(q_abs, q_r, rows, scales, num_pages, block_table, max_pages, masks, words, plan_dev, info, scale,
+                     workspace, ws_bytes, o_lat, lse, dev_err, stream, true);
 }
 
 mla_status mla_debug_set_decode_wait_limit(uint64_t cycles) {

@@ -1,0 +1,181 @@
+// Trees of drafted tokens over the paged latent cache: the nodes' masks,
+// positions and slots before a verification step, and the accepted path's rows
+// brought together after it.  The attention between the two is in
+// decode_paged.cu (decode_tree_kernel).
+//
+// [P2] "DeepSeek的推理为什么比别人便宜一个数量级？…": the MTP section drafts a
+// chain of tokens for each step; a tree is the same draft with alternatives.
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "internal.h"
+#include "ptx.cuh"
+
+namespace mla {
+namespace tree {
+
+constexpr int kMaxNodes = MLA_TREE_MAX_NODES, kMaxWords = kMaxNodes / 64;
+
+// The slot of position pos, or -1 where the table has no page of the pool.
+__device__ __forceinline__ int64_t slot_of(const int32_t* __restrict__ row, int32_t max_pages, int64_t num_pages,
+                                           int32_t pos) {
+  const int32_t page = pos / MLA_PAGE_SIZE;
+  const int32_t id = page < max_pages ? __ldg(row + page) : -1;
+  return id >= 0 && (int64_t)id < num_pages ? (int64_t)id * MLA_PAGE_SIZE + pos % MLA_PAGE_SIZE : -1;
+}
+
+// The masks of a tree are the closure of "parent of": M(i) = {i} ∪ M(parent(i)).
+// One CTA a sequence, a thread a node; every node holds the mask and the length
+// of a piece of its path and a pointer to the node above the piece, and a round
+// joins the piece above, so that a chain of n nodes takes log2 n rounds.
+__global__ void __launch_bounds__(kMaxNodes) layout_kernel(const TreeLayoutArgs a) {
+  __shared__ uint64_t mask[kMaxWords][kMaxNodes];
+  __shared__ int16_t up[kMaxNodes], length[kMaxNodes];
+  const int b = blockIdx.x, i = threadIdx.x;
+  const int32_t q0 = __ldg(a.q_starts + b), q1 = __ldg(a.q_starts + b + 1), len = __ldg(a.seq_lens + b);
+  const int32_t n = q1 - q0;
+  if (q0 < 0 || q1 < q0 || q1 > a.T || n > 64 * a.words || n > len) {
+    if (i == 0) atomicOr(a.dev_err, (int32_t)MLA_DEVERR_TREE);
+    return;
+  }
+  const bool in = i < n;
+  int32_t p = in ? __ldg(a.parents + q0 + i) : -1;
+  if (p < -1 || p >= i) {
+    atomicOr(a.dev_err, (int32_t)MLA_DEVERR_TREE);
+    p = -1;
+  }
+  uint64_t m[kMaxWords];
+#pragma unroll
+  for (int w = 0; w < kMaxWords; ++w) mask[w][i] = m[w] = i / 64 == w ? 1ull << (i % 64) : 0ull;
+  int d = 1;
+  length[i] = 1;
+  up[i] = (int16_t)p;
+  while (__syncthreads_or(p >= 0)) {
+    int next = -1;
+    if (p >= 0) {
+#pragma unroll
+      for (int w = 0; w < kMaxWords; ++w) m[w] |= mask[w][p];
+      d += length[p];
+      next = up[p];
+    }
+    __syncthreads();
+    if (p >= 0) {
+#pragma unroll
+      for (int w = 0; w < kMaxWords; ++w) mask[w][i] = m[w];
+      length[i] = (int16_t)d;
+      up[i] = (int16_t)next;
+    }
+    p = next;
+  }
+  if (!in) return;
+  const int64_t row = (int64_t)q0 + i;
+#pragma unroll
+  for (int w = 0; w < kMaxWords; ++w)
+    if (w < a.words) a.masks[row * a.words + w] = m[w];
+  if (a.positions) a.positions[row] = len - n + d - 1;
+  if (a.slots) {
+    const int64_t s = slot_of(a.block_table + (int64_t)b * a.max_pages, a.max_pages, a.num_pages, len - n + i);
+    if (s < 0) atomicOr(a.dev_err, (int32_t)MLA_DEVERR_PAGE_OOB);
+    a.slots[row] = s;
+  }
+}
+
+// Row r of the kept nodes (ascending, the k_r-th node of the tree) moves from
+// slot n0 + k_r to slot n0 + r in every layer.  k_r >= r and rises with r, so a
+// row may be written as soon as the rows up to it have been read: a batch is
+// loaded, a barrier, and stored, and no batch needs a slot that an earlier one
+// wrote.
+template <int kPieces, bool kScales>
+struct CompactCfg {
+  static constexpr int kPer = kPieces + (kScales ? 1 : 0);  // threads a row: its 16-byte pieces and its scale
+  static constexpr int kRows = 256 / kPer;                  // rows at a time
+  static constexpr int kBatch = 4;                          // of a thread
+};
+
+template <int kPieces, bool kScales>
+__global__ void __launch_bounds__(256) compact_kernel(const TreeCompactArgs a) {
+  using C = CompactCfg<kPieces, kScales>;
+  __shared__ int64_t slot[kMaxNodes];
+  __shared__ int16_t node[kMaxNodes];
+  const int b = blockIdx.x, layer = blockIdx.y, t = threadIdx.x;
+  const int32_t q0 = __ldg(a.q_starts + b), q1 = __ldg(a.q_starts + b + 1), len = __ldg(a.seq_lens + b);
+  const int32_t acc = __ldg(a.accepted + b), n = q1 - q0;
+  if (q0 < 0 || q1 < q0 || q1 > a.T || n > 64 * a.words || n > len || acc < -1 || acc >= n) {
+    if (t == 0 && layer == 0) atomicOr(a.dev_err, (int32_t)MLA_DEVERR_TREE);
+    return;
+  }
+  int kept = 0, rank = 0;
+  bool mine = false;
+  if (acc >= 0) {
+#pragma unroll
+    for (int w = 0; w < kMaxWords; ++w) {
+      if (w >= a.words || 64 * w > acc) break;
+      uint64_t m = __ldg(reinterpret_cast<const unsigned long long*>(a.masks) + ((int64_t)q0 + acc) * a.words + w);
+      if (acc - 64 * w < 63) m &= (1ull << (acc - 64 * w + 1)) - 1ull;
+      if (t / 64 == w) {
+        mine = (m >> (t % 64)) & 1;
+        rank = kept + __popcll(m & ((1ull << (t % 64)) - 1ull));
+      }
+      kept += __popcll(m);
+    }
+  }
+  if (t == 0 && layer == 0) a.new_lens[b] = len - n + kept;
+  if (t <= acc) {
+    slot[t] = slot_of(a.block_table + (int64_t)b * a.max_pages, a.max_pages, a.c.num_pages, len - n + t);
+    if (mine) {
+      if (slot[t] < 0 && layer == 0) atomicOr(a.dev_err, (int32_t)MLA_DEVERR_PAGE_OOB);
+      node[rank] = (int16_t)t;
+    }
+  }
+  __syncthreads();
+  const int piece = t % C::kPer, r0 = t / C::kPer;
+  uint4* rows = reinterpret_cast<uint4*>(a.c.rows + layer * a.c.row_stride);
+  float* scales = kScales ? reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(a.c.scales) + layer * a.c.scale_stride) : nullptr;
+  for (int k0 = 0; k0 < kept; k0 += C::kRows * C::kBatch) {
+    uint4 v[C::kBatch];
+    bool moves[C::kBatch];
+#pragma unroll
+    for (int j = 0; j < C::kBatch; ++j) {
+      const int k = k0 + j * C::kRows + r0;
+      moves[j] = r0 < C::kRows && k < kept && node[k] != k && slot[node[k]] >= 0 && slot[k] >= 0;
+      if (!moves[j]) continue;
+      const int64_t s = slot[node[k]];
+      if (kScales && piece == kPieces)
+        v[j].x = __float_as_uint(scales[s]);
+      else
+        v[j] = rows[s * kPieces + piece];
+    }
+    __syncthreads();
+#pragma unroll
+    for (int j = 0; j < C::kBatch; ++j) {
+      if (!moves[j]) continue;
+      const int64_t d = slot[k0 + j * C::kRows + r0];
+      if (kScales && piece == kPieces)
+        scales[d] = __uint_as_float(v[j].x);
+      else
+        rows[d * kPieces + piece] = v[j];
+    }
+  }
+}
+
+template <int kPieces, bool kScales>
+cudaError_t run_compact(const TreeCompactArgs& a, cudaStream_t stream) {
+  compact_kernel<kPieces, kScales><<<dim3(a.B, a.c.layers), 256, 0, stream>>>(a);
+  return cudaGetLastError();
+}
+
+}  // namespace tree
+
+cudaError_t launch_tree_layout(const TreeLayoutArgs& args, cudaStream_t stream) {
+  tree::layout_kernel<<<args.B, tree::kMaxNodes, 0, stream>>>(args);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_tree_compact(const TreeCompactArgs& args, int row_bytes, cudaStream_t stream) {
+  if (row_bytes == MLA_FP8_ROW_BYTES) return tree::run_compact<MLA_FP8_ROW_BYTES / 16, true>(args, stream);
+  if (row_bytes == MLA_NVFP4_ROW_BYTES) return tree::run_compact<MLA_NVFP4_ROW_BYTES / 16, false>(args, stream);
+  return tree::run_compact<MLA_TOKEN_ELEMS * 2 / 16, false>(args, stream);
+}
+
+}  // namespace mla
