@@ -812,21 +812,34 @@ mla_status mla_tree_layout(const int32_t* parents, const int32_t* q_starts, cons
 typedef struct mla_tree_info {
   mla_plan_info plan; /* plan.magic == MLA_TREE_PLAN_MAGIC */
   int32_t max_nodes;  /* the largest tree */
+  int32_t num_trees;  /* sequences with nodes */
+  int64_t total_pages; /* cache pages of those sequences */
 } mla_tree_info;
 
 /*
  * The split schedule of mla_decode_plan_host for trees: the same arguments
- * (q_lens[b] nodes, at most MLA_TREE_MAX_NODES, else MLA_ERR_UNSUPPORTED),
- * buffers (mla_decode_plan_bytes, mla_decode_workspace_size) and errors.  It
- * depends on the lengths alone, not on the trees' shapes.  A plan of one kind
- * passed to the other kind's decode is MLA_ERR_INVALID_ARG.
+ * (q_lens[b] nodes, at most MLA_TREE_MAX_NODES, else MLA_ERR_UNSUPPORTED) and
+ * errors, in a buffer of mla_tree_plan_bytes.  It depends on the lengths alone,
+ * not on the trees' shapes.  A plan of one kind passed to the other kind's
+ * decode is MLA_ERR_INVALID_ARG.
  */
+mla_status mla_tree_plan_bytes(int32_t T, int32_t num_clusters, size_t* bytes);
 mla_status mla_tree_plan_host(const int32_t* seq_lens, const int32_t* q_lens, int32_t B, int32_t num_clusters,
                               void* plan_host, size_t plan_bytes, mla_tree_info* info);
 /* As mla_tree_plan_host, then copies the plan to plan_dev on `stream` (as
  * mla_decode_plan, not into a capture). */
 mla_status mla_tree_plan(const int32_t* seq_lens_host, const int32_t* q_lens_host, int32_t B, int32_t num_clusters,
                          void* plan_dev, size_t plan_bytes, mla_tree_info* info, void* stream);
+
+/*
+ * Workspace bytes of a tree decode.  mla_decode_workspace_size(num_clusters), or
+ * what the plan's split rows need of it, is enough for either cache.  Over the
+ * FP8 cache (fp8 != 0), where several rows read each page, the size given here
+ * has room for those pages in f16 (72 KB a page, up to 4.5 GB): with it the
+ * decode unpacks a page once instead of once a row.  The results are the same,
+ * bit for bit.
+ */
+mla_status mla_tree_workspace_size(const mla_tree_info* info, int32_t fp8, size_t* bytes);
 
 /*
  * Steps A3 and A4 for the nodes of trees: mla_decode_paged(_fp8) in which row t,

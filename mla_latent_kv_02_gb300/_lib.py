@@ -30,7 +30,7 @@ class mla_window_info(C.Structure):
 
 
 class mla_tree_info(C.Structure):
-    _fields_ = [("plan", mla_plan_info), ("max_nodes", C.c_int32)]
+    _fields_ = [("plan", mla_plan_info), ("max_nodes", C.c_int32), ("num_trees", C.c_int32), ("total_pages", C.c_int64)]
 
 
 P = C.c_void_p
@@ -106,6 +106,8 @@ SIGNATURES = {
     "mla_copy_pages_fp8": (C.c_int, [P, P, I64, I32, I64, I64, P, P, I32, P]),
     "mla_copy_pages_nvfp4": (C.c_int, [P, I64, I32, I64, P, P, I32, P]),
     "mla_tree_layout": (C.c_int, [P, P, P, I32, I32, I32, P, I32, I64, P, P, P, P, P]),
+    "mla_tree_plan_bytes": (C.c_int, [I32, I32, C.POINTER(SZ)]),
+    "mla_tree_workspace_size": (C.c_int, [C.POINTER(mla_tree_info), I32, C.POINTER(SZ)]),
     "mla_tree_plan_host": (C.c_int, [PI32, PI32, I32, I32, P, SZ, C.POINTER(mla_tree_info)]),
     "mla_tree_plan": (C.c_int, [PI32, PI32, I32, I32, P, SZ, C.POINTER(mla_tree_info), P]),
     "mla_decode_tree": (C.c_int, [P, P, P, I64, P, I32, P, I32, P, C.POINTER(mla_tree_info), C.c_float, P, SZ, P, P, P, P]),

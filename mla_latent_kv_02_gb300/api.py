@@ -522,6 +522,15 @@ class DecodePlan:
         return int(self.info.num_clusters)
 
 
+def _torch_stream(stream, raw: int, dev: int):
+    if stream is None:
+        return torch.cuda.current_stream(dev)
+    if isinstance(stream, torch.cuda.Stream):
+        return stream
+    # any object with a `cuda_stream`
+    return torch.cuda.ExternalStream(raw, device=dev) if raw else torch.cuda.default_stream(dev)
+
+
 def _use(plan, stream, dev: int) -> int:
     """The raw handle of the stream that a call reads or writes a plan's buffers
     on.  The allocator learns of every such stream: a plan may be dropped as soon
@@ -529,12 +538,7 @@ def _use(plan, stream, dev: int) -> int:
     the work queued there."""
     raw = _on(stream, dev)
     if raw not in plan.streams:
-        if stream is None:
-            on = torch.cuda.current_stream(dev)
-        elif isinstance(stream, torch.cuda.Stream):
-            on = stream
-        else:  # any object with a `cuda_stream`
-            on = torch.cuda.ExternalStream(raw, device=dev) if raw else torch.cuda.default_stream(dev)
+        on = _torch_stream(stream, raw, dev)
         plan.plan.record_stream(on)
         plan.workspace.record_stream(on)
         plan.streams.add(raw)
@@ -726,6 +730,8 @@ def _planned(cls, buf, info, num_clusters: int, device, stream, into):
     if (into is not None and into.plan.numel() >= words and into.workspace.numel() >= ws_bytes
             and into.plan.device == device):
         plan = replace(into)
+        if cls is TreePlan:
+            plan.unpack = None  # judged for the new lengths
     else:
         with torch.cuda.stream(stream):
             plan = _plan_buffers(cls, words, ws_bytes, device)
@@ -733,6 +739,20 @@ def _planned(cls, buf, info, num_clusters: int, device, stream, into):
     plan.host[:buf.size] = torch.from_numpy(buf)
     _upload(plan, words, stream)
     return plan
+
+
+def _room_to_unpack(plan, stream, dev: int) -> None:
+    """Before a tree plan's first decode over the FP8 cache: a workspace with room
+    for the pages in f16, taken on the stream of the call."""
+    need = mla_tree_workspace_size(plan.info, True)
+    if plan.workspace.numel() < need:
+        raw = _on(stream, dev)
+        on = _torch_stream(stream, raw, dev)
+        with torch.cuda.stream(on):
+            plan.workspace = torch.empty(need, dtype=torch.uint8, device=plan.plan.device)
+        plan.plan.record_stream(on)
+        plan.streams = {raw}  # the others learn of the new block when they next use it
+    plan.unpack = True
 
 
 def mla_decode_window(q_abs, q_r, kv_cache, block_table, plan: WindowPlan, o_lat, dev_err, lse=None,
@@ -867,10 +887,23 @@ def mla_tree_layout(parents, q_starts, seq_lens, masks, dev_err, positions=None,
         _in(dev_err, "dev_err", torch.int32, (1,), dev), _on(stream, dev)))
 
 
+def mla_tree_plan_bytes(T: int, num_clusters: int) -> int:
+    out = C.c_size_t()
+    _check(lib().mla_tree_plan_bytes(int(T), int(num_clusters), C.byref(out)))
+    return int(out.value)
+
+
+def mla_tree_workspace_size(info, fp8: bool) -> int:
+    """Workspace bytes of a tree decode with the plan summary `info`."""
+    out = C.c_size_t()
+    _check(lib().mla_tree_workspace_size(C.byref(info), int(fp8), C.byref(out)))
+    return int(out.value)
+
+
 def mla_tree_plan_host(seq_lens: Sequence[int], q_lens: Sequence[int], num_clusters: int):
     """Host planner of the tree decode only (no GPU): returns (plan int32 array, info)."""
     sl, ql = _host_i32(seq_lens, q_lens)
-    nbytes = mla_decode_plan_bytes(int(ql.sum()) if ql.size else 0, num_clusters)
+    nbytes = mla_tree_plan_bytes(int(ql.sum()) if ql.size else 0, num_clusters)
     buf = np.zeros(nbytes // 4, dtype=np.int32)
     info = mla_tree_info()
     _check(lib().mla_tree_plan_host(sl.ctypes.data_as(_P32), ql.ctypes.data_as(_P32), int(sl.size), int(num_clusters),
@@ -886,6 +919,7 @@ class TreePlan:
     workspace: torch.Tensor     # uint8 device buffer
     host: torch.Tensor          # pinned int32 staging of the plan (reused by `into=`)
     streams: set = field(default_factory=set, repr=False, compare=False)  # raw handles of the streams that use the buffers
+    unpack: Optional[bool] = field(default=None, repr=False, compare=False)  # the workspace holds an FP8 cache's pages in f16
 
     @property
     def num_clusters(self) -> int:
@@ -896,7 +930,9 @@ def mla_tree_plan(seq_lens: Sequence[int], q_lens: Sequence[int], device=None, n
                   stream=None, into: Optional[TreePlan] = None) -> TreePlan:
     """mla_decode_plan for trees of drafted nodes (q_lens[b] of them, the last of
     seq_lens[b] tokens): one plan serves every layer of a step, whatever the
-    trees' shapes.  Uploads, streams, sharing and `into` as for mla_window_plan."""
+    trees' shapes.  Uploads, streams, sharing and `into` as for mla_window_plan.
+    The first decode over an FP8 cache that several rows share takes a larger
+    workspace (mla_tree_workspace_size); it stays with the plan."""
     if num_clusters is None:
         num_clusters = mla_decode_max_clusters()
     buf, info = mla_tree_plan_host(seq_lens, q_lens, num_clusters)
@@ -921,6 +957,8 @@ def mla_decode_tree_fp8(q_abs, q_r, rows, scales, block_table, masks, plan: Tree
     pages = rows.shape[0]
     cache = (_in(rows, "rows", torch.uint8, (pages, PAGE, FP8_ROW_BYTES), dev),
              _in(scales, "scales", torch.float32, (pages, PAGE), dev))
+    if isinstance(plan, TreePlan) and not plan.unpack:
+        _room_to_unpack(plan, stream, dev)
     _decode_tree(lib().mla_decode_tree_fp8, cache, pages, q_abs, q_r, block_table, masks, plan, o_lat, dev_err, lse, scale,
                  stream, dev)
 

@@ -117,26 +117,35 @@ constexpr int kSmallBytes = kSmallMisc + 128;
 //   bf16: 0 producer, 1 QK^T, 2-9 softmax, 10 P·V                (352 threads)
 //   FP8:  0 producer, 1 QK^T, 2 P·V, 3 idle, 4-11 softmax,
 //         12-15 converters; warpgroups 0 and 3 give registers to 1 and 2 (512)
-template <bool kF8>
+//   row warps (a tree's bf16 or unpacked rows): as FP8, with 12-15 loading a
+//         segment's queries and storing its rows                  (512)
+template <bool kF8, bool kRows = false>
 struct Cfg;
 template <>
-struct Cfg<false> {
+struct Cfg<false, true> {
+  static constexpr int kStages = 4;
+  static constexpr int kStageBytes = 4 * kChunkBytes + kRopeBytes;  // 36 KB
+  static constexpr int kSoftWarp0 = 4, kPvWarp = 2, kConvWarp0 = 1 << 20;
+  static constexpr int kThreads = 512;
+};
+template <>
+struct Cfg<false, false> {
   static constexpr int kStages = 4;
   static constexpr int kStageBytes = 4 * kChunkBytes + kRopeBytes;  // 36 KB
   static constexpr int kSoftWarp0 = 2, kPvWarp = 2 + kSWarps, kConvWarp0 = 1 << 20;
   static constexpr int kThreads = 32 * (kPvWarp + 1);
 };
 template <>
-struct Cfg<true> {
+struct Cfg<true, false> {
   static constexpr int kStages = 4;
   static constexpr int kStageBytes = kF8StageBytes;                 // 37 KB
   static constexpr int kSoftWarp0 = 4, kPvWarp = 2, kConvWarp0 = 12;
   static constexpr int kThreads = 512;
 };
 
-template <bool kF8>
-struct Layout : Cfg<kF8> {
-  using C = Cfg<kF8>;
+template <bool kF8, bool kRows = false>
+struct Layout : Cfg<kF8, kRows> {
+  using C = Cfg<kF8, kRows>;
   static constexpr int kOffKV = 0;
   static constexpr int kOffX = C::kStages * C::kStageBytes;
   static constexpr int kOffOnes = kOffX + kXBufs * kXBytes;
@@ -163,6 +172,8 @@ struct Layout : Cfg<kF8> {
     B_X_FULL0,                      // exchange buffer i filled by the peer
     B_DRAIN = B_X_FULL0 + kXBufs,
     B_DRAIN_PV,
+    B_Q_FREE,                       // row warps: a segment's last QK^T has read the queries
+    B_ROW_DONE,                     // row warps: a segment's last P·V is complete
     B_F8_FULL,                      // FP8: stage i's codes, RoPE half and scales landed
     B_COUNT = B_F8_FULL + (kF8 ? C::kStages : 0)
   };
@@ -177,11 +188,11 @@ constexpr uint32_t kTileThreads = 128;                    // the warpgroup that 
 
 // bf16 operands for the bf16 cache; f16 for the FP8 cache (an E4M3 value is
 // an exact f16, and P is computed in f16 in both).
-template <bool kF8>
+template <bool kF16>
 struct Idesc {
-  static constexpr uint32_t kQK = kF8 ? idesc_f16_f32(128, 64, false, false) : idesc_bf16_f32(128, 64, false, false);
-  static constexpr uint32_t kPV = kF8 ? idesc_f16_f32(128, 256, false, true) : idesc_bf16_f32(128, 256, false, true);
-  static constexpr uint32_t kSum = kF8 ? idesc_f16_f32(128, 16, false, false) : idesc_bf16_f32(128, 16, false, false);
+  static constexpr uint32_t kQK = kF16 ? idesc_f16_f32(128, 64, false, false) : idesc_bf16_f32(128, 64, false, false);
+  static constexpr uint32_t kPV = kF16 ? idesc_f16_f32(128, 256, false, true) : idesc_bf16_f32(128, 256, false, true);
+  static constexpr uint32_t kSum = kF16 ? idesc_f16_f32(128, 16, false, false) : idesc_bf16_f32(128, 16, false, false);
 };
 
 // What a row sees: every token up to its own; a sliding window and sinks; or
@@ -306,11 +317,17 @@ __device__ __forceinline__ uint32_t as_u32(__half2 h) { return *reinterpret_cast
 // set to -infinity and their latents cleared before P.V.  A row may see nothing
 // of a tile, and nothing at all: its maximum is then -infinity, its weights and
 // its sum 0, its output 0.
-template <bool kF8, Sees kSees>
+//
+// kF16 without kF8: the pages are f16 rows unpacked from the FP8 cache
+// (unpack_kernel, tree.cu), one after another from the segment's first page;
+// operands and results are those of the FP8 kernel, bit for bit.
+template <bool kF8, Sees kSees, bool kF16 = kF8>
 __device__ __forceinline__ void decode_body(const CUtensorMap& kv_map, const CUtensorMap& rope_map,
                                             const DecodeArgs& a, const WindowArgs* win, const TreeArgs* tree) {
   constexpr bool kWin = kSees == Sees::kWindow, kTree = kSees == Sees::kTree, kMasked = kWin || kTree;
-  using L = Layout<kF8>;
+  constexpr bool kUnpacked = kF16 && !kF8;
+  constexpr bool kRowWarps = kTree && !kF8;
+  using L = Layout<kF8, kRowWarps>;
   constexpr int kStages = L::kStages, kStageBytes = L::kStageBytes, kThreads = L::kThreads;
   constexpr int kPvWarp = L::kPvWarp, kSoftWarp0 = L::kSoftWarp0, kConvWarp0 = L::kConvWarp0;
   constexpr int kOffKV = L::kOffKV, kOffX = L::kOffX, kOffOnes = L::kOffOnes, kOffQ = L::kOffQ;
@@ -319,8 +336,8 @@ __device__ __forceinline__ void decode_body(const CUtensorMap& kv_map, const CUt
                 B_S_FULL1 = L::B_S_FULL1, B_S_FREE = L::B_S_FREE, B_P_FULL = L::B_P_FULL,
                 B_O_DONE0 = L::B_O_DONE0, B_O_DONE1 = L::B_O_DONE1, B_Q_READY = L::B_Q_READY,
                 B_O_FREE = L::B_O_FREE, B_X_FULL0 = L::B_X_FULL0, B_DRAIN = L::B_DRAIN, B_DRAIN_PV = L::B_DRAIN_PV,
-                B_F8_FULL = L::B_F8_FULL;
-  constexpr uint32_t kIdescQK = Idesc<kF8>::kQK, kIdescPV = Idesc<kF8>::kPV, kIdescSum = Idesc<kF8>::kSum;
+                B_F8_FULL = L::B_F8_FULL, B_Q_FREE = L::B_Q_FREE, B_ROW_DONE = L::B_ROW_DONE;
+  constexpr uint32_t kIdescQK = Idesc<kF16>::kQK, kIdescPV = Idesc<kF16>::kPV, kIdescSum = Idesc<kF16>::kSum;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t bars = raw + kSmallBar;
@@ -358,6 +375,10 @@ __device__ __forceinline__ void decode_body(const CUtensorMap& kv_map, const CUt
     mbar_init(BAR(B_O_DONE1), 1);
     mbar_init(BAR(B_Q_READY), kTileThreads);
     mbar_init(BAR(B_O_FREE), kTileThreads);
+    if (kRowWarps) {
+      mbar_init(BAR(B_Q_FREE), 1);
+      mbar_init(BAR(B_ROW_DONE), 1);
+    }
     for (int i = 0; i < kXBufs; ++i) {
       mbar_init(BAR(B_X_FULL0 + i), 1);
       armed[i] = -1;
@@ -407,7 +428,7 @@ __device__ __forceinline__ void decode_body(const CUtensorMap& kv_map, const CUt
   for (int i = threadIdx.x; i < 4 * kH; i += kThreads) st_shared_v2_volatile(pair + 8u * i, 0u, 0xFFFFFFFFu);
   if (layout_fits) {
     uint32_t* ones = reinterpret_cast<uint32_t*>(smem_raw + (base - raw) + kOffOnes);
-    const uint32_t one2 = kF8 ? 0x3C003C00u : 0x3F803F80u;  // f16 / bf16 1.0 pairs
+    const uint32_t one2 = kF16 ? 0x3C003C00u : 0x3F803F80u;  // f16 / bf16 1.0 pairs
     for (int i = threadIdx.x; i < kOnesBytes / 4; i += kThreads) ones[i] = one2;
     fence_proxy_async_smem();
   }
@@ -448,7 +469,9 @@ __device__ __forceinline__ void decode_body(const CUtensorMap& kv_map, const CUt
         if (kWin) wt = window_tiles(sg[6], win->sinks);
         for (int pg = pb; pg < pe; ++pg) {
           const uint32_t st = g % kStages, use = g / kStages;
-          int32_t pid = __ldg(bt + (kWin && pg >= wt.sink_tiles ? pg + wt.skip : pg));  // in flight while the stage drains
+          int32_t pid;  // in flight while the stage drains
+          if constexpr (kUnpacked) pid = sg[7] + pg;
+          else pid = __ldg(bt + (kWin && pg >= wt.sink_tiles ? pg + wt.skip : pg));
           const bool merged = kWin && wt.merged && pg == wt.sink_tiles;
           int32_t spid = merged ? __ldg(bt + win->sinks / kPage) : 0;  // the sinks' page
           if (pg == pe - 1 && s + 1 < s_end) {
@@ -559,6 +582,7 @@ __device__ __forceinline__ void decode_body(const CUtensorMap& kv_map, const CUt
         for (int kk = 0; kk < 2; ++kk)
           mma_ts(tmem + kColS, tmem + kColQ + 128 + kk * 8, dr + (uint64_t)((kk * 32) >> 4), kIdescQK, 1u);
         tc_commit(BAR(B_S_FULL0 + (tq & 1u)));
+        if (kRowWarps && cq.last()) tc_commit(BAR(B_Q_FREE));
         cq.next();
       }
       // Every MMA of this thread must be finished before TMEM is released.
@@ -630,6 +654,7 @@ __device__ __forceinline__ void decode_body(const CUtensorMap& kv_map, const CUt
         // this commit frees the page stage once P·V(tp) has read it.
         tc_commit(BAR(B_KV_EMPTY + tp % kStages));
         tc_commit(BAR(B_O_DONE0 + (tp & 1u)));
+        if (kRowWarps && cp.last()) tc_commit(BAR(B_ROW_DONE));
         return true;
       };
       for (uint32_t tp = 0; cp.valid(); ++tp) {
@@ -814,7 +839,7 @@ __device__ __forceinline__ void decode_body(const CUtensorMap& kv_map, const CUt
           r[4 * j + 3] = __float_as_uint(x.w);
         }
         __syncwarp();
-        if constexpr (kF8) {
+        if constexpr (kF16) {
 #pragma unroll
           for (int j = 0; j < 16; ++j) r[j] = bf16x2_to_f16x2(r[j]);
         }
@@ -880,7 +905,7 @@ __device__ __forceinline__ void decode_body(const CUtensorMap& kv_map, const CUt
                           (uint32_t)kXWarp, mapa(BAR(B_X_FULL0 + t % kXBufs), peer));
         push_cnt[sw] += 1u;  // copies this warp issued into the peer
       }
-      if (c.last() && c.s + 1 < c.s_end) load_q(c.s + 1);
+      if (!kRowWarps && c.last() && c.s + 1 < c.s_end) load_q(c.s + 1);
       return true;
     };
 
@@ -888,7 +913,7 @@ __device__ __forceinline__ void decode_body(const CUtensorMap& kv_map, const CUt
     uint32_t G = 0;
     for (int s = s_begin; s < s_end; ++s) G += (uint32_t)(a.segs[8 * s + 3] - a.segs[8 * s + 2]);
 
-    if (wg == 0) mbar_arrive(BAR(B_O_FREE));  // O is free for the first segment
+    if (!kRowWarps && wg == 0) mbar_arrive(BAR(B_O_FREE));  // O is free for the first segment
     if (sw == 0 && lane == 0)                  // arm the ring: the first kXBufs tiles each expect one peer push
       for (uint32_t t = 0; t < G && t < (uint32_t)kXBufs; ++t) {
         mbar_arrive_expect_tx(BAR(B_X_FULL0 + t), (uint32_t)kXBytes);
@@ -897,7 +922,7 @@ __device__ __forceinline__ void decode_body(const CUtensorMap& kv_map, const CUt
     TileCursor<kSees> cf;  // this warpgroup's tile
     cf.init(a.segs, s_begin, s_end, win, tree);
     if (wg == 1 && cf.valid()) cf.next();
-    if (wg == 0 && G > 0) load_q(s_begin);
+    if (!kRowWarps && wg == 0 && G > 0) load_q(s_begin);
     uint32_t own[kWords];
     bool ok = true;
     for (uint32_t g = (uint32_t)wg; g < G && ok; g += 2) {
@@ -1000,7 +1025,7 @@ __device__ __forceinline__ void decode_body(const CUtensorMap& kv_map, const CUt
 #pragma unroll
       for (int j = 0; j < kWords; ++j) {
         const uint32_t p16 = ex2_f16x2(as_u32(__hfma2(as_h2(own[j]), c2h, mc2)));
-        if constexpr (kF8) {
+        if constexpr (kF16) {
           own[j] = p16;
         } else {
           const float2 p = __half22float2(as_h2(p16));
@@ -1033,7 +1058,7 @@ __device__ __forceinline__ void decode_body(const CUtensorMap& kv_map, const CUt
       __syncwarp();
       if (lane == 0) mbar_arrive(BAR(B_P_FULL));
 
-      if (cf.last()) {
+      if (!kRowWarps && cf.last()) {
         // ---- epilogue of this segment: wait for its last P·V, normalise, store
         const int row = cf.row, slot = cf.slot;
         w = wait_phase(BAR(B_O_DONE0 + (g & 1u)), (g >> 1) & 1u, err, abort_flag, a.wait_limit, a.wait_every);
@@ -1115,7 +1140,152 @@ __device__ __forceinline__ void decode_body(const CUtensorMap& kv_map, const CUt
     __syncwarp();
     if (!peer_ready) cluster_wait();
   };
-  if constexpr (kF8) {
+  auto role_rows = [&]() {
+    // ---------------------------------------------------------------- a segment's queries and its finished row
+    // One warpgroup between the segments, so that neither sits on the softmax:
+    // it holds the first pieces of the next row's queries in registers when the
+    // last QK^T of a row is complete, and stores a finished row while the next
+    // row's first tiles are on their way.  (Thread = head row = TMEM lane.)
+    const int q4 = warp & 3, h = q4 * 32 + lane;
+    const uint32_t tl = tmem + ((uint32_t)(q4 * 32) << 16);
+    const uint32_t buf = base + kOffQ + (uint32_t)(q4 * kQWarp);  // 64 bytes of each of the warp's 32 rows
+    const float c2 = a.scale_log2;
+    mbar_arrive(BAR(B_O_FREE));  // O is free for the first segment
+    // 16-byte piece k of row r, the pieces of eight rows spread over the banks
+    auto at = [&](uint32_t r, uint32_t k) { return buf + r * 64u + ((k ^ ((r >> 1) & 3u)) << 4); };
+    const uint32_t wr = (uint32_t)lane >> 2, wk = (uint32_t)lane & 3u;  // four lanes a row: whole sectors in memory
+    auto queries = [&](int s, uint32_t phase) -> bool {
+      const size_t row0 = (size_t)a.segs[8 * s] * kH + q4 * 32 + wr;
+      const uint4* lat = reinterpret_cast<const uint4*>(a.q_abs + row0 * kDC + rank * 256) + wk;
+      const uint4* rp = reinterpret_cast<const uint4*>(a.q_r + row0 * kDR + rank * kRopeHalf) + wk;
+      constexpr int kAhead = 3;  // rounds of 64 bytes a row in flight: eight latent, one RoPE
+      uint4 v[kAhead][4];
+      auto fetch = [&](int k) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[k % kAhead][i] = k < 8 ? __ldg(lat + 4 * k + i * kDC) : __ldg(rp + i * kDR);
+      };
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k) fetch(k);
+      if (s > s_begin) {
+        const bool w = wait_phase<false, true>(BAR(B_Q_FREE), phase, err, abort_flag, a.wait_limit, a.wait_every);
+        if (!__all_sync(0xffffffffu, w)) return false;
+        tc_fence_after();
+      }
+#pragma unroll
+      for (int k = 0; k < 9; ++k) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) st_shared_v4(at(8 * i + wr, wk), v[k % kAhead][i].x, v[k % kAhead][i].y, v[k % kAhead][i].z, v[k % kAhead][i].w);
+        __syncwarp();
+        if (k + kAhead < 9) fetch(k + kAhead);
+        uint32_t r[16];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float4 x = ld_shared_v4(at(lane, j));
+          r[4 * j] = __float_as_uint(x.x);
+          r[4 * j + 1] = __float_as_uint(x.y);
+          r[4 * j + 2] = __float_as_uint(x.z);
+          r[4 * j + 3] = __float_as_uint(x.w);
+        }
+        __syncwarp();
+        if constexpr (kF16) {
+#pragma unroll
+          for (int j = 0; j < 16; ++j) r[j] = bf16x2_to_f16x2(r[j]);
+        }
+        tmem_st16(tl + kColQ + 16 * k, r);
+      }
+      tmem_st_wait();
+      tc_fence_before();
+      mbar_arrive(BAR(B_Q_READY));
+      return true;
+    };
+    // The row of segment s, whose last tile is g: O / l as bf16, or as an fp32
+    // partial.  The reference max is in tile g's slot; the slot's next writer,
+    // tile g + 4, needs P·V of g + 1 and with it this segment's O freed.
+    auto finish = [&](int s, uint32_t g, uint32_t phase) -> bool {
+      const bool w = wait_phase<false, true>(BAR(B_ROW_DONE), phase, err, abort_flag, a.wait_limit, a.wait_every);
+      if (!__all_sync(0xffffffffu, w)) return false;
+      tc_fence_after();
+      const int row = a.segs[8 * s], slot = a.segs[8 * s + 5];
+      const float m = __uint_as_float(ld_shared_v2_volatile(pair + 8u * ((g & 3u) * kH + h)).x);
+      const float lt = __uint_as_float(tmem_ld1_sync(tl + kColSum));
+      const float inv = lt == 0.f ? 0.f : 1.f / lt;
+      const uint64_t keep = l2_policy_evict_last();  // partials are read once, by the combine right after
+      uint32_t o[32];
+      tmem_ld32_sync(tl + kColO, o);
+#pragma unroll 1
+      for (int c = 0; c < 256; c += 32) {
+        uint32_t x[32];
+#pragma unroll
+        for (int i = 0; i < 32; ++i) x[i] = __float_as_uint(__uint_as_float(o[i]) * inv);
+        if (c + 32 < 256) {
+          tmem_ld32_sync(tl + kColO + c + 32, o);
+        } else {
+          tc_fence_before();
+          mbar_arrive(BAR(B_O_FREE));
+        }
+        if (slot < 0) {
+          uint16_t* dst = a.o_lat + ((size_t)row * kH + q4 * 32 + wr) * kDC + rank * 256 + c + wk * 8;
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            uint32_t y[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) y[j] = pack_bf16x2(__uint_as_float(x[8 * k + 2 * j]), __uint_as_float(x[8 * k + 2 * j + 1]));
+            st_shared_v4(at(lane, k), y[0], y[1], y[2], y[3]);
+          }
+          __syncwarp();
+#pragma unroll
+          for (int i = 0; i < 4; ++i) *reinterpret_cast<float4*>(dst + (size_t)(8 * i) * kDC) = ld_shared_v4(at(8 * i + wr, wk));
+          __syncwarp();
+        } else {
+          float* dst = a.part_o + ((size_t)slot * kH + q4 * 32 + wr) * kDC + rank * 256 + c + wk * 4;
+#pragma unroll
+          for (int hf = 0; hf < 2; ++hf) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) st_shared_v4(at(lane, k), x[16 * hf + 4 * k], x[16 * hf + 4 * k + 1], x[16 * hf + 4 * k + 2], x[16 * hf + 4 * k + 3]);
+            __syncwarp();
+#pragma unroll
+            for (int i = 0; i < 4; ++i) st_global_v4_hint(dst + (size_t)(8 * i) * kDC + 16 * hf, ld_shared_v4(at(8 * i + wr, wk)), keep);
+            __syncwarp();
+          }
+        }
+      }
+      if (rank == 0) {
+        const float lse2 = m * c2 + log2f(lt);
+        if (slot < 0) {
+          if (a.lse) a.lse[(size_t)row * kH + h] = lse2 * 0.6931471805599453f;
+        } else {
+          a.part_lse[(size_t)slot * kH + h] = lse2;
+        }
+      }
+      return true;
+    };
+    uint32_t g = 0;  // tiles of the segments before s
+    bool ok = true;
+    for (int s = s_begin; s < s_end && ok; ++s) {
+      const uint32_t before = (uint32_t)(s - 1 - s_begin) & 1u;
+      ok = queries(s, before) && (s == s_begin || finish(s - 1, g - 1, before));
+      g += (uint32_t)(a.segs[8 * s + 3] - a.segs[8 * s + 2]);
+    }
+    if (ok && s_end > s_begin) finish(s_end - 1, g - 1, (uint32_t)(s_end - 1 - s_begin) & 1u);
+    __syncwarp();
+  };
+  if constexpr (kRowWarps) {
+    // 512 threads x 128 registers at launch: 128*96 + 256*160 + 128*96.
+    if (warp < 4) {
+      regs_dec<96>();
+      if (warp == 0) role_producer();
+      else if (warp == 1) role_qk();
+      else if (warp == kPvWarp) role_pv();
+      cluster_wait();
+    } else if (warp >= 12) {
+      regs_dec<96>();
+      role_rows();
+      cluster_wait();
+    } else {
+      regs_inc<160>();
+      role_softmax();
+    }
+  } else if constexpr (kF8) {
     // 512 threads x 128 registers at launch: warpgroup 0 (producer, MMA
     // issue, an idle warp) drops to 64, warpgroup 3 (converters, which hold
     // a tile's codes and row factors in registers) to 112, the softmax
@@ -1202,11 +1372,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<kF8>::kThreads, 
   decode_body<kF8, Sees::kWindow>(kv_map, rope_map, a, &win, nullptr);
 }
 
-template <bool kF8>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<kF8>::kThreads, 1)
+template <bool kF8, bool kF16>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<kF8, !kF8>::kThreads, 1)
     decode_tree_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constant__ CUtensorMap rope_map,
                        const DecodeArgs a, const TreeArgs tree) {
-  decode_body<kF8, Sees::kTree>(kv_map, rope_map, a, nullptr, &tree);
+  decode_body<kF8, Sees::kTree, kF16>(kv_map, rope_map, a, nullptr, &tree);
 }
 
 }  // namespace decode
@@ -1231,14 +1401,15 @@ static cudaError_t run_window(const CUtensorMap& kv_map, const CUtensorMap& rope
   return cudaGetLastError();
 }
 
-template <bool kF8>
+template <bool kF8, bool kF16>
 static cudaError_t run_tree(const CUtensorMap& kv_map, const CUtensorMap& rope_map, const DecodeArgs& args,
                             const TreeArgs& tree, int num_clusters, cudaStream_t stream) {
-  auto* kern = decode::decode_tree_kernel<kF8>;
-  constexpr int smem = decode::Layout<kF8>::kSmemBytes;
+  auto* kern = decode::decode_tree_kernel<kF8, kF16>;
+  using L = decode::Layout<kF8, !kF8>;
+  constexpr int smem = L::kSmemBytes;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  kern<<<2 * num_clusters, decode::Layout<kF8>::kThreads, smem, stream>>>(kv_map, rope_map, args, tree);
+  kern<<<2 * num_clusters, L::kThreads, smem, stream>>>(kv_map, rope_map, args, tree);
   return cudaGetLastError();
 }
 
@@ -1279,9 +1450,12 @@ cudaError_t launch_decode_window(const CUtensorMap& kv_map, const CUtensorMap& r
 }
 
 cudaError_t launch_decode_tree(const CUtensorMap& kv_map, const CUtensorMap& rope_map, const DecodeArgs& args,
-                               const TreeArgs& tree, int num_clusters, bool fp8, cudaStream_t stream) {
-  return fp8 ? run_tree<true>(kv_map, rope_map, args, tree, num_clusters, stream)
-             : run_tree<false>(kv_map, rope_map, args, tree, num_clusters, stream);
+                               const TreeArgs& tree, int num_clusters, TreeCache cache, cudaStream_t stream) {
+  switch (cache) {
+    case TreeCache::kFp8: return run_tree<true, true>(kv_map, rope_map, args, tree, num_clusters, stream);
+    case TreeCache::kUnpacked: return run_tree<false, true>(kv_map, rope_map, args, tree, num_clusters, stream);
+    default: return run_tree<false, false>(kv_map, rope_map, args, tree, num_clusters, stream);
+  }
 }
 
 }  // namespace mla

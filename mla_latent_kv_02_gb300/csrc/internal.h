@@ -21,11 +21,16 @@ mla_status set_last_error(mla_status s, const char* message);
 //   [8..15] reserved
 //   seg_off   at kPlanHeader, num_clusters + 1 entries
 //   segments  at seg_base, num_segments x 8: {row, b, page_begin, page_end,
-//             visible, out_slot (-1 = final), window's or tree's first token, 0}
+//             visible, out_slot (-1 = final), window's or tree's first token,
+//             tree: its sequence's first page among the unpacked ones}
 //   split rows at split_base, num_split_rows x 4: {row, slot_begin, n_slots, 0}
+//   trees     behind them (tree plans only), num_seqs x 8: {b, first unpacked
+//             page, pages, first token of the tree, tokens, first row, nodes, 0},
+//             one entry for each sequence that has nodes
 constexpr int kPlanHeader = 16;
 constexpr int kSegWords = 8;
 constexpr int kSplitWords = 4;
+constexpr int kTreeWords = 8;
 
 struct PlanLayout {
   int64_t seg_off;  // word offsets
@@ -181,6 +186,24 @@ struct TreeArgs {
   int32_t words;
 };
 
+// The FP8 cache's pages as f16 rows [page][64][576], for a tree decode that reads
+// each of them for several rows.
+struct TreeUnpackArgs {
+  const uint8_t* rows;
+  const float* scales;
+  int64_t num_pages;
+  const int32_t* block_table;
+  const uint64_t* masks;
+  const int32_t* trees;        // the plan's table
+  uint4* out;
+  int32_t* dev_err;
+  int32_t max_pages;
+  int32_t B;
+  int32_t T;
+  int32_t words;
+  int32_t out_pages;
+};
+
 // Trees of drafted nodes, a sequence each (tree.cu): sequence b's nodes are
 // rows [q_starts[b], q_starts[b + 1]) of T, its last ones of seq_lens[b] tokens.
 struct TreeLayoutArgs {
@@ -254,8 +277,10 @@ cudaError_t launch_decode(const CUtensorMap& kv_map, const CUtensorMap& rope_map
                           int num_clusters, bool fp8, cudaStream_t stream);
 cudaError_t launch_decode_window(const CUtensorMap& kv_map, const CUtensorMap& rope_map, const DecodeArgs& args,
                                  const WindowArgs& window, int num_clusters, bool fp8, cudaStream_t stream);
+enum class TreeCache { kBf16, kFp8, kUnpacked };
 cudaError_t launch_decode_tree(const CUtensorMap& kv_map, const CUtensorMap& rope_map, const DecodeArgs& args,
-                               const TreeArgs& tree, int num_clusters, bool fp8, cudaStream_t stream);
+                               const TreeArgs& tree, int num_clusters, TreeCache cache, cudaStream_t stream);
+cudaError_t launch_tree_unpack(const TreeUnpackArgs& args, int num_trees, int max_tree_pages, cudaStream_t stream);
 cudaError_t launch_combine(const CombineArgs& args, int num_split_rows, cudaStream_t stream);
 
 cudaError_t launch_kv_append(const uint16_t* c_kv_new, const uint16_t* k_r_new, const int64_t* slots, int32_t n,

@@ -96,6 +96,7 @@ struct PlanRow {
   int32_t visible;
   int32_t npages;  // tiles the row reads
   int32_t lo;      // the window's first token (0: the row sees every token up to its own), or the tree's
+  int32_t base;    // the first unpacked page of the row's sequence (trees)
 };
 
 // Minimum 64-token tiles per cluster: below it, the per-range fixed costs
@@ -112,8 +113,47 @@ struct PlanKind {
   uint32_t magic() const { return tree ? MLA_TREE_PLAN_MAGIC : window > 0 ? MLA_WINDOW_PLAN_MAGIC : MLA_PLAN_MAGIC; }
 };
 
+// A tree plan's costs, in tiles (about 1 us).  A piece of a row takes four tiles'
+// time beside its tiles: the queries into TMEM and the row out of it are 64 to
+// 128 KB a CTA, while the next piece's first tile is under way (254 rows over
+// 1 024 to 4 096 tokens: 205 us without it, 195 with four, 198 with eight).
+constexpr int64_t kTreeRowTiles = 4;
+// A partial result, 256 KB written, read and merged, in 64ths of a tile (8 rows
+// over 1 024 tokens: 20.7 us in 32 pieces, 24.9 in 68; one row over 8 192: 24.7
+// in 32 pieces, 28.8 in 64).
+constexpr int64_t kTreePartial = 10;
+// The share of the L2 cache (129 MB) that a plan counts on for the sequences
+// being read at one time.
+constexpr int64_t kTreeSharedBytes = 64ll << 20;
+
+// Lanes of a tree plan.  Rows are planned lane by lane, lane j holding the j-th
+// share of every sequence's rows: the clusters of a lane walk the sequences
+// together, and every lane at the same time, so that num_clusters / lanes
+// sequences are being read at once, each by `lanes` clusters.  The fewest lanes
+// that keep those in L2, of those that divide the clusters evenly (12 rows of 64
+// sequences of 8 192 tokens: 1 410 us in four lanes, 1 475 in one; two rows: 260
+// us in two lanes, 270 in one).
+int32_t tree_lanes(const int32_t* seq_lens, const int32_t* q_lens, int32_t B, int32_t num_clusters) {
+  int64_t tokens = 0, seqs = 0;
+  int32_t most = 0;
+  for (int32_t b = 0; b < B; ++b)
+    if (q_lens[b] > 0) {
+      tokens += seq_lens[b];
+      ++seqs;
+      most = std::max(most, q_lens[b]);
+    }
+  int32_t lanes = 1;
+  for (int32_t l = 1; l <= std::min(most, num_clusters); ++l) {
+    if (num_clusters % l) continue;
+    lanes = l;
+    if (std::min<int64_t>(num_clusters / l, seqs) * (tokens / seqs) * kRowBytes <= kTreeSharedBytes) break;
+  }
+  return lanes;
+}
+
 mla_status build_plan(const int32_t* seq_lens, const int32_t* q_lens, int32_t B, int32_t num_clusters,
-                      int32_t* out, size_t out_words, mla_plan_info* info, const PlanKind& kind = {}) {
+                      int32_t* out, size_t out_words, mla_plan_info* info, const PlanKind& kind = {},
+                      mla_tree_info* tree_info = nullptr) {
   const int32_t window = kind.window, sinks = kind.sinks;
   if (B < 0) return fail(MLA_ERR_INVALID_ARG, "B = %d is negative", B);
   if (B > 0) {
@@ -122,6 +162,8 @@ mla_status build_plan(const int32_t* seq_lens, const int32_t* q_lens, int32_t B,
   }
   if (num_clusters < 1) return fail(MLA_ERR_INVALID_ARG, "num_clusters = %d < 1", num_clusters);
   std::vector<PlanRow> rows;
+  std::vector<int32_t> trees;  // the plan's table
+  int64_t tree_pages = 0;
   int64_t total = 0;
   int32_t max_pages = 0;
   for (int32_t b = 0; b < B; ++b) {
@@ -131,6 +173,12 @@ mla_status build_plan(const int32_t* seq_lens, const int32_t* q_lens, int32_t B,
     if (kind.tree && q > MLA_TREE_MAX_NODES)
       return fail(MLA_ERR_UNSUPPORTED, "q_lens[%d] = %d: a tree has at most %d nodes", b, q, MLA_TREE_MAX_NODES);
     max_pages = std::max<int32_t>(max_pages, (n - 1) / MLA_PAGE_SIZE + 1);
+    const int32_t base = (int32_t)std::min<int64_t>(tree_pages, INT32_MAX);
+    if (kind.tree && q > 0) {
+      const int32_t pages = (n - 1) / MLA_PAGE_SIZE + 1;
+      trees.insert(trees.end(), {b, base, pages, n - q, n, (int32_t)rows.size(), q, 0});
+      tree_pages += pages;
+    }
     for (int32_t i = 0; i < q; ++i) {
       const int32_t vis = n - q + i + 1;
       int32_t np = (vis - 1) / MLA_PAGE_SIZE + 1, lo = kind.tree ? n - q : 0;
@@ -138,22 +186,102 @@ mla_status build_plan(const int32_t* seq_lens, const int32_t* q_lens, int32_t B,
         lo = vis - window;
         np -= mla::window_tiles(lo, sinks).skip;
       }
-      rows.push_back({b, vis, np, lo});
+      rows.push_back({b, vis, np, lo, base});
       total += np;
     }
     if ((int64_t)rows.size() > (int64_t)INT32_MAX / MLA_NUM_HEADS)
       return fail(MLA_ERR_INVALID_ARG, "too many query rows");
   }
   const int64_t T = (int64_t)rows.size();
-  // Lanes: when every sequence has the same number Q >= 2 of query rows
-  // (multi-token decode), the clusters are split into Q lanes and lane j takes
-  // row j of every sequence, cut into equal contiguous tile ranges the same
-  // way in every lane.  Cluster c of each lane then reads the same pages at
-  // nearly the same time, so the rows of a sequence share one DRAM read of
-  // each page through L2.  Otherwise there is one lane over all rows.
-  int32_t lanes = 1;
-  {
-    int32_t q0 = -1;
+  // The order of the rows and its cut into the clusters' ranges.
+  struct Seg {
+    int32_t row, b, pb, pe, vis, slot, lo, base;
+  };
+  std::vector<Seg> segs;
+  std::vector<int32_t> seg_off;
+  std::vector<int32_t> row_pieces(T, 0);
+  auto piece = [&](int32_t rr, int64_t pb, int64_t pe) {
+    segs.push_back({rr, rows[rr].b, (int32_t)pb, (int32_t)pe, rows[rr].visible, -1, rows[rr].lo, rows[rr].base});
+    ++row_pieces[rr];
+  };
+  // Rows in the order of `order` as one line of tiles, cut into at most `ranges` equal ranges.
+  auto cut = [&](const std::vector<int32_t>& order, int64_t ranges) {
+    int64_t all = 0;
+    for (int32_t r : order) all += rows[r].npages;
+    if (all == 0) return;
+    const int64_t per = std::max<int64_t>((all + ranges - 1) / ranges, kMinTilesPerCluster);
+    int64_t row_start = 0;
+    size_t k = 0;  // index into order
+    for (int64_t lo = 0; lo < all; lo += per) {
+      const int64_t hi = std::min(all, lo + per);
+      seg_off.push_back((int32_t)segs.size());
+      while (k < order.size() && row_start + rows[order[k]].npages <= lo) row_start += rows[order[k++]].npages;
+      int64_t rs = row_start;
+      for (size_t kk = k; kk < order.size() && rs < hi; rs += rows[order[kk++]].npages) {
+        const int32_t rr = order[kk];
+        const int64_t pb = std::max<int64_t>(lo - rs, 0), pe = std::min<int64_t>(hi - rs, rows[rr].npages);
+        if (pe > pb) piece(rr, pb, pe);
+      }
+    }
+  };
+  // The same where a piece of a row costs its tiles and kTreeRowTiles more: each
+  // range takes pieces up to `budget`, none of under kMinTilesPerCluster tiles
+  // unless the row has no more.  Calls begin() for a range and take(row, first,
+  // last) for a piece; false when more than `ranges` ranges would be needed.
+  auto fill = [&](const std::vector<int32_t>& order, int64_t ranges, int64_t budget, auto begin, auto take) {
+    int64_t used = 0, left = 0;
+    for (int32_t rr : order) {
+      for (int64_t at = 0, n = rows[rr].npages; at < n;) {
+        int64_t t = left - kTreeRowTiles;
+        if (t < std::min(kMinTilesPerCluster, n - at)) {
+          if (++used > ranges) return false;
+          begin();
+          left = budget;
+          t = std::max(left - kTreeRowTiles, kMinTilesPerCluster);
+        }
+        if (n - at - t < kMinTilesPerCluster) t = n - at;  // no crumb stays behind
+        take(rr, at, at + t);
+        at += t;
+        left -= t + kTreeRowTiles;
+      }
+    }
+    return true;
+  };
+  if (kind.tree) {
+    std::vector<int32_t> order;
+    order.reserve(rows.size());
+    const int32_t lanes = tree_lanes(seq_lens, q_lens, B, num_clusters);
+    for (int32_t lane = 0; lane < lanes; ++lane) {
+      int32_t r = 0;
+      for (int32_t b = 0; b < B; r += q_lens[b++])
+        for (int64_t i = (int64_t)q_lens[b] * lane / lanes; i < (int64_t)q_lens[b] * (lane + 1) / lanes; ++i)
+          order.push_back(r + (int32_t)i);
+    }
+    // Ranges: all of them, or for few rows as many as pay: each further piece of
+    // a row is a partial result to write, read and merge.
+    int64_t best_ranges = 0, best_budget = 0, best_cost = INT64_MAX;
+    const bool few = (int64_t)rows.size() < 2 * (int64_t)num_clusters;
+    for (int64_t ranges = num_clusters; total > 0 && ranges >= 1; ranges = few ? std::min(ranges - 1, ranges * 7 / 8) : 0) {
+      int64_t budget = (total + kTreeRowTiles * std::max<int64_t>(T, ranges) + ranges - 1) / ranges, pieces;
+      while (pieces = 0, !fill(order, ranges, budget, [] {}, [&](int32_t, int64_t, int64_t) { ++pieces; })) budget += 1 + budget / 1024;
+      const int64_t partials = pieces > T ? std::min(pieces, 2 * (pieces - T)) : 0;
+      const int64_t cost = 64 * budget + kTreePartial * partials;
+      if (cost < best_cost) {
+        best_cost = cost;
+        best_ranges = ranges;
+        best_budget = budget;
+      }
+    }
+    if (total > 0)
+      fill(order, best_ranges, best_budget, [&] { seg_off.push_back((int32_t)segs.size()); }, piece);
+  } else {
+    // Lanes: when every sequence has the same number Q >= 2 of query rows
+    // (multi-token decode), the clusters are split into Q lanes and lane j takes
+    // row j of every sequence, cut into equal contiguous tile ranges the same
+    // way in every lane.  Cluster c of each lane then reads the same pages at
+    // nearly the same time, so the rows of a sequence share one DRAM read of
+    // each page through L2.  Otherwise there is one lane over all rows.
+    int32_t lanes = 1, q0 = -1;
     bool uniform = true;
     for (int32_t b = 0; b < B; ++b) {
       if (q_lens[b] == 0) continue;
@@ -161,44 +289,11 @@ mla_status build_plan(const int32_t* seq_lens, const int32_t* q_lens, int32_t B,
       uniform = uniform && q_lens[b] == q0;
     }
     if (uniform && q0 >= 2 && num_clusters / q0 >= 1) lanes = q0;
-  }
-  std::vector<std::vector<int32_t>> lane_rows(lanes);
-  {
+    std::vector<std::vector<int32_t>> lane_rows(lanes);
     int32_t r = 0;
     for (int32_t b = 0; b < B; ++b)
       for (int32_t i = 0; i < q_lens[b]; ++i, ++r) lane_rows[lanes == 1 ? 0 : i].push_back(r);
-  }
-  const int32_t clusters_per_lane = num_clusters / lanes;
-  // segments
-  struct Seg {
-    int32_t row, b, pb, pe, vis, slot, lo;
-  };
-  std::vector<Seg> segs;
-  std::vector<int32_t> seg_off;
-  std::vector<int32_t> row_pieces(T, 0);
-  for (int32_t lane = 0; lane < lanes; ++lane) {
-    const std::vector<int32_t>& lr = lane_rows[lane];
-    int64_t lane_total = 0;
-    for (int32_t r : lr) lane_total += rows[r].npages;
-    if (lane_total == 0) continue;
-    const int64_t tiles_per =
-        std::max<int64_t>((lane_total + clusters_per_lane - 1) / clusters_per_lane, kMinTilesPerCluster);
-    const int64_t used = (lane_total + tiles_per - 1) / tiles_per;
-    int64_t row_start = 0;
-    size_t k = 0;  // index into lr
-    for (int64_t c = 0; c < used; ++c) {
-      const int64_t lo = c * tiles_per, hi = std::min(lane_total, lo + tiles_per);
-      seg_off.push_back((int32_t)segs.size());
-      while (k < lr.size() && row_start + rows[lr[k]].npages <= lo) row_start += rows[lr[k++]].npages;
-      int64_t rs = row_start;
-      for (size_t kk = k; kk < lr.size() && rs < hi; rs += rows[lr[kk++]].npages) {
-        const int32_t rr = lr[kk];
-        const int64_t pb = std::max<int64_t>(lo - rs, 0), pe = std::min<int64_t>(hi - rs, rows[rr].npages);
-        if (pe <= pb) continue;
-        segs.push_back({rr, rows[rr].b, (int32_t)pb, (int32_t)pe, rows[rr].visible, -1, rows[rr].lo});
-        ++row_pieces[rr];
-      }
-    }
+    for (const std::vector<int32_t>& order : lane_rows) cut(order, num_clusters / lanes);
   }
   const int64_t used = (int64_t)seg_off.size();
   seg_off.push_back((int32_t)segs.size());
@@ -218,10 +313,10 @@ mla_status build_plan(const int32_t* seq_lens, const int32_t* q_lens, int32_t B,
   }
   const int64_t nsplit = (int64_t)split.size() / mla::kSplitWords;
   const mla::PlanLayout L = mla::plan_layout(used, (int64_t)segs.size(), nsplit);
-  if ((size_t)L.words > out_words)
-    return fail(MLA_ERR_INVALID_ARG, "plan buffer holds %zu bytes, %lld needed", out_words * 4,
-                (long long)L.words * 4);
-  std::fill(out, out + L.words, 0);
+  const int64_t words = L.words + (int64_t)trees.size();
+  if ((size_t)words > out_words)
+    return fail(MLA_ERR_INVALID_ARG, "plan buffer holds %zu bytes, %lld needed", out_words * 4, (long long)words * 4);
+  std::fill(out, out + words, 0);
   const uint32_t magic = kind.magic();
   out[0] = (int32_t)magic;
   out[1] = (int32_t)T;
@@ -241,8 +336,10 @@ mla_status build_plan(const int32_t* seq_lens, const int32_t* q_lens, int32_t B,
     w[4] = segs[i].vis;
     w[5] = segs[i].slot;
     w[6] = segs[i].lo;
+    w[7] = kind.tree ? segs[i].base : 0;
   }
   std::copy(split.begin(), split.end(), out + L.split_base);
+  std::copy(trees.begin(), trees.end(), out + L.words);
   if (info) {
     info->magic = magic;
     info->T = (int32_t)T;
@@ -253,7 +350,13 @@ mla_status build_plan(const int32_t* seq_lens, const int32_t* q_lens, int32_t B,
     info->num_split_rows = (int32_t)nsplit;
     info->max_pages_needed = max_pages;
     info->total_tiles = total;
-    info->plan_bytes = (size_t)L.words * 4;
+    info->plan_bytes = (size_t)words * 4;
+  }
+  if (tree_info) {
+    tree_info->max_nodes = 0;
+    for (size_t i = 6; i < trees.size(); i += mla::kTreeWords) tree_info->max_nodes = std::max(tree_info->max_nodes, trees[i]);
+    tree_info->num_trees = (int32_t)(trees.size() / mla::kTreeWords);
+    tree_info->total_pages = tree_pages;
   }
   return MLA_OK;
 }
@@ -267,6 +370,10 @@ mla_status no_throw(F&& body) {
     return fail(MLA_ERR_NO_SPACE, "out of host memory");
   }
 }
+
+// A tree decode unpacks at most so many pages of the FP8 cache (4.5 GB).
+constexpr int64_t kMostUnpackedPages = 1 << 16;
+constexpr int64_t kUnpackTiles = 800;
 
 size_t workspace_bytes_for(int64_t partials) {
   return (size_t)partials * (MLA_NUM_HEADS * MLA_LATENT_DIM * 4 + MLA_NUM_HEADS * 4);
@@ -1547,9 +1654,10 @@ mla_status mla_decode_workspace_size(int32_t num_clusters, size_t* bytes) {
 
 // build_plan where an exception may not pass.
 static mla_status plan_checked(const int32_t* seq_lens, const int32_t* q_lens, int32_t B, int32_t num_clusters,
-                               int32_t* out, size_t out_words, mla_plan_info* info, const PlanKind& kind = {}) {
+                               int32_t* out, size_t out_words, mla_plan_info* info, const PlanKind& kind = {},
+                               mla_tree_info* tree_info = nullptr) {
   try {
-    return build_plan(seq_lens, q_lens, B, num_clusters, out, out_words, info, kind);
+    return build_plan(seq_lens, q_lens, B, num_clusters, out, out_words, info, kind, tree_info);
   } catch (const std::bad_alloc&) {
     return fail(MLA_ERR_NO_SPACE, "out of host memory");
   }
@@ -1580,7 +1688,7 @@ static mla_status not_captured(void* stream) {
 // A plan built in memory of the call's own and copied to plan_dev.
 static mla_status plan_upload(const int32_t* seq_lens_host, const int32_t* q_lens_host, int32_t B, int32_t num_clusters,
                               void* plan_dev, size_t plan_bytes, mla_plan_info* info, void* stream,
-                              const PlanKind& kind = {}) {
+                              const PlanKind& kind = {}, mla_tree_info* tree_info = nullptr) {
   CHECK_PTR(plan_dev);
   CHECK_ALIGN16(plan_dev);
   if (B < 0) return fail(MLA_ERR_INVALID_ARG, "B = %d is negative", B);
@@ -1590,12 +1698,13 @@ static mla_status plan_upload(const int32_t* seq_lens_host, const int32_t* q_len
   for (int32_t b = 0; b < B; ++b) T += q_lens_host[b] > 0 ? q_lens_host[b] : 0;
   if (T > INT32_MAX / MLA_NUM_HEADS) return fail(MLA_ERR_INVALID_ARG, "too many query rows");
   size_t need = 0;
-  mla_status s = mla_decode_plan_bytes((int32_t)T, num_clusters, &need);
+  mla_status s = kind.tree ? mla_tree_plan_bytes((int32_t)T, num_clusters, &need)
+                           : mla_decode_plan_bytes((int32_t)T, num_clusters, &need);
   if (s != MLA_OK) return s;
   const size_t words = std::min(plan_bytes, need) / 4;
   std::unique_ptr<int32_t[]> host(new (std::nothrow) int32_t[words + 1]);
   if (!host) return fail(MLA_ERR_NO_SPACE, "out of host memory");
-  s = plan_checked(seq_lens_host, q_lens_host, B, num_clusters, host.get(), words, info, kind);
+  s = plan_checked(seq_lens_host, q_lens_host, B, num_clusters, host.get(), words, info, kind, tree_info);
   if (s == MLA_OK) s = not_captured(stream);
   if (s != MLA_OK) return s;
   // Pageable source: the call returns once the data is staged, so `host` may go.
@@ -1640,10 +1749,10 @@ mla_status mla_window_plan(const int32_t* seq_lens_host, const int32_t* q_lens_h
   return MLA_OK;
 }
 
-static int32_t most_nodes(const int32_t* q_lens, int32_t B) {
-  int32_t most = 0;
-  for (int32_t b = 0; b < B; ++b) most = std::max(most, q_lens[b]);
-  return most;
+mla_status mla_tree_plan_bytes(int32_t T, int32_t num_clusters, size_t* bytes) {
+  mla_status s = mla_decode_plan_bytes(T, num_clusters, bytes);
+  if (s == MLA_OK) *bytes += (size_t)T * mla::kTreeWords * 4;  // each tree has a node at least
+  return s;
 }
 
 mla_status mla_tree_plan_host(const int32_t* seq_lens, const int32_t* q_lens, int32_t B, int32_t num_clusters,
@@ -1651,19 +1760,34 @@ mla_status mla_tree_plan_host(const int32_t* seq_lens, const int32_t* q_lens, in
   CHECK_PTR(plan_host);
   CHECK_PTR(info);
   if (!aligned(plan_host, 4)) return fail(MLA_ERR_MISALIGNED, "plan_host is not 4-byte aligned");
-  mla_status s = plan_checked(seq_lens, q_lens, B, num_clusters, (int32_t*)plan_host, plan_bytes / 4, &info->plan,
-                              {0, 0, true});
-  if (s == MLA_OK) info->max_nodes = most_nodes(q_lens, B);
-  return s;
+  return plan_checked(seq_lens, q_lens, B, num_clusters, (int32_t*)plan_host, plan_bytes / 4, &info->plan, {0, 0, true},
+                      info);
 }
 
 mla_status mla_tree_plan(const int32_t* seq_lens_host, const int32_t* q_lens_host, int32_t B, int32_t num_clusters,
                          void* plan_dev, size_t plan_bytes, mla_tree_info* info, void* stream) {
   CHECK_PTR(info);
-  mla_status s = plan_upload(seq_lens_host, q_lens_host, B, num_clusters, plan_dev, plan_bytes, &info->plan, stream,
-                             {0, 0, true});
-  if (s == MLA_OK) info->max_nodes = most_nodes(q_lens_host, B);
-  return s;
+  return plan_upload(seq_lens_host, q_lens_host, B, num_clusters, plan_dev, plan_bytes, &info->plan, stream,
+                     {0, 0, true}, info);
+}
+
+// Whether a tree decode over the FP8 cache unpacks its pages.  A tile of f16
+// rows takes 0.85 us less than one that has to be converted, over 76 clusters;
+// unpacking costs 0.02 us a page and 9 us: even at twice the pages and 800 tiles
+// (16 sequences of 8 192 tokens: two rows 125 us, unpacked 132; three rows 181
+// and 164; 64 rows over one of 32 768: 880 and 460).
+static bool tree_unpacks(const mla_tree_info& info) {
+  return info.total_pages > 0 && info.total_pages <= kMostUnpackedPages && info.num_trees <= 65535 &&
+         info.plan.total_tiles >= 2 * info.total_pages + kUnpackTiles;
+}
+static size_t unpacked_bytes(const mla_tree_info& info) { return (size_t)info.total_pages * MLA_PAGE_BYTES; }
+
+mla_status mla_tree_workspace_size(const mla_tree_info* info, int32_t fp8, size_t* bytes) {
+  CHECK_PTR(info);
+  CHECK_PTR(bytes);
+  if (info->plan.magic != MLA_TREE_PLAN_MAGIC) return fail(MLA_ERR_INVALID_ARG, "info is not a tree plan summary");
+  *bytes = workspace_bytes_for(info->plan.num_partials) + (fp8 && tree_unpacks(*info) ? unpacked_bytes(*info) : 0);
+  return MLA_OK;
 }
 
 // window: the windowed decode's parameters; tree: the tree decode's; both null
@@ -1673,7 +1797,7 @@ static mla_status decode_common(const void* q_abs, const void* q_r, const void* 
                                 const void* plan_dev, const mla_plan_info* info, float scale, void* workspace,
                                 size_t ws_bytes, void* o_lat, float* lse, int32_t* dev_err, void* stream,
                                 bool fp8, const mla_window_info* window = nullptr,
-                                const mla::TreeArgs* tree = nullptr) {
+                                const mla::TreeArgs* tree = nullptr, const mla_tree_info* tree_info = nullptr) {
   CHECK_PTR(info);
   if (info->magic != (tree ? MLA_TREE_PLAN_MAGIC : window ? MLA_WINDOW_PLAN_MAGIC : MLA_PLAN_MAGIC))
     return fail(MLA_ERR_INVALID_ARG, "info is not a %s plan summary", tree ? "tree" : window ? "window" : "decode");
@@ -1718,9 +1842,27 @@ static mla_status decode_common(const void* q_abs, const void* q_r, const void* 
       return fail(MLA_ERR_INVALID_ARG, "workspace holds %zu bytes, the plan needs %zu", ws_bytes, need_ws);
   }
 
+  const mla::PlanLayout L = mla::plan_layout(info->num_clusters, info->num_segments, info->num_split_rows);
+  const int32_t* plan = (const int32_t*)plan_dev;
+  // A tree decode over the FP8 cache reads a page for many rows: where that
+  // pays and the workspace has the room, the pages are unpacked to f16 once.
+  const bool unpack = fp8 && tree && tree_unpacks(*tree_info) && ws_bytes >= need_ws + unpacked_bytes(*tree_info);
+  if (unpack) {
+    CHECK_PTR(workspace);
+    CHECK_ALIGN16(workspace);
+    uint8_t* out = (uint8_t*)workspace + need_ws;
+    const mla::TreeUnpackArgs u = {(const uint8_t*)kv_cache, kv_scales, num_pages, block_table, tree->masks, plan + L.words,
+                                   (uint4*)out, dev_err, max_pages, info->B, info->T, tree->words,
+                                   (int32_t)tree_info->total_pages};
+    cudaError_t e = mla::launch_tree_unpack(u, tree_info->num_trees, info->max_pages_needed, (cudaStream_t)stream);
+    if (e != cudaSuccess) return cuda_fail(e, "unpack launch");
+    kv_cache = out;
+    num_pages = tree_info->total_pages;
+  }
+
   CUtensorMap kv_map, rope_map;
   mla_status s;
-  if (fp8) {
+  if (fp8 && !unpack) {
     // Codes: a CTA's 256 of each token row, 64 rows per box (no swizzle: the
     // converters read them); RoPE halves as bf16 columns 256.. of the rows.
     const uint64_t cdims[2] = {MLA_FP8_ROW_BYTES, (uint64_t)num_pages * MLA_PAGE_SIZE};
@@ -1781,8 +1923,6 @@ static mla_status decode_common(const void* q_abs, const void* q_r, const void* 
     }
   }
 
-  const mla::PlanLayout L = mla::plan_layout(info->num_clusters, info->num_segments, info->num_split_rows);
-  const int32_t* plan = (const int32_t*)plan_dev;
   float* part_o = (float*)workspace;
   float* part_lse = part_o ? part_o + (size_t)info->num_partials * MLA_NUM_HEADS * MLA_LATENT_DIM : nullptr;
 
@@ -1804,10 +1944,11 @@ static mla_status decode_common(const void* q_abs, const void* q_r, const void* 
   a.B = info->B;
   a.num_segments = info->num_segments;
   a.num_partials = info->num_partials;
-  a.kv_scales = fp8 ? kv_scales : nullptr;
+  a.kv_scales = fp8 && !unpack ? kv_scales : nullptr;
   a.wait_limit = g_decode_wait_limit.load(std::memory_order_relaxed);
   a.wait_every = a.wait_limit < (1ull << 20) ? 0u : 255u;
-  cudaError_t e = tree     ? mla::launch_decode_tree(kv_map, rope_map, a, *tree, info->num_clusters, fp8, (cudaStream_t)stream)
+  const mla::TreeCache cache = unpack ? mla::TreeCache::kUnpacked : fp8 ? mla::TreeCache::kFp8 : mla::TreeCache::kBf16;
+  cudaError_t e = tree     ? mla::launch_decode_tree(kv_map, rope_map, a, *tree, info->num_clusters, cache, (cudaStream_t)stream)
                   : window ? mla::launch_decode_window(kv_map, rope_map, a, win, info->num_clusters, fp8, (cudaStream_t)stream)
                            : mla::launch_decode(kv_map, rope_map, a, info->num_clusters, fp8, (cudaStream_t)stream);
   if (e != cudaSuccess) return cuda_fail(e, "decode launch");
@@ -1872,9 +2013,11 @@ static mla_status decode_tree(const void* q_abs, const void* q_r, const void* kv
   if (info->max_nodes > 64 * words)
     return fail(MLA_ERR_INVALID_ARG, "the plan has a tree of %d nodes, a mask of %d words holds %d", info->max_nodes,
                 words, 64 * words);
+  if (info->num_trees < 0 || info->total_pages < 0)
+    return fail(MLA_ERR_INVALID_ARG, "info is not a tree plan summary");
   const mla::TreeArgs tree = {masks, words};
   return decode_common(q_abs, q_r, kv_cache, kv_scales, num_pages, block_table, max_pages, plan_dev, &info->plan,
-                       scale, workspace, ws_bytes, o_lat, lse, dev_err, stream, fp8, nullptr, &tree);
+                       scale, workspace, ws_bytes, o_lat, lse, dev_err, stream, fp8, nullptr, &tree, info);
 }
 
 mla_status mla_decode_tree(const void* q_abs, const void* q_r, const void* kv_cache, int64_t num_pages,

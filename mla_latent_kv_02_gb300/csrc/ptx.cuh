@@ -532,6 +532,13 @@ __device__ __forceinline__ void tmem_ld32_sync(uint32_t taddr, uint32_t (&r)[32]
                :
                : "memory");
 }
+// Wait for columns that tmem_ld32 asked for, tied to the registers they land in.
+__device__ __forceinline__ void tmem_ld32_wait(uint32_t (&r)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : MLA_RW8(r, 0), MLA_RW8(r, 8), MLA_RW8(r, 16), MLA_RW8(r, 24)
+               :
+               : "memory");
+}
 // Load 64 columns (one row's whole tile slice) and wait; registers tied to the wait.
 __device__ __forceinline__ void tmem_ld64_sync(uint32_t taddr, uint32_t (&r)[64]) {
   asm volatile(

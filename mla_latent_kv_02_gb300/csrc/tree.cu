@@ -9,6 +9,7 @@
 
 #include <cstdint>
 
+#include "fp8.cuh"
 #include "internal.h"
 #include "ptx.cuh"
 
@@ -159,6 +160,75 @@ __global__ void __launch_bounds__(256) compact_kernel(const TreeCompactArgs a) {
   }
 }
 
+// One CTA a page (x) of a tree's sequence (y): its 64 rows of E4M3 codes become
+// f16 rows of 576, code * 2^k and RoPE, each value as the FP8 decode forms it on
+// chip.  A token's scale outside the f16 range counts only where a row sees it:
+// every row sees the tokens before the tree, and the nodes' masks are asked in
+// that case alone.  Rows past the sequence's end become zeros.
+__global__ void __launch_bounds__(256) unpack_kernel(const TreeUnpackArgs a) {
+  const int4 lo = __ldg(reinterpret_cast<const int4*>(a.trees) + 2 * blockIdx.y);
+  const int4 hi = __ldg(reinterpret_cast<const int4*>(a.trees) + 2 * blockIdx.y + 1);
+  const int32_t b = lo.x, base = lo.y, pages = lo.z, n0 = lo.w, len = hi.x, row0 = hi.y, nodes = hi.z;
+  const int t = threadIdx.x, pg = blockIdx.x;
+  if (pg >= pages) return;
+  if (b < 0 || b >= a.B || base < 0 || pages > a.out_pages - base || pages > a.max_pages || n0 < 0 || row0 < 0 ||
+      nodes < 0 || nodes > a.T - row0) {
+    if (t == 0) atomicOr(a.dev_err, (int32_t)MLA_DEVERR_PLAN);
+    return;
+  }
+  int32_t id = __ldg(a.block_table + (int64_t)b * a.max_pages + pg);
+  if (id < 0 || (int64_t)id >= a.num_pages) {
+    if (t == 0) atomicOr(a.dev_err, (int32_t)MLA_DEVERR_PAGE_OOB);
+    id = 0;
+  }
+  const uint4* src = reinterpret_cast<const uint4*>(a.rows + (int64_t)id * MLA_PAGE_SIZE * MLA_FP8_ROW_BYTES);
+  uint4* dst = a.out + ((int64_t)base + pg) * MLA_PAGE_SIZE * (MLA_TOKEN_ELEMS / 8);
+  const int piece = t % 32, r0 = t / 32;  // a warp a row: 32 pieces of 16 codes
+  const int last = min(len - pg * MLA_PAGE_SIZE, MLA_PAGE_SIZE);
+  uint4 code[8];
+  float scale[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const int r = r0 + 8 * j;
+    code[j] = r < last ? __ldg(src + r * (MLA_FP8_ROW_BYTES / 16) + piece) : make_uint4(0u, 0u, 0u, 0u);
+    scale[j] = r < last ? __ldg(a.scales + (int64_t)id * MLA_PAGE_SIZE + r) : 1.f;
+  }
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const int r = r0 + 8 * j;
+    bool ok;
+    const uint32_t f = dev::fp8_f16_factor(scale[j], ok);
+    if (!ok) {
+      const int k = pg * MLA_PAGE_SIZE + r - n0;  // its node
+      bool seen = k < 0;
+      if (k >= 0 && (k >> 6) < a.words)
+        for (int i = k + piece; i < nodes; i += 32)
+          seen = seen || (__ldg(reinterpret_cast<const unsigned long long*>(a.masks) + ((int64_t)row0 + i) * a.words + (k >> 6)) >> (k & 63) & 1);
+      if (seen) atomicOr(a.dev_err, (int32_t)MLA_DEVERR_FP8_RANGE);
+    }
+    const uint32_t c[4] = {code[j].x, code[j].y, code[j].z, code[j].w};
+    uint32_t h[8];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      h[2 * q] = dev::mul_f16x2(dev::e4m3x2_to_f16x2(c[q] & 0xFFFFu), f);
+      h[2 * q + 1] = dev::mul_f16x2(dev::e4m3x2_to_f16x2(c[q] >> 16), f);
+    }
+    uint4* to = dst + r * (MLA_TOKEN_ELEMS / 8) + 2 * piece;
+    to[0] = make_uint4(h[0], h[1], h[2], h[3]);
+    to[1] = make_uint4(h[4], h[5], h[6], h[7]);
+  }
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {  // the 64 RoPE values: eight pieces a row
+    const int r = j * 32 + t / 8, q = t % 8;
+    uint4 v = r < last ? __ldg(src + r * (MLA_FP8_ROW_BYTES / 16) + 32 + q) : make_uint4(0u, 0u, 0u, 0u);
+    v.x = dev::bf16x2_to_f16x2(v.x);
+    v.y = dev::bf16x2_to_f16x2(v.y);
+    v.z = dev::bf16x2_to_f16x2(v.z);
+    v.w = dev::bf16x2_to_f16x2(v.w);
+    dst[r * (MLA_TOKEN_ELEMS / 8) + 64 + q] = v;
+  }
+}
+
 template <int kPieces, bool kScales>
 cudaError_t run_compact(const TreeCompactArgs& a, cudaStream_t stream) {
   compact_kernel<kPieces, kScales><<<dim3(a.B, a.c.layers), 256, 0, stream>>>(a);
@@ -166,6 +236,11 @@ cudaError_t run_compact(const TreeCompactArgs& a, cudaStream_t stream) {
 }
 
 }  // namespace tree
+
+cudaError_t launch_tree_unpack(const TreeUnpackArgs& args, int num_trees, int max_tree_pages, cudaStream_t stream) {
+  tree::unpack_kernel<<<dim3(max_tree_pages, num_trees), 256, 0, stream>>>(args);
+  return cudaGetLastError();
+}
 
 cudaError_t launch_tree_layout(const TreeLayoutArgs& args, cudaStream_t stream) {
   tree::layout_kernel<<<args.B, tree::kMaxNodes, 0, stream>>>(args);

@@ -233,6 +233,90 @@ def test_chain_is_the_causal_decode(api, kind):
     assert api.mla_check(err) == 0 and torch.equal(o, o2) and torch.equal(lse, lse2)
 
 
+def direct(api, plan):
+    """The same plan with the smallest workspace: the FP8 pages are converted tile by tile."""
+    plan.unpack = True                                       # the workspace is not judged again
+    plan.workspace = plan.workspace[:max(16, api.mla_tree_workspace_size(plan.info, False))]
+    return plan
+
+
+@pytest.mark.parametrize("nodes", [[40, 17], [256, 3]])
+def test_unpacked_pages_give_the_same_bits(api, nodes):
+    cache = Cache(api, [2050 + nodes[0], 700 + nodes[1]], "fp8", 11)
+    m = torch.from_numpy(masks([tree(b, n) for b, n in enumerate(nodes)], (max(nodes) + 63) // 64)).cuda()
+    q_abs, q_r = queries(sum(nodes), 11)
+    plans = [api.mla_tree_plan(cache.n, nodes) for _ in range(2)]
+    small = api.mla_tree_workspace_size(plans[0].info, False)
+    assert api.mla_tree_workspace_size(plans[0].info, True) == small + plans[0].info.total_pages * 64 * 1152
+    o, lse, err = decode(api, cache, q_abs, q_r, m, plans[0])
+    assert plans[0].workspace.numel() >= small + plans[0].info.total_pages * 64 * 1152
+    o2, lse2, err2 = decode(api, cache, q_abs, q_r, m, direct(api, plans[1]))
+    assert plans[1].workspace.numel() < plans[0].workspace.numel()
+    assert api.mla_check(err) == 0 and api.mla_check(err2) == 0
+    assert torch.equal(o, o2) and torch.equal(lse, lse2)
+    check(cache, q_abs, q_r, m, o, lse, nodes, set(range(0, sum(nodes), 29)))
+    plans[0] = api.mla_tree_plan([90], [2], into=plans[0])   # buffers kept, judged for the new lengths
+    few = Cache(api, [90], "fp8", 12)
+    m2 = torch.from_numpy(masks([tree(0, 2)], 1)).cuda()
+    o3, lse3, err3 = decode(api, few, q_abs[:2], q_r[:2], m2, plans[0])
+    assert api.mla_check(err3) == 0
+    check(few, q_abs[:2], q_r[:2], m2, o3, lse3, [2])
+
+
+@pytest.mark.parametrize("unpack", [False, True])
+def test_only_seen_scales_are_judged(api, unpack):
+    n0, q = 1500, 64
+    cache = Cache(api, [n0 + q], "fp8", 13)
+    q_abs, q_r = queries(q, 13)
+    full = masks([tree(0, q)], 1)
+    free = full.copy()
+    free[:, 0] &= ~(1 << 20)                                 # no row sees node 20
+    plan = api.mla_tree_plan(cache.n, [q])
+    assert api.mla_tree_workspace_size(plan.info, True) > api.mla_tree_workspace_size(plan.info, False)
+    if not unpack:
+        direct(api, plan)
+
+    def word_after(position, scale, m):
+        page, at = int(cache.bt[0, position // 64]), position % 64
+        held = cache.scales[page, at].clone()
+        cache.scales[page, at] = scale
+        o, lse, err = decode(api, cache, q_abs, q_r, torch.from_numpy(m).cuda(), plan)
+        cache.scales[page, at] = held
+        return int(err.item())
+
+    assert word_after(n0 + 20, 2.0 ** 20, free) == 0 and word_after(n0 + 20, float("nan"), free) == 0
+    assert word_after(n0 + 20, 2.0 ** 20, full) == api.DEVERR_FP8_RANGE
+    assert word_after(700, 2.0 ** -20, free) == api.DEVERR_FP8_RANGE
+    assert word_after(n0 + 63, 2.0 ** 8, full) == api.DEVERR_FP8_RANGE
+    o, lse, err = decode(api, cache, q_abs, q_r, torch.from_numpy(free).cuda(), plan)
+    assert int(err.item()) == 0
+    check(cache, q_abs, q_r, torch.from_numpy(free), o, lse, [q], {0, 19, 20, 21, 63})
+
+
+@pytest.mark.parametrize("kind, unpack", [("bf16", False), ("fp8", False), ("fp8", True)])
+def test_expired_wait_is_reported(api, kind, unpack):
+    """A bound of 64 cycles makes waits run out: the word says so, and the next call on the same buffers is right."""
+    cache = Cache(api, [1500 + 64], kind, 14)
+    q_abs, q_r = queries(64, 14)
+    m = torch.from_numpy(masks([tree(0, 64)], 1)).cuda()
+    plan = api.mla_tree_plan(cache.n, [64])
+    if kind == "fp8" and not unpack:
+        direct(api, plan)
+    o, lse, err = decode(api, cache, q_abs, q_r, m, plan)
+    assert api.mla_check(err) == 0
+    api.mla_debug_set_decode_wait_limit(64)
+    try:
+        late = decode(api, cache, q_abs, q_r, m, plan)[2]
+        torch.cuda.synchronize()
+    finally:
+        api.mla_debug_set_decode_wait_limit(0)
+    with pytest.raises(api.MlaError) as e:
+        api.mla_check(late)
+    assert e.value.status == 6
+    again = decode(api, cache, q_abs, q_r, m, plan)
+    assert api.mla_check(again[2]) == 0 and torch.equal(again[0], o) and torch.equal(again[1], lse)
+
+
 def test_decode_tree_reports_bad_pages_and_refuses(api):
     cache = Cache(api, [200], "bf16", 1)
     q_abs, q_r = queries(3, 1)

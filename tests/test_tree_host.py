@@ -35,8 +35,9 @@ def test_tree_plan_covers_what_each_node_may_see(api, seq, q, clusters):
     off, segs = _segments(plan)
     assert off[0] == 0 and off[-1] == len(segs) and all(a <= b for a, b in zip(off, off[1:]))
     tiles = {t: [] for t in range(len(rows))}
-    for row, b, pb, pe, vis, slot, first, zero in segs:
-        assert rows[row] == (b, first, vis) and 0 <= pb < pe and zero == 0 and -1 <= slot < info.plan.num_partials
+    base = [sum((n + 63) // 64 for n, m in list(zip(seq, q))[:b] if m) for b in range(len(seq))]
+    for row, b, pb, pe, vis, slot, first, page in segs:
+        assert rows[row] == (b, first, vis) and 0 <= pb < pe and page == base[b] and -1 <= slot < info.plan.num_partials
         tiles[row].append((pb, pe, slot))
     for t, (b, first, vis) in enumerate(rows):
         at = 0
@@ -44,6 +45,13 @@ def test_tree_plan_covers_what_each_node_may_see(api, seq, q, clusters):
             assert pb == at and (slot < 0) == (len(tiles[t]) == 1)
             at = pe
         assert at == (vis - 1) // 64 + 1
+    table = plan[(16 + info.plan.num_clusters + 1 + 7) // 8 * 8 + 8 * len(segs) + 4 * info.plan.num_split_rows:]
+    trees = [[int(x) for x in table[8 * k:8 * k + 7]] for k in range(info.num_trees)]
+    held = [b for b, m in enumerate(q) if m]
+    assert trees == [[b, base[b], (seq[b] + 63) // 64, seq[b] - q[b], seq[b], sum(q[:b]), q[b]] for b in held]
+    assert info.total_pages == sum((seq[b] + 63) // 64 for b in held)
+    words = (16 + info.plan.num_clusters + 1 + 7) // 8 * 8 + 8 * len(segs) + 4 * info.plan.num_split_rows + 8 * len(held)
+    assert info.plan.plan_bytes == 4 * words <= api.mla_tree_plan_bytes(len(rows), clusters)
     assert info.plan.total_tiles == sum((vis - 1) // 64 + 1 for _, _, vis in rows)
 
 
@@ -67,18 +75,19 @@ def _lib_call(name, *args):
 def test_decode_tree_refusals(api):
     """Everything is judged before a launch: no GPU is touched."""
     ok, odd = C.c_void_p(1 << 20), C.c_void_p((1 << 20) + 4)
-    _, info = api.mla_tree_plan_host([200, 90], [70, 3], 4)
+    _, info = api.mla_tree_plan_host([200, 2000], [70, 3], 40)
+    assert info.plan.num_partials > 0
     _, full = api.mla_decode_plan_host([200], [70], 4)
     ws = 1 << 28
 
-    def call(masks=ok, words=2, info=info, scale=0.07, q=ok, cols=4, pages=9, w=ok, wb=ws, o=ok, err=ok, table=ok):
+    def call(masks=ok, words=2, info=info, scale=0.07, q=ok, cols=40, pages=9, w=ok, wb=ws, o=ok, err=ok, table=ok):
         return _lib_call("mla_decode_tree", q, ok, ok, pages, table, cols, masks, words, ok, C.byref(info), C.c_float(scale), w,
                          wb, o, None, err, None)
 
     assert call(words=1) == 1                               # 70 nodes need two words
     assert call(words=0) == 1 and call(words=5) == 1
     assert call(masks=None) == 1 and call(masks=odd) == 2
-    assert call(scale=0.0) == 1 and call(q=None) == 1 and call(q=odd) == 2 and call(cols=3) == 1
+    assert call(scale=0.0) == 1 and call(q=None) == 1 and call(q=odd) == 2 and call(cols=31) == 1
     assert call(pages=0) == 1 and call(w=None) == 1 and call(wb=16) == 1 and call(o=None) == 1 and call(err=None) == 1
     wrong = _lib.mla_tree_info()
     wrong.plan = full
