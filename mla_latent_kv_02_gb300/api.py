@@ -806,13 +806,18 @@ def _layers(t, name: str, dtype, page, dev: int):
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if t.get_device() != dev:
         raise ValueError(f"{name} is on {t.device}, the current device is cuda:{dev}")
-    shape = t.shape
-    if len(shape) not in (len(page) + 1, len(page) + 2) or shape[-len(page):] != page:
+    shape, n = t.shape, len(page)
+    if len(shape) == n + 1 and shape[1:] == page:
+        layers, stride, whole = 1, 0, t.is_contiguous()
+    elif len(shape) == n + 2 and shape[2:] == page:
+        layers = shape[0]
+        stride = t.stride(0) * t.element_size()
+        whole = t.is_contiguous() or (layers > 0 and t[0].is_contiguous())
+    else:
         raise ValueError(f"{name} has shape {tuple(shape)}, expected ([layers,] pages, {', '.join(map(str, page))})")
-    layers, stride = (shape[0], t.stride(0) * t.element_size()) if len(shape) > len(page) + 1 else (1, 0)
-    if not (t.is_contiguous() or (len(shape) > len(page) + 1 and layers > 0 and t[0].is_contiguous())):
+    if not whole:
         raise ValueError(f"{name}: a layer's pages must be contiguous")
-    return t.data_ptr(), shape[-len(page) - 1], layers, stride
+    return t.data_ptr(), shape[-n - 1], layers, stride
 
 
 def _fp8_layers(rows, scales, dev: int):
@@ -854,16 +859,17 @@ def mla_copy_pages_nvfp4(rows, src, dst, stream=None) -> None:
 
 # ------------------------------------------------------------------ trees of drafted tokens
 def _table(block_table, B: int, dev: int):
-    if not isinstance(block_table, torch.Tensor) or block_table.dim() != 2 or block_table.shape[0] < B:
+    shape = block_table.shape if isinstance(block_table, torch.Tensor) else ()
+    if len(shape) != 2 or shape[0] < B:
         raise ValueError(f"block_table must be [sequences, pages] of at least {B} sequences")
-    return _in(block_table, "block_table", torch.int32, tuple(block_table.shape), dev), block_table.shape[1]
+    return _in(block_table, "block_table", torch.int32, shape, dev), shape[1]
 
 
 def _masks(masks, T: int, dev: int):
-    if not isinstance(masks, torch.Tensor) or masks.dim() != 2:
-        raise ValueError("masks must be a tensor [nodes, words]")
-    words = masks.shape[1]
-    return _in(masks, "masks", torch.int64, (T, words), dev), words
+    shape = masks.shape if isinstance(masks, torch.Tensor) else ()
+    if len(shape) != 2 or shape[0] != T:
+        raise ValueError(f"masks must be a tensor [nodes, words] of {T} nodes")
+    return _in(masks, "masks", torch.int64, shape, dev), shape[1]
 
 
 def mla_tree_layout(parents, q_starts, seq_lens, masks, dev_err, positions=None, slots=None, block_table=None,

@@ -393,13 +393,16 @@ __device__ __forceinline__ void decode_body(const CUtensorMap& kv_map, const CUt
     mbar_init(BAR(B_DRAIN_PV), 1);
     fence_mbar_init();
   }
-  if (threadIdx.x == 64) {
+  // A tree's cluster may hold dozens of segments: a lane looks at each of them
+  // (one thread took 0.3 us a segment before the first page could be asked for).
+  constexpr int kCheckers = kTree ? 32 : 1;
+  if (threadIdx.x >= 64 && threadIdx.x < 64 + kCheckers) {
     // Validate this cluster's plan range; an inconsistent plan (or a shared
     // memory window that cannot hold the aligned layout) is skipped whole, by
     // every role alike, and reported instead of being dereferenced.
     int32_t sb = a.seg_off[cid], se = a.seg_off[cid + 1];
     bool good = layout_fits && sb >= 0 && se >= sb && se <= a.num_segments;
-    for (int s = sb; good && s < se; ++s) {
+    for (int s = sb + (int)threadIdx.x - 64; good && s < se; s += kCheckers) {
       const int32_t* sg = a.segs + 8 * s;
       const int32_t row = sg[0], b = sg[1], pb = sg[2], pe = sg[3], vis = sg[4], slot = sg[5];
       good = row >= 0 && row < a.T && b >= 0 && b < a.B && pb >= 0 && pe > pb && pe <= a.max_pages && vis >= 1 &&
@@ -416,12 +419,15 @@ __device__ __forceinline__ void decode_body(const CUtensorMap& kv_map, const CUt
         good = first >= 0 && first < vis && vis - first <= 64 * tree->words;
       }
     }
-    if (!good) {
-      atomicOr(err, (int32_t)MLA_DEVERR_PLAN);
-      sb = se = 0;
+    if (kTree) good = __all_sync(0xffffffffu, good);
+    if (threadIdx.x == 64) {
+      if (!good) {
+        atomicOr(err, (int32_t)MLA_DEVERR_PLAN);
+        sb = se = 0;
+      }
+      seg_range[0] = sb;
+      seg_range[1] = se;
     }
-    seg_range[0] = sb;
-    seg_range[1] = se;
   }
   // Row-max slots start with an impossible tile tag; the ones tile feeds the
   // row-sum MMA (written by the generic proxy, read by the tensor core).
@@ -461,6 +467,10 @@ __device__ __forceinline__ void decode_body(const CUtensorMap& kv_map, const CUt
     if (lane == 0) {
       uint32_t g = 0;
       bool ok = true;
+      if (kRowWarps && s_begin < s_end) {  // the first row's queries: their later rounds find them in L2
+        const size_t qrow = (size_t)a.segs[8 * s_begin];
+        prefetch_l2_bulk(reinterpret_cast<const uint8_t*>(a.q_abs) + qrow * (kH * kDC * 2) + rank * (kH * kDC), kH * kDC);
+      }
       for (int s = s_begin; s < s_end && ok; ++s) {
         const int32_t* sg = a.segs + 8 * s;
         const int b = sg[1], pb = sg[2], pe = sg[3];
@@ -1270,15 +1280,15 @@ __device__ __forceinline__ void decode_body(const CUtensorMap& kv_map, const CUt
     __syncwarp();
   };
   if constexpr (kRowWarps) {
-    // 512 threads x 128 registers at launch: 128*96 + 256*160 + 128*96.
+    // 512 threads x 128 registers at launch: 128*88 + 256*160 + 128*104.
     if (warp < 4) {
-      regs_dec<96>();
+      regs_dec<88>();
       if (warp == 0) role_producer();
       else if (warp == 1) role_qk();
       else if (warp == kPvWarp) role_pv();
       cluster_wait();
     } else if (warp >= 12) {
-      regs_dec<96>();
+      regs_dec<104>();
       role_rows();
       cluster_wait();
     } else {

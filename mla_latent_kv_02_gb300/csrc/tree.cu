@@ -7,6 +7,7 @@
 // chain of tokens for each step; a tree is the same draft with alternatives.
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cstdint>
 
 #include "fp8.cuh"
@@ -46,6 +47,8 @@ __global__ void __launch_bounds__(kMaxNodes) layout_kernel(const TreeLayoutArgs 
     atomicOr(a.dev_err, (int32_t)MLA_DEVERR_TREE);
     p = -1;
   }
+  int64_t at = -1;  // asked for now, used after the rounds
+  if (a.slots && in) at = slot_of(a.block_table + (int64_t)b * a.max_pages, a.max_pages, a.num_pages, len - n + i);
   uint64_t m[kMaxWords];
 #pragma unroll
   for (int w = 0; w < kMaxWords; ++w) mask[w][i] = m[w] = i / 64 == w ? 1ull << (i % 64) : 0ull;
@@ -76,9 +79,8 @@ __global__ void __launch_bounds__(kMaxNodes) layout_kernel(const TreeLayoutArgs 
     if (w < a.words) a.masks[row * a.words + w] = m[w];
   if (a.positions) a.positions[row] = len - n + d - 1;
   if (a.slots) {
-    const int64_t s = slot_of(a.block_table + (int64_t)b * a.max_pages, a.max_pages, a.num_pages, len - n + i);
-    if (s < 0) atomicOr(a.dev_err, (int32_t)MLA_DEVERR_PAGE_OOB);
-    a.slots[row] = s;
+    if (at < 0) atomicOr(a.dev_err, (int32_t)MLA_DEVERR_PAGE_OOB);
+    a.slots[row] = at;
   }
 }
 
@@ -86,7 +88,8 @@ __global__ void __launch_bounds__(kMaxNodes) layout_kernel(const TreeLayoutArgs 
 // slot n0 + k_r to slot n0 + r in every layer.  k_r >= r and rises with r, so a
 // row may be written as soon as the rows up to it have been read: a batch is
 // loaded, a barrier, and stored, and no batch needs a slot that an earlier one
-// wrote.
+// wrote.  A CTA takes a sequence (x) in `per` layers (y), layer after layer, so
+// that the look-up of its slots, four loads one behind the other, is paid once.
 template <int kPieces, bool kScales>
 struct CompactCfg {
   static constexpr int kPer = kPieces + (kScales ? 1 : 0);  // threads a row: its 16-byte pieces and its scale
@@ -95,15 +98,16 @@ struct CompactCfg {
 };
 
 template <int kPieces, bool kScales>
-__global__ void __launch_bounds__(256) compact_kernel(const TreeCompactArgs a) {
+__global__ void __launch_bounds__(256) compact_kernel(const TreeCompactArgs a, int per) {
   using C = CompactCfg<kPieces, kScales>;
   __shared__ int64_t slot[kMaxNodes];
   __shared__ int16_t node[kMaxNodes];
-  const int b = blockIdx.x, layer = blockIdx.y, t = threadIdx.x;
+  const int b = blockIdx.x, layer0 = blockIdx.y * per, t = threadIdx.x;
+  const bool first = blockIdx.y == 0;
   const int32_t q0 = __ldg(a.q_starts + b), q1 = __ldg(a.q_starts + b + 1), len = __ldg(a.seq_lens + b);
   const int32_t acc = __ldg(a.accepted + b), n = q1 - q0;
   if (q0 < 0 || q1 < q0 || q1 > a.T || n > 64 * a.words || n > len || acc < -1 || acc >= n) {
-    if (t == 0 && layer == 0) atomicOr(a.dev_err, (int32_t)MLA_DEVERR_TREE);
+    if (t == 0 && first) atomicOr(a.dev_err, (int32_t)MLA_DEVERR_TREE);
     return;
   }
   int kept = 0, rank = 0;
@@ -121,41 +125,46 @@ __global__ void __launch_bounds__(256) compact_kernel(const TreeCompactArgs a) {
       kept += __popcll(m);
     }
   }
-  if (t == 0 && layer == 0) a.new_lens[b] = len - n + kept;
+  if (t == 0 && first) a.new_lens[b] = len - n + kept;
   if (t <= acc) {
     slot[t] = slot_of(a.block_table + (int64_t)b * a.max_pages, a.max_pages, a.c.num_pages, len - n + t);
     if (mine) {
-      if (slot[t] < 0 && layer == 0) atomicOr(a.dev_err, (int32_t)MLA_DEVERR_PAGE_OOB);
+      if (slot[t] < 0 && first) atomicOr(a.dev_err, (int32_t)MLA_DEVERR_PAGE_OOB);
       node[rank] = (int16_t)t;
     }
   }
   __syncthreads();
   const int piece = t % C::kPer, r0 = t / C::kPer;
-  uint4* rows = reinterpret_cast<uint4*>(a.c.rows + layer * a.c.row_stride);
-  float* scales = kScales ? reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(a.c.scales) + layer * a.c.scale_stride) : nullptr;
-  for (int k0 = 0; k0 < kept; k0 += C::kRows * C::kBatch) {
+  const int units = min(per, a.c.layers - layer0) * kept;  // unit u: kept row u % kept of layer layer0 + u / kept
+  for (int u0 = 0; u0 < units; u0 += C::kRows * C::kBatch) {
     uint4 v[C::kBatch];
-    bool moves[C::kBatch];
+    uint8_t* to[C::kBatch];
 #pragma unroll
     for (int j = 0; j < C::kBatch; ++j) {
-      const int k = k0 + j * C::kRows + r0;
-      moves[j] = r0 < C::kRows && k < kept && node[k] != k && slot[node[k]] >= 0 && slot[k] >= 0;
-      if (!moves[j]) continue;
-      const int64_t s = slot[node[k]];
-      if (kScales && piece == kPieces)
-        v[j].x = __float_as_uint(scales[s]);
-      else
-        v[j] = rows[s * kPieces + piece];
+      const int u = u0 + j * C::kRows + r0;
+      to[j] = nullptr;
+      if (r0 >= C::kRows || u >= units) continue;
+      const int layer = layer0 + u / kept, k = u % kept;
+      const int64_t src = slot[node[k]], dst = slot[k];
+      if (node[k] == k || src < 0 || dst < 0) continue;
+      if (kScales && piece == kPieces) {
+        uint8_t* scales = reinterpret_cast<uint8_t*>(a.c.scales) + layer * a.c.scale_stride;
+        v[j].x = *reinterpret_cast<const uint32_t*>(scales + src * 4);
+        to[j] = scales + dst * 4;
+      } else {
+        uint8_t* rows = a.c.rows + layer * a.c.row_stride;
+        v[j] = *reinterpret_cast<const uint4*>(rows + (src * kPieces + piece) * 16);
+        to[j] = rows + (dst * kPieces + piece) * 16;
+      }
     }
     __syncthreads();
 #pragma unroll
     for (int j = 0; j < C::kBatch; ++j) {
-      if (!moves[j]) continue;
-      const int64_t d = slot[k0 + j * C::kRows + r0];
+      if (!to[j]) continue;
       if (kScales && piece == kPieces)
-        scales[d] = __uint_as_float(v[j].x);
+        *reinterpret_cast<uint32_t*>(to[j]) = v[j].x;
       else
-        rows[d * kPieces + piece] = v[j];
+        *reinterpret_cast<uint4*>(to[j]) = v[j];
     }
   }
 }
@@ -231,7 +240,11 @@ __global__ void __launch_bounds__(256) unpack_kernel(const TreeUnpackArgs a) {
 
 template <int kPieces, bool kScales>
 cudaError_t run_compact(const TreeCompactArgs& a, cudaStream_t stream) {
-  compact_kernel<kPieces, kScales><<<dim3(a.B, a.c.layers), 256, 0, stream>>>(a);
+  // up to six CTAs an SM: more layers to a CTA beyond that (64 sequences in 60
+  // layers: 8.0 us in a stream, 10.3 with a CTA for each, floor 5.5)
+  const int64_t most = 6 * 152;
+  const int per = (int)std::min<int64_t>(a.c.layers, ((int64_t)a.B * a.c.layers + most - 1) / most);
+  compact_kernel<kPieces, kScales><<<dim3(a.B, (a.c.layers + per - 1) / per), 256, 0, stream>>>(a, per);
   return cudaGetLastError();
 }
 
