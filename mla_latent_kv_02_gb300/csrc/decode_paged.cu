@@ -454,6 +454,7 @@ __device__ __forceinline__ void decode_body(const CUtensorMap& kv_map, const CUt
   // arrives here, the softmax warps wait before their first push and the
   // others before the exit barrier, so that the loads start at once.
   cluster_arrive();
+  if (kUnpacked) grid_dependency_wait();           // the unpacked pages
   if (threadIdx.x == 0) grid_launch_dependents();  // the combine's blocks may take their places
   const uint32_t tmem = *tmem_slot;
 
@@ -1419,8 +1420,7 @@ static cudaError_t run_tree(const CUtensorMap& kv_map, const CUtensorMap& rope_m
   constexpr int smem = L::kSmemBytes;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  kern<<<2 * num_clusters, L::kThreads, smem, stream>>>(kv_map, rope_map, args, tree);
-  return cudaGetLastError();
+  return launch_dependent(kern, dim3(2 * num_clusters), L::kThreads, smem, kF16 && !kF8, stream, kv_map, rope_map, args, tree);
 }
 
 cudaError_t decode_max_clusters(int* out) {

@@ -373,7 +373,7 @@ mla_status no_throw(F&& body) {
 
 // A tree decode unpacks at most so many pages of the FP8 cache (4.5 GB).
 constexpr int64_t kMostUnpackedPages = 1 << 16;
-constexpr int64_t kUnpackTiles = 800;
+constexpr int64_t kUnpackTiles = 256;
 
 size_t workspace_bytes_for(int64_t partials) {
   return (size_t)partials * (MLA_NUM_HEADS * MLA_LATENT_DIM * 4 + MLA_NUM_HEADS * 4);
@@ -1771,14 +1771,16 @@ mla_status mla_tree_plan(const int32_t* seq_lens_host, const int32_t* q_lens_hos
                      {0, 0, true}, info);
 }
 
-// Whether a tree decode over the FP8 cache unpacks its pages.  A tile of f16
-// rows takes 0.85 us less than one that has to be converted, over 76 clusters;
-// unpacking costs 0.02 us a page and 9 us: even at twice the pages and 800 tiles
-// (16 sequences of 8 192 tokens: two rows 125 us, unpacked 132; three rows 181
-// and 164; 64 rows over one of 32 768: 880 and 460).
+// Whether a tree decode over the FP8 cache unpacks its pages: with two rows to a
+// page or more (a sequence's first row may need one page less), and enough tiles
+// to pay for a launch.  A tile of f16 rows takes half the time of one that has to
+// be converted; unpacked and not: 16 sequences of 8 192 tokens, two rows 113 and
+// 125 us, three rows of 2 048 tokens 53 and 64; 12 rows over 4 096 tokens 31 and
+// 36; 16 rows over 1 024 (272 tiles) 26.7 and 27.0; 64 rows over 32 768 459 and
+// 880.
 static bool tree_unpacks(const mla_tree_info& info) {
   return info.total_pages > 0 && info.total_pages <= kMostUnpackedPages && info.num_trees <= 65535 &&
-         info.plan.total_tiles >= 2 * info.total_pages + kUnpackTiles;
+         info.plan.total_tiles >= kUnpackTiles && info.plan.total_tiles + info.num_trees >= 2 * info.total_pages;
 }
 static size_t unpacked_bytes(const mla_tree_info& info) { return (size_t)info.total_pages * MLA_PAGE_BYTES; }
 

@@ -179,6 +179,7 @@ __global__ void __launch_bounds__(256) unpack_kernel(const TreeUnpackArgs a) {
   const int4 hi = __ldg(reinterpret_cast<const int4*>(a.trees) + 2 * blockIdx.y + 1);
   const int32_t b = lo.x, base = lo.y, pages = lo.z, n0 = lo.w, len = hi.x, row0 = hi.y, nodes = hi.z;
   const int t = threadIdx.x, pg = blockIdx.x;
+  if (t == 0) dev::grid_launch_dependents();  // the decode may get ready; it waits before it reads a page
   if (pg >= pages) return;
   if (b < 0 || b >= a.B || base < 0 || pages > a.out_pages - base || pages > a.max_pages || n0 < 0 || row0 < 0 ||
       nodes < 0 || nodes > a.T - row0) {
@@ -192,39 +193,39 @@ __global__ void __launch_bounds__(256) unpack_kernel(const TreeUnpackArgs a) {
   }
   const uint4* src = reinterpret_cast<const uint4*>(a.rows + (int64_t)id * MLA_PAGE_SIZE * MLA_FP8_ROW_BYTES);
   uint4* dst = a.out + ((int64_t)base + pg) * MLA_PAGE_SIZE * (MLA_TOKEN_ELEMS / 8);
-  const int piece = t % 32, r0 = t / 32;  // a warp a row: 32 pieces of 16 codes
+  // Eight codes and one 16-byte store a thread, two warps a row: a warp stores
+  // 512 bytes in one piece (16 codes and two stores left half sectors: 100 MB
+  // through L2 for 38).
+  constexpr int kRows = 8;  // of a thread at a time
+  const int piece = t % 64, r0 = t / 64;
   const int last = min(len - pg * MLA_PAGE_SIZE, MLA_PAGE_SIZE);
-  uint4 code[8];
-  float scale[8];
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    const int r = r0 + 8 * j;
-    code[j] = r < last ? __ldg(src + r * (MLA_FP8_ROW_BYTES / 16) + piece) : make_uint4(0u, 0u, 0u, 0u);
-    scale[j] = r < last ? __ldg(a.scales + (int64_t)id * MLA_PAGE_SIZE + r) : 1.f;
-  }
+  for (int half = 0; half < 2; ++half) {
+    uint2 code[kRows];
+    float scale[kRows];
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    const int r = r0 + 8 * j;
-    bool ok;
-    const uint32_t f = dev::fp8_f16_factor(scale[j], ok);
-    if (!ok) {
-      const int k = pg * MLA_PAGE_SIZE + r - n0;  // its node
-      bool seen = k < 0;
-      if (k >= 0 && (k >> 6) < a.words)
-        for (int i = k + piece; i < nodes; i += 32)
-          seen = seen || (__ldg(reinterpret_cast<const unsigned long long*>(a.masks) + ((int64_t)row0 + i) * a.words + (k >> 6)) >> (k & 63) & 1);
-      if (seen) atomicOr(a.dev_err, (int32_t)MLA_DEVERR_FP8_RANGE);
+    for (int j = 0; j < kRows; ++j) {
+      const int r = 32 * half + r0 + 4 * j;
+      code[j] = r < last ? __ldg(reinterpret_cast<const uint2*>(src + r * (MLA_FP8_ROW_BYTES / 16)) + piece) : make_uint2(0u, 0u);
+      scale[j] = r < last ? __ldg(a.scales + (int64_t)id * MLA_PAGE_SIZE + r) : 1.f;
     }
-    const uint32_t c[4] = {code[j].x, code[j].y, code[j].z, code[j].w};
-    uint32_t h[8];
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      h[2 * q] = dev::mul_f16x2(dev::e4m3x2_to_f16x2(c[q] & 0xFFFFu), f);
-      h[2 * q + 1] = dev::mul_f16x2(dev::e4m3x2_to_f16x2(c[q] >> 16), f);
+    for (int j = 0; j < kRows; ++j) {
+      const int r = 32 * half + r0 + 4 * j;
+      bool ok;
+      const uint32_t f = dev::fp8_f16_factor(scale[j], ok);
+      if (!ok) {
+        const int k = pg * MLA_PAGE_SIZE + r - n0;  // its node
+        bool seen = k < 0;
+        if (k >= 0 && (k >> 6) < a.words)
+          for (int i = k + piece; i < nodes; i += 64)
+            seen = seen || (__ldg(reinterpret_cast<const unsigned long long*>(a.masks) + ((int64_t)row0 + i) * a.words + (k >> 6)) >> (k & 63) & 1);
+        if (seen) atomicOr(a.dev_err, (int32_t)MLA_DEVERR_FP8_RANGE);
+      }
+      dst[r * (MLA_TOKEN_ELEMS / 8) + piece] =
+          make_uint4(dev::mul_f16x2(dev::e4m3x2_to_f16x2(code[j].x & 0xFFFFu), f), dev::mul_f16x2(dev::e4m3x2_to_f16x2(code[j].x >> 16), f),
+                     dev::mul_f16x2(dev::e4m3x2_to_f16x2(code[j].y & 0xFFFFu), f), dev::mul_f16x2(dev::e4m3x2_to_f16x2(code[j].y >> 16), f));
     }
-    uint4* to = dst + r * (MLA_TOKEN_ELEMS / 8) + 2 * piece;
-    to[0] = make_uint4(h[0], h[1], h[2], h[3]);
-    to[1] = make_uint4(h[4], h[5], h[6], h[7]);
   }
 #pragma unroll
   for (int j = 0; j < 2; ++j) {  // the 64 RoPE values: eight pieces a row
