@@ -835,7 +835,7 @@ mla_status mla_tree_plan(const int32_t* seq_lens_host, const int32_t* q_lens_hos
  * Workspace bytes of a tree decode.  mla_decode_workspace_size(num_clusters), or
  * what the plan's split rows need of it, is enough for either cache.  Over the
  * FP8 cache (fp8 != 0), where several rows read each page, the size given here
- * has room for those pages in f16 (72 KB a page, up to 4.5 GB): with it the
+ * has room for those pages in f16 (72 KB a page, up to 4.8 GB): with it the
  * decode unpacks a page once instead of once a row.  The results are the same,
  * bit for bit.
  */

@@ -730,8 +730,6 @@ def _planned(cls, buf, info, num_clusters: int, device, stream, into):
     if (into is not None and into.plan.numel() >= words and into.workspace.numel() >= ws_bytes
             and into.plan.device == device):
         plan = replace(into)
-        if cls is TreePlan:
-            plan.unpack = None  # judged for the new lengths
     else:
         with torch.cuda.stream(stream):
             plan = _plan_buffers(cls, words, ws_bytes, device)
@@ -743,16 +741,21 @@ def _planned(cls, buf, info, num_clusters: int, device, stream, into):
 
 def _room_to_unpack(plan, stream, dev: int) -> None:
     """Before a tree plan's first decode over the FP8 cache: a workspace with room
-    for the pages in f16, taken on the stream of the call."""
+    for the pages in f16, taken on the stream of the call.  Where the memory
+    cannot be had the decode converts its pages tile by tile."""
+    plan.unpack = True
     need = mla_tree_workspace_size(plan.info, True)
-    if plan.workspace.numel() < need:
-        raw = _on(stream, dev)
-        on = _torch_stream(stream, raw, dev)
+    if plan.workspace.numel() >= need:
+        return
+    raw = _on(stream, dev)
+    on = _torch_stream(stream, raw, dev)
+    try:
         with torch.cuda.stream(on):
             plan.workspace = torch.empty(need, dtype=torch.uint8, device=plan.plan.device)
-        plan.plan.record_stream(on)
-        plan.streams = {raw}  # the others learn of the new block when they next use it
-    plan.unpack = True
+    except torch.OutOfMemoryError:
+        return
+    plan.plan.record_stream(on)
+    plan.streams = {raw}  # the others learn of the new block when they next use it
 
 
 def mla_decode_window(q_abs, q_r, kv_cache, block_table, plan: WindowPlan, o_lat, dev_err, lse=None,
@@ -925,7 +928,9 @@ class TreePlan:
     workspace: torch.Tensor     # uint8 device buffer
     host: torch.Tensor          # pinned int32 staging of the plan (reused by `into=`)
     streams: set = field(default_factory=set, repr=False, compare=False)  # raw handles of the streams that use the buffers
-    unpack: Optional[bool] = field(default=None, repr=False, compare=False)  # the workspace holds an FP8 cache's pages in f16
+    rows: int = 0               # the summary's T and B, at hand for every call
+    seqs: int = 0
+    unpack: bool = field(default=False, repr=False, compare=False)  # the workspace was judged for an FP8 cache
 
     @property
     def num_clusters(self) -> int:
@@ -942,7 +947,9 @@ def mla_tree_plan(seq_lens: Sequence[int], q_lens: Sequence[int], device=None, n
     if num_clusters is None:
         num_clusters = mla_decode_max_clusters()
     buf, info = mla_tree_plan_host(seq_lens, q_lens, num_clusters)
-    return _planned(TreePlan, buf, info, num_clusters, device, stream, into)
+    plan = _planned(TreePlan, buf, info, num_clusters, device, stream, into)
+    plan.rows, plan.seqs, plan.unpack = int(info.plan.T), int(info.plan.B), False
+    return plan
 
 
 def mla_decode_tree(q_abs, q_r, kv_cache, block_table, masks, plan: TreePlan, o_lat, dev_err, lse=None,
@@ -972,15 +979,13 @@ def mla_decode_tree_fp8(q_abs, q_r, rows, scales, block_table, masks, plan: Tree
 def _decode_tree(call, cache, pages, q_abs, q_r, block_table, masks, plan, o_lat, dev_err, lse, scale, stream, dev) -> None:
     if not isinstance(plan, TreePlan):
         raise TypeError("plan must come from mla_tree_plan")
-    T, sums = q_abs.shape[0], plan.info.plan
-    if sums.T != T:
-        raise ValueError(f"plan has {sums.T} rows, q_abs has {T}")
+    T, ws = plan.rows, plan.workspace
     m, words = _masks(masks, T, dev)
-    table, cols = _table(block_table, sums.B, dev)
-    ws_bytes = plan.workspace.numel()
+    table, cols = _table(block_table, plan.seqs, dev)
+    if plan.plan.get_device() != dev or ws.get_device() != dev:
+        raise ValueError(f"the plan is on {plan.plan.device}, the current device is cuda:{dev}")
     _check(call(_in(q_abs, "q_abs", torch.bfloat16, (T, H, D_C), dev), _in(q_r, "q_r", torch.bfloat16, (T, H, D_R), dev),
-                *cache, pages, table, cols, m, words, _in(plan.plan, "plan.plan", torch.int32, (plan.plan.numel(),), dev),
-                plan.info, float(scale), _in(plan.workspace, "plan.workspace", torch.uint8, (ws_bytes,), dev), ws_bytes,
+                *cache, pages, table, cols, m, words, plan.plan.data_ptr(), plan.info, scale, ws.data_ptr(), ws.numel(),
                 _in(o_lat, "o_lat", torch.bfloat16, (T, H, D_C), dev),
                 None if lse is None else _in(lse, "lse", torch.float32, (T, H), dev),
                 _in(dev_err, "dev_err", torch.int32, (1,), dev), _use(plan, stream, dev)))

@@ -371,7 +371,7 @@ mla_status no_throw(F&& body) {
   }
 }
 
-// A tree decode unpacks at most so many pages of the FP8 cache (4.5 GB).
+// A tree decode unpacks at most so many pages of the FP8 cache (4.8 GB).
 constexpr int64_t kMostUnpackedPages = 1 << 16;
 constexpr int64_t kUnpackTiles = 256;
 

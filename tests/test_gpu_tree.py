@@ -263,6 +263,85 @@ def test_unpacked_pages_give_the_same_bits(api, nodes):
     check(few, q_abs[:2], q_r[:2], m2, o3, lse3, [2])
 
 
+def test_unpacked_decode_is_captured(api):
+    """First use of a plan inside a capture, two graphs of one plan, replayed in turn after the cache has changed."""
+    n0, q = 1200, 48
+    caches = [Cache(api, [n0 + q], "fp8", s) for s in (21, 22)]
+    m = torch.from_numpy(masks([tree(0, q)], 1)).cuda()
+    q_abs, q_r = queries(q, 21)
+    plan = api.mla_tree_plan(caches[0].n, [q])
+    warm = api.mla_tree_plan(caches[0].n, [q])
+    want = [decode(api, c, q_abs, q_r, m, warm)[0] for c in caches]
+    rows, scales, table = caches[0].rows.clone(), caches[0].scales.clone(), caches[0].table.clone()
+    live = Cache.__new__(Cache)
+    live.kind, live.n, live.rows, live.scales, live.table = "fp8", caches[0].n, rows, scales, table
+    outs, graphs, err = [torch.zeros_like(want[0]) for _ in range(2)], [], word()
+    lse = torch.zeros((q, 128), dtype=torch.float32, device="cuda")
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    for o in outs:
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=side):
+            decode(api, live, q_abs, q_r, m, plan, o=o, lse=lse, err=err)
+        graphs.append(graph)
+    assert plan.workspace.numel() >= api.mla_tree_workspace_size(plan.info, True)
+    for turn in (0, 1, 0):
+        rows.copy_(caches[turn].rows)
+        scales.copy_(caches[turn].scales)
+        table.copy_(caches[turn].table)
+        for o, graph in zip(outs, graphs):
+            o.zero_()
+            graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(outs[0], want[turn]) and torch.equal(outs[1], want[turn]), turn
+    assert int(err.item()) == 0
+
+
+@pytest.mark.parametrize("kind", ["bf16", "fp8"])
+def test_decodes_on_other_streams(api, kind):
+    """One plan, uploaded on one stream, decoded on two others one after the other, dropped while queued."""
+    cache = Cache(api, [700 + 40, 300 + 9], kind, 31)
+    nodes = [40, 9]
+    m = torch.from_numpy(masks([tree(b, n) for b, n in enumerate(nodes)], 1)).cuda()
+    q_abs, q_r = queries(49, 31)
+    want, want_lse, _ = decode(api, cache, q_abs, q_r, m, api.mla_tree_plan(cache.n, nodes))
+    a, b = torch.cuda.Stream(), torch.cuda.Stream()
+    outs = [(torch.zeros_like(want), torch.zeros_like(want_lse)) for _ in range(2)]
+    err = word()
+    torch.cuda.synchronize()
+    plan = api.mla_tree_plan(cache.n, nodes, stream=a)
+    decode(api, cache, q_abs, q_r, m, plan, stream=a, o=outs[0][0], lse=outs[0][1], err=err)
+    b.wait_stream(a)
+    with torch.cuda.stream(b):
+        decode(api, cache, q_abs, q_r, m, plan, o=outs[1][0], lse=outs[1][1], err=err)
+    del plan
+    junk = [torch.full((1 << 24,), 255, dtype=torch.uint8, device="cuda") for _ in range(8)]  # blocks that are free again
+    torch.cuda.synchronize()
+    assert int(err.item()) == 0 and len(junk) == 8
+    for o, lse in outs:
+        assert torch.equal(o, want) and torch.equal(lse, want_lse)
+
+
+def test_two_plans_at_once(api):
+    """Decodes of two plans in flight on two streams do not touch each other."""
+    caches = [Cache(api, [900 + 24], "bf16", 41), Cache(api, [1500 + 40], "fp8", 42)]
+    nodes = [24, 40]
+    ms = [torch.from_numpy(masks([tree(5, n)], 1)).cuda() for n in nodes]
+    qs = [queries(n, 50 + n) for n in nodes]
+    want = [decode(api, c, *q, m, api.mla_tree_plan(c.n, [n])) for c, q, m, n in zip(caches, qs, ms, nodes)]
+    streams = [torch.cuda.Stream() for _ in nodes]
+    torch.cuda.synchronize()
+    plans = [api.mla_tree_plan(c.n, [n], stream=s) for c, n, s in zip(caches, nodes, streams)]
+    outs = [(torch.zeros_like(w[0]), torch.zeros_like(w[1]), word()) for w in want]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for c, q, m, p, s, (o, lse, err) in zip(caches, qs, ms, plans, streams, outs):
+            decode(api, c, *q, m, p, stream=s, o=o, lse=lse, err=err)
+    torch.cuda.synchronize()
+    for w, (o, lse, err) in zip(want, outs):
+        assert int(err.item()) == 0 and torch.equal(o, w[0]) and torch.equal(lse, w[1])
+
+
 @pytest.mark.parametrize("unpack", [False, True])
 def test_only_seen_scales_are_judged(api, unpack):
     n0, q = 1500, 64
