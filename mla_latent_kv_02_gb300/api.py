@@ -100,17 +100,18 @@ def mla_kv_bytes(layers: int, dc: int, dr: int, elem_bytes: int, tokens: int, se
 
 
 _P32 = C.POINTER(C.c_int32)
+_NP_I32 = np.dtype(np.int32)
 
 
 def _i32(x, name: str) -> np.ndarray:
     """Host values as a contiguous int32 array; what int32 does not hold is refused."""
+    if type(x) is np.ndarray and x.dtype is _NP_I32 and x.flags.c_contiguous:
+        return x
     v = np.asarray(x)
-    if type(x) is not np.ndarray or v.dtype != np.int32:
-        a = np.ascontiguousarray(v, dtype=np.int32)
-        if (a != v).any():
-            raise ValueError(f"{name} must be whole numbers that int32 holds")
-        return a
-    return np.ascontiguousarray(v)
+    a = np.ascontiguousarray(v, dtype=np.int32)
+    if (a != v).any():
+        raise ValueError(f"{name} must be whole numbers that int32 holds")
+    return a
 
 
 class MlaPool:

