@@ -570,25 +570,24 @@ __device__ __forceinline__ void decode_body(const CUtensorMap& kv_map, const CUt
     // softmax has read S(t-1).  P·V is issued by its own warp, so a long
     // QK^T issue (the tensor pipe throttles it) never delays P·V, nor the
     // other way round; the two streams share only the tensor pipe.
-    if (lane == 0) {
-      TileCursor<Sees::kAll> cq;
-      cq.init(a.segs, s_begin, s_end);
-      // Stage-0 descriptors: latent chunks (K-major) and the RoPE half,
-      // advanced by adding the byte offset >> 4 to the start-address field
-      // (no carry: shared addresses stay below 2^18).
-      const uint64_t kdesc0 = sdesc_sw128(base + kOffKV, 16, 1024);
-      const uint64_t rdesc0 = sdesc_sw64(base + kOffKV + 4 * kChunkBytes, 16, 512);
-      for (uint32_t tq = 0; cq.valid(); ++tq) {
-        const uint32_t st = tq % kStages;
-        if (!wait_phase<false, kIssueSuspend>(BAR(B_KV_FULL + st), (tq / kStages) & 1u, err, abort_flag, a.wait_limit, a.wait_every)) break;
-        // FP8: the RoPE half came with the codes (already complete; waited for its TMA visibility)
-        if (kF8 && !wait_phase<false, kIssueSuspend>(BAR(B_F8_FULL + st), (tq / kStages) & 1u, err, abort_flag, a.wait_limit, a.wait_every))
-          break;
-        if (tq > 0 && !wait_phase<false, kIssueSuspend>(BAR(B_S_FREE), (tq - 1) & 1u, err, abort_flag, a.wait_limit, a.wait_every)) break;
-        if (cq.first() &&
-            !wait_phase<false, kIssueSuspend>(BAR(B_Q_READY), (uint32_t)(cq.s - s_begin) & 1u, err, abort_flag, a.wait_limit, a.wait_every))
-          break;
-        tc_fence_after();
+    TileCursor<Sees::kAll> cq;
+    cq.init(a.segs, s_begin, s_end);
+    // Stage-0 descriptors: latent chunks (K-major) and the RoPE half,
+    // advanced by adding the byte offset >> 4 to the start-address field
+    // (no carry: shared addresses stay below 2^18).
+    const uint64_t kdesc0 = sdesc_sw128(base + kOffKV, 16, 1024);
+    const uint64_t rdesc0 = sdesc_sw64(base + kOffKV + 4 * kChunkBytes, 16, 512);
+    for (uint32_t tq = 0; cq.valid(); ++tq) {
+      const uint32_t st = tq % kStages;
+      bool ok = wait_phase<false, kIssueSuspend>(BAR(B_KV_FULL + st), (tq / kStages) & 1u, err, abort_flag, a.wait_limit, a.wait_every);
+      // FP8: the RoPE half came with the codes (already complete; waited for its TMA visibility)
+      if (kF8) ok = ok && wait_phase<false, kIssueSuspend>(BAR(B_F8_FULL + st), (tq / kStages) & 1u, err, abort_flag, a.wait_limit, a.wait_every);
+      if (tq > 0) ok = ok && wait_phase<false, kIssueSuspend>(BAR(B_S_FREE), (tq - 1) & 1u, err, abort_flag, a.wait_limit, a.wait_every);
+      if (cq.first())
+        ok = ok && wait_phase<false, kIssueSuspend>(BAR(B_Q_READY), (uint32_t)(cq.s - s_begin) & 1u, err, abort_flag, a.wait_limit, a.wait_every);
+      if (!__all_sync(0xffffffffu, ok)) break;
+      tc_fence_after();
+      if (elect_one()) {
         // [128 x 64] += Q_r[128 x 288] · K_r^T, K-major, 16 per step: 4 latent
         // chunks (128-byte swizzle) then the RoPE half (64-byte swizzle).
         const uint64_t dk = kdesc0 + (uint64_t)((st * kStageBytes) >> 4);
@@ -604,12 +603,14 @@ __device__ __forceinline__ void decode_body(const CUtensorMap& kv_map, const CUt
           mma_ts(tmem + kColS, tmem + kColQ + 128 + kk * 8, dr + (uint64_t)((kk * 32) >> 4), kIdescQK, 1u);
         tc_commit(BAR(B_S_FULL0 + (tq & 1u)));
         if (kRowWarps && cq.last()) tc_commit(BAR(B_Q_FREE));
-        cq.next();
       }
-      // Every MMA of this thread must be finished before TMEM is released.
-      tc_commit(BAR(B_DRAIN));
-      wait_phase_drain(BAR(B_DRAIN), 0);
+      __syncwarp();
+      cq.next();
     }
+    // Every MMA of this warp must be finished before TMEM is released.
+    if (elect_one()) tc_commit(BAR(B_DRAIN));
+    __syncwarp();
+    wait_phase_drain(BAR(B_DRAIN), 0);
     __syncwarp();
   };
   // Zeroes the latents of tile t's tokens whose bit of `seen` is clear, by one
@@ -643,23 +644,26 @@ __device__ __forceinline__ void decode_body(const CUtensorMap& kv_map, const CUt
   };
   auto role_pv = [&]() {
     // ---------------------------------------------------------------- P·V issue
-    // Masked: the whole warp walks the tiles, lane 0 issues, and a tile's
-    // masked tokens have their latents cleared once QK^T has read the page,
-    // while the softmax is at work: their P is 0, but 0 times an infinity or a
-    // NaN is not 0.  (128 rows of 2112 tokens: 93.9 us, 92.9 without the
-    // clearing, 95.8 with the softmax warps clearing.)
-    if (kMasked || lane == 0) {
-      TileCursor<kSees> cp;
-      cp.init(a.segs, s_begin, s_end, win, tree);
-      // The latent chunks read MN-major for P·V, and the ones tile.
-      const uint64_t vdesc0 = sdesc_sw128(base + kOffKV, 8192, 1024);
-      const uint64_t odesc0 = sdesc_sw128(base + kOffOnes, 16, 1024);
-      auto issue = [&](uint32_t tp) -> bool {
-        const bool first = cp.first();
-        if (!wait_phase<false, kIssueSuspend>(BAR(B_P_FULL), tp & 1u, err, abort_flag, a.wait_limit, a.wait_every)) return false;
-        if (first && !wait_phase<false, kIssueSuspend>(BAR(B_O_FREE), (uint32_t)(cp.s - s_begin) & 1u, err, abort_flag, a.wait_limit, a.wait_every))
-          return false;
-        tc_fence_after();
+    // Masked: a tile's masked tokens have their latents cleared once QK^T has read
+    // the page, while the softmax is at work: their P is 0, but 0 times an
+    // infinity or a NaN is not 0.  (128 rows of 2112 tokens: 93.9 us, 92.9 without
+    // the clearing, 95.8 with the softmax warps clearing.)
+    TileCursor<kSees> cp;
+    cp.init(a.segs, s_begin, s_end, win, tree);
+    // The latent chunks read MN-major for P·V, and the ones tile.
+    const uint64_t vdesc0 = sdesc_sw128(base + kOffKV, 8192, 1024);
+    const uint64_t odesc0 = sdesc_sw128(base + kOffOnes, 16, 1024);
+    for (uint32_t tp = 0; cp.valid(); ++tp) {
+      if constexpr (kMasked) {
+        if (cp.edge() && !clear_masked(cp.visible(), tp)) break;
+      }
+      const bool first = cp.first();
+      bool ok = wait_phase<false, kIssueSuspend>(BAR(B_P_FULL), tp & 1u, err, abort_flag, a.wait_limit, a.wait_every);
+      if (first)
+        ok = ok && wait_phase<false, kIssueSuspend>(BAR(B_O_FREE), (uint32_t)(cp.s - s_begin) & 1u, err, abort_flag, a.wait_limit, a.wait_every);
+      if (!__all_sync(0xffffffffu, ok)) break;
+      tc_fence_after();
+      if (elect_one()) {
         // O_r[128 x 256] += P[128 x 64] · V_r[64 x 256]; V_r is MN-major: 4 atoms
         // of 64 columns 8 KB apart (LBO), 8-token row groups 1 KB apart (SBO).
         // l[128 x 16] += P · 1 (every column holds the row sum of P), issued
@@ -676,25 +680,13 @@ __device__ __forceinline__ void decode_body(const CUtensorMap& kv_map, const CUt
         tc_commit(BAR(B_KV_EMPTY + tp % kStages));
         tc_commit(BAR(B_O_DONE0 + (tp & 1u)));
         if (kRowWarps && cp.last()) tc_commit(BAR(B_ROW_DONE));
-        return true;
-      };
-      for (uint32_t tp = 0; cp.valid(); ++tp) {
-        bool ok = true;
-        if constexpr (kMasked) {
-          if (cp.edge() && !clear_masked(cp.visible(), tp)) break;
-          if (lane == 0) ok = issue(tp);
-          ok = __shfl_sync(0xffffffffu, (int)ok, 0) != 0;
-        } else {
-          ok = issue(tp);
-        }
-        if (!ok) break;
-        cp.next();
       }
-      if (lane == 0) {
-        tc_commit(BAR(B_DRAIN_PV));
-        wait_phase_drain(BAR(B_DRAIN_PV), 0);
-      }
+      __syncwarp();
+      cp.next();
     }
+    if (elect_one()) tc_commit(BAR(B_DRAIN_PV));
+    __syncwarp();
+    wait_phase_drain(BAR(B_DRAIN_PV), 0);
     __syncwarp();
   };
   auto role_convert = [&]() {

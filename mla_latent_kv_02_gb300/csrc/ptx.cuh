@@ -348,6 +348,17 @@ __device__ __forceinline__ void tc_commit(uint32_t bar) {
                : "memory");
 }
 // D(tmem) (+)= A(smem) * B(smem)
+// One lane of a converged warp, the same at every call.  An issuing role walks
+// its loop with the whole warp and branches on this around its MMAs: operands
+// that the compiler sees to be the same in every lane stay in uniform registers,
+// and an M = 128, N = 64 MMA is issued every 32 cycles, its own time.  Behind
+// `if (lane == 0)` each operand moves there anew: 47 to 60 cycles an MMA.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred P;\n\telect.sync _|P, 0xffffffff;\n\tselp.b32 %0, 1, 0, P;\n\t}" : "=r"(p));
+  return p != 0;
+}
+
 __device__ __forceinline__ void mma_ss(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
                                        uint32_t accumulate) {
   asm volatile(
