@@ -73,8 +73,23 @@ constexpr int kXBytes = kH * kPage * 2;                   // one CTA's fp16 part
 // Softmax: two warpgroups take alternate tiles whole (thread = head row).
 constexpr int kSWarps = 8;
 constexpr int kWords = kPage / 2;                         // fp16x2 words of a row's 64 scores
-constexpr int kXRow = kPage * 2;                          // one row of a partial S tile (128 bytes)
-constexpr int kXWarp = 32 * kXRow;                        // one warp's 32 rows (4 KB)
+constexpr int kXWarp = kXBytes / 4;                       // a warp's share of an exchange buffer (4 KB)
+// The scores of a tile cross in parts, each with a barrier of its own.  In two,
+// 32 tokens each, the second part's way (an SM sends about 20 bytes a cycle) is
+// under the first part's arithmetic: 64 unpacked rows of 32 832 tokens 392 -> 369
+// us, 768 rows of 8 204 tokens 1 259 -> 1 229.  Over the FP8 cache, where the
+// converters bind and leave fewer registers, one part is faster (320 and 344 us on
+// 128 rows of 8 194 tokens).
+template <int kParts>
+struct Exchange {
+  static constexpr int kBytes = kXBytes / kParts;         // [128 heads x 64 / kParts tokens] fp16
+  static constexpr int kRow = kPage * 2 / kParts;         // a row's scores
+  static constexpr int kWarp = 32 * kRow;                 // one warp's 32 rows
+  static constexpr int kPieces = kRow / 16;               // 16-byte pieces of a row, swizzled
+  static constexpr int kWords2 = kWords / kParts;         // fp16x2 words of a row
+  static __device__ __forceinline__ uint32_t swizzle(int h) { return kParts == 1 ? (uint32_t)(h & 7) : (uint32_t)((h >> 1) & 3); }
+  static_assert(kParts == 1 || kParts == 2, "the swizzles above");
+};
 constexpr int kXBufs = 4;                                 // exchange ring depth
 constexpr int kXLead = kXBufs - 2;                        // staging buffer offset
 static_assert(kXLead >= 1 && kXLead <= kXBufs - 2, "the exchange ring needs two tiles between staging and reuse");
@@ -104,10 +119,10 @@ constexpr int kSmallMisc = kSmallPair + 4 * kH * 8;
 // misc: +0 abort flag, +8 TMEM address, +16 segment range [2], +32 copies
 // issued per softmax warp [8], +64 the peer's copies [8] (written by the
 // peer), +96 the abort flags of this CTA and the peer [2], +104 the last tile
-// armed on each exchange buffer [4], +120 the last tile whose scores each
-// softmax warpgroup has seen complete [2] (windowed).
-constexpr int kMiscPush = 32, kMiscPeerPush = 64, kMiscAborts = 96, kMiscArmed = 104, kMiscScored = 120;
-constexpr int kSmallBytes = kSmallMisc + 128;
+// whose scores each softmax warpgroup has seen complete [2] (masked), +112 the
+// last tile armed on each part of each exchange buffer [2][4].
+constexpr int kMiscPush = 32, kMiscPeerPush = 64, kMiscAborts = 96, kMiscScored = 104, kMiscArmed = 112;
+constexpr int kSmallBytes = kSmallMisc + 144;
 
 // The two cache formats.  bf16: the producer's TMA fills a 4-deep ring of
 // [latent half | RoPE half] stages.  FP8: the TMA fills the same 4-deep ring
@@ -169,8 +184,8 @@ struct Layout : Cfg<kF8, kRows> {
     B_O_DONE1,
     B_Q_READY,
     B_O_FREE,
-    B_X_FULL0,                      // exchange buffer i filled by the peer
-    B_DRAIN = B_X_FULL0 + kXBufs,
+    B_X_FULL0,                      // exchange buffer i's first part filled by the peer; + kXBufs: its second
+    B_DRAIN = B_X_FULL0 + 2 * kXBufs,
     B_DRAIN_PV,
     B_Q_FREE,                       // row warps: a segment's last QK^T has read the queries
     B_ROW_DONE,                     // row warps: a segment's last P·V is complete
@@ -183,7 +198,7 @@ struct Layout : Cfg<kF8, kRows> {
 constexpr uint32_t kColO = 0, kColS = 256, kColSum = 320, kColQ = 336, kColP = 480, kTmemCols = 512;
 // The producer and the two MMA-issuing threads poll (mbarrier.test_wait)
 // rather than sleep: their wake-up sits on the score chain.
-constexpr bool kIssueSuspend = false;
+constexpr bool kIssueSuspend = true;
 constexpr uint32_t kTileThreads = 128;                    // the warpgroup that handles one tile
 
 // bf16 operands for the bf16 cache; f16 for the FP8 cache (an E4M3 value is
@@ -287,9 +302,9 @@ struct TileCursor {
   }
 };
 
-template <bool kValue>
-struct Flag {
-  static constexpr bool value = kValue;
+template <int kValue>
+struct Part {
+  static constexpr int value = kValue;
 };
 
 __device__ __forceinline__ __half2 as_h2(uint32_t u) { return *reinterpret_cast<const __half2*>(&u); }
@@ -337,6 +352,8 @@ __device__ __forceinline__ void decode_body(const CUtensorMap& kv_map, const CUt
   constexpr bool kWin = kSees == Sees::kWindow, kTree = kSees == Sees::kTree, kMasked = kWin || kTree;
   constexpr bool kUnpacked = kF16 && !kF8;
   constexpr bool kRowWarps = kTree && !kF8;
+  constexpr int kParts = kF8 ? 1 : 2;
+  using X = Exchange<kParts>;
   using L = Layout<kF8, kRowWarps>;
   constexpr int kStages = L::kStages, kStageBytes = L::kStageBytes, kThreads = L::kThreads;
   constexpr int kPvWarp = L::kPvWarp, kSoftWarp0 = L::kSoftWarp0, kConvWarp0 = L::kConvWarp0;
@@ -389,7 +406,7 @@ __device__ __forceinline__ void decode_body(const CUtensorMap& kv_map, const CUt
       mbar_init(BAR(B_Q_FREE), 1);
       mbar_init(BAR(B_ROW_DONE), 1);
     }
-    for (int i = 0; i < kXBufs; ++i) {
+    for (int i = 0; i < kParts * kXBufs; ++i) {
       mbar_init(BAR(B_X_FULL0 + i), 1);
       armed[i] = -1;
     }
@@ -475,52 +492,54 @@ __device__ __forceinline__ void decode_body(const CUtensorMap& kv_map, const CUt
   // register budget at the top of a branch that reaches only its own roles.
   auto role_producer = [&]() {
     // ---------------------------------------------------------------- producer
-    if (lane == 0) {
-      uint32_t g = 0;
-      bool ok = true;
-      if (kRowWarps && s_begin < s_end) {  // the first row's queries: their later rounds find them in L2
-        const size_t qrow = (size_t)a.segs[8 * s_begin];
-        prefetch_l2_bulk(reinterpret_cast<const uint8_t*>(a.q_abs) + qrow * (kH * kDC * 2) + rank * (kH * kDC), kH * kDC);
-      }
-      for (int s = s_begin; s < s_end && ok; ++s) {
-        const int32_t* sg = a.segs + 8 * s;
-        const int b = sg[1], pb = sg[2], pe = sg[3];
-        const int32_t* bt = a.block_table + (int64_t)b * a.max_pages;
-        WindowTiles wt = {0, 0, 0, 0};
-        if (kWin) wt = window_tiles(sg[6], win->sinks);
-        for (int pg = pb; pg < pe; ++pg) {
-          const uint32_t st = g % kStages, use = g / kStages;
-          int32_t pid;  // in flight while the stage drains
-          if constexpr (kUnpacked) pid = sg[7] + pg;
-          else pid = __ldg(bt + (kWin && pg >= wt.sink_tiles ? pg + wt.skip : pg));
-          const bool merged = kWin && wt.merged && pg == wt.sink_tiles;
-          int32_t spid = merged ? __ldg(bt + win->sinks / kPage) : 0;  // the sinks' page
-          if (pg == pe - 1 && s + 1 < s_end) {
-            // The next segment's query row is read right after this segment's
-            // last QK^T: warm L2 with it (each CTA one half of q_abs[row],
-            // CTA 0 also q_r[row]) so that load is not a DRAM round trip.
-            const size_t qrow = (size_t)a.segs[8 * (s + 1)];
-            const uint8_t* qa = reinterpret_cast<const uint8_t*>(a.q_abs) + qrow * (kH * kDC * 2);
-            prefetch_l2_bulk(qa + rank * (kH * kDC), kH * kDC);
-            if (rank == 0) prefetch_l2_bulk(reinterpret_cast<const uint8_t*>(a.q_r) + qrow * (kH * kDR * 2), kH * kDR * 2);
-          }
-          if (use > 0 && !wait_phase<false, kIssueSuspend>(BAR(B_KV_EMPTY + st), (use - 1) & 1u, err, abort_flag, a.wait_limit, a.wait_every)) {
-            ok = false;
-            break;
-          }
-          if (pid < 0 || (int64_t)pid >= a.num_pages) {
-            atomicOr(err, (int32_t)MLA_DEVERR_PAGE_OOB);
-            pid = 0;
-          }
-          const uint32_t dst = base + kOffKV + st * kStageBytes;
+    uint32_t g = 0;
+    bool ok = true;
+    if (kRowWarps && s_begin < s_end && elect_one()) {  // the first row's queries: their later rounds find them in L2
+      const size_t qrow = (size_t)a.segs[8 * s_begin];
+      prefetch_l2_bulk(reinterpret_cast<const uint8_t*>(a.q_abs) + qrow * (kH * kDC * 2) + rank * (kH * kDC), kH * kDC);
+    }
+    for (int s = s_begin; s < s_end && ok; ++s) {
+      const int32_t* sg = a.segs + 8 * s;
+      const int b = sg[1], pb = sg[2], pe = sg[3];
+      const int32_t* bt = a.block_table + (int64_t)b * a.max_pages;
+      WindowTiles wt = {0, 0, 0, 0};
+      if (kWin) wt = window_tiles(sg[6], win->sinks);
+      for (int pg = pb; pg < pe; ++pg) {
+        const uint32_t st = g % kStages, use = g / kStages;
+        int32_t pid;  // in flight while the stage drains
+        if constexpr (kUnpacked) pid = sg[7] + pg;
+        else pid = __ldg(bt + (kWin && pg >= wt.sink_tiles ? pg + wt.skip : pg));
+        const bool merged = kWin && wt.merged && pg == wt.sink_tiles;
+        int32_t spid = merged ? __ldg(bt + win->sinks / kPage) : 0;  // the sinks' page
+        if (pg == pe - 1 && s + 1 < s_end && elect_one()) {
+          // The next segment's query row is read right after this segment's
+          // last QK^T: warm L2 with it (each CTA one half of q_abs[row],
+          // CTA 0 also q_r[row]) so that load is not a DRAM round trip.
+          const size_t qrow = (size_t)a.segs[8 * (s + 1)];
+          const uint8_t* qa = reinterpret_cast<const uint8_t*>(a.q_abs) + qrow * (kH * kDC * 2);
+          prefetch_l2_bulk(qa + rank * (kH * kDC), kH * kDC);
+          if (rank == 0) prefetch_l2_bulk(reinterpret_cast<const uint8_t*>(a.q_r) + qrow * (kH * kDR * 2), kH * kDR * 2);
+        }
+        __syncwarp();
+        if (use > 0) {
+          ok = wait_phase<false, kIssueSuspend>(BAR(B_KV_EMPTY + st), (use - 1) & 1u, err, abort_flag, a.wait_limit, a.wait_every);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+        }
+        if (pid < 0 || (int64_t)pid >= a.num_pages) {
+          atomicOr(err, (int32_t)MLA_DEVERR_PAGE_OOB);
+          pid = 0;
+        }
+        const uint32_t dst = base + kOffKV + st * kStageBytes;
+        if (merged && (spid < 0 || (int64_t)spid >= a.num_pages)) {
+          atomicOr(err, (int32_t)MLA_DEVERR_PAGE_OOB);
+          spid = 0;
+        }
+        if (elect_one()) {
           if (merged) {
             // tokens [0, split) of the sinks' page and [split, 64) of the
             // window's first page, at their places in the tile; split is a
             // multiple of eight, so every box starts on a swizzle atom
-            if (spid < 0 || (int64_t)spid >= a.num_pages) {
-              atomicOr(err, (int32_t)MLA_DEVERR_PAGE_OOB);
-              spid = 0;
-            }
             const int n0 = win->split, y0 = spid * kPage, y1 = pid * kPage + n0;
             if constexpr (kF8) {
               const uint32_t bar = BAR(B_F8_FULL + st);
@@ -555,13 +574,14 @@ __device__ __forceinline__ void decode_body(const CUtensorMap& kv_map, const CUt
             tma_load_2d(dst + 4 * kChunkBytes, &rope_map, kDC + (int)rank * kRopeHalf, pid * kPage,
                         BAR(B_KV_FULL + st));
           }
-          ++g;
         }
+        __syncwarp();
+        ++g;
       }
-      // Loads still in flight must land before this CTA may exit.
-      for (uint32_t k = (g > (uint32_t)kStages ? g - kStages : 0u); k < g; ++k)
-        wait_phase_drain(BAR((kF8 ? B_F8_FULL : B_KV_FULL) + k % kStages), (k / kStages) & 1u);
     }
+    // Loads still in flight must land before this CTA may exit.
+    for (uint32_t k = (g > (uint32_t)kStages ? g - kStages : 0u); k < g; ++k)
+      wait_phase_drain(BAR((kF8 ? B_F8_FULL : B_KV_FULL) + k % kStages), (k / kStages) & 1u);
     __syncwarp();
   };
   auto role_qk = [&]() {
@@ -812,8 +832,9 @@ __device__ __forceinline__ void decode_body(const CUtensorMap& kv_map, const CUt
     const int q4 = warp & 3;                 // TMEM lane quarter this warp may access
     const int h = q4 * 32 + lane;            // head row = TMEM lane
     const uint32_t tl = tmem + ((uint32_t)(q4 * 32) << 16);
-    const uint32_t swz = (uint32_t)(h & 7);  // 128-byte rows: 16-byte chunk k sits at k ^ (h & 7)
-    const uint32_t row_off = (uint32_t)(h * kXRow);
+    const uint32_t swz = X::swizzle(h);  // 16-byte piece k of a row sits at k ^ swz
+    const uint32_t row_off = (uint32_t)(h * X::kRow);
+    const uint32_t part_off = (uint32_t)(q4 * X::kWarp);
     const uint32_t warp_off = (uint32_t)(q4 * kXWarp);
     const bool wg_leader = ((sw & 3) == 0 && lane == 0);
     // Scores cross the pair and are compared unscaled; the scale (times
@@ -886,16 +907,6 @@ __device__ __forceinline__ void decode_body(const CUtensorMap& kv_map, const CUt
       if (!__all_sync(0xffffffffu, w)) return false;
       if (kMasked && wg_leader) scored[wg] = (int32_t)t;
       tc_fence_after();
-      {
-        uint32_t r[64];
-        tmem_ld64_sync(tl + kColS, r);
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(BAR(B_S_FREE));
-#pragma unroll
-        for (int j = 0; j < kWords; ++j)
-          own[j] = cvt_f16x2_satfinite(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1]));
-      }
       // Stage in own buffer (t + kXLead) mod kXBufs and push into the peer's
       // buffer t mod kXBufs.  Both need the peer's tile t - kXLead to have
       // landed here; this warpgroup already waited for exactly that (with
@@ -903,21 +914,33 @@ __device__ __forceinline__ void decode_body(const CUtensorMap& kv_map, const CUt
       // but one, so no wait is needed here.
       static_assert(kXLead == 2, "tile t - kXLead must be this warpgroup's, already finished");
       const uint32_t stage = base + kOffX + ((t + kXLead) % kXBufs) * kXBytes;
-#pragma unroll
-      for (int k = 0; k < 8; ++k)
-        st_shared_v4(stage + row_off + (((uint32_t)k ^ swz) << 4), own[4 * k], own[4 * k + 1], own[4 * k + 2],
-                     own[4 * k + 3]);
-      fence_proxy_async_smem();
+      uint32_t r[64];
+      tmem_ld64_sync(tl + kColS, r);
+      tc_fence_before();
       __syncwarp();
-      if (!peer_ready) {
-        cluster_wait();
-        peer_ready = true;
+      if (lane == 0) mbar_arrive(BAR(B_S_FREE));
+#pragma unroll
+      for (int p = 0; p < kParts; ++p) {
+#pragma unroll
+        for (int j = p * X::kWords2; j < (p + 1) * X::kWords2; ++j)
+          own[j] = cvt_f16x2_satfinite(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1]));
+#pragma unroll
+        for (int k = 0; k < X::kPieces; ++k) {
+          const int j = p * X::kWords2 + 4 * k;
+          st_shared_v4(stage + p * X::kBytes + row_off + (((uint32_t)k ^ swz) << 4), own[j], own[j + 1], own[j + 2], own[j + 3]);
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (!peer_ready) {
+          cluster_wait();
+          peer_ready = true;
+        }
+        if (lane == 0)
+          bulk_copy_to_peer(mapa(base + kOffX + (t % kXBufs) * kXBytes + p * X::kBytes + part_off, peer),
+                            stage + p * X::kBytes + part_off, (uint32_t)X::kWarp,
+                            mapa(BAR(B_X_FULL0 + p * kXBufs + t % kXBufs), peer));
       }
-      if (lane == 0) {
-        bulk_copy_to_peer(mapa(base + kOffX + (t % kXBufs) * kXBytes + warp_off, peer), stage + warp_off,
-                          (uint32_t)kXWarp, mapa(BAR(B_X_FULL0 + t % kXBufs), peer));
-        push_cnt[sw] += 1u;  // copies this warp issued into the peer
-      }
+      if (lane == 0) push_cnt[sw] += 1u;  // tiles this warp sent to the peer, every part
       if (!kRowWarps && c.last() && c.s + 1 < c.s_end) load_q(c.s + 1);
       return true;
     };
@@ -928,10 +951,11 @@ __device__ __forceinline__ void decode_body(const CUtensorMap& kv_map, const CUt
 
     if (!kRowWarps && wg == 0) mbar_arrive(BAR(B_O_FREE));  // O is free for the first segment
     if (sw == 0 && lane == 0)                  // arm the ring: the first kXBufs tiles each expect one peer push
-      for (uint32_t t = 0; t < G && t < (uint32_t)kXBufs; ++t) {
-        mbar_arrive_expect_tx(BAR(B_X_FULL0 + t), (uint32_t)kXBytes);
-        armed[t] = (int32_t)t;
-      }
+      for (uint32_t t = 0; t < G && t < (uint32_t)kXBufs; ++t)
+        for (uint32_t p = 0; p < (uint32_t)kParts; ++p) {
+          mbar_arrive_expect_tx(BAR(B_X_FULL0 + p * kXBufs + t), (uint32_t)X::kBytes);
+          armed[p * kXBufs + t] = (int32_t)t;
+        }
     TileCursor<kSees> cf;  // this warpgroup's tile
     cf.init(a.segs, s_begin, s_end, win, tree);
     if (wg == 1 && cf.valid()) cf.next();
@@ -943,53 +967,61 @@ __device__ __forceinline__ void decode_body(const CUtensorMap& kv_map, const CUt
         ok = false;
         break;
       }
-      // ---- add the peer's half (fp16, unscaled)
+      // ---- add what the peer sent (fp16, unscaled), part by part; mask it (causal,
+      //      length, window, tree) and take the row max
       const uint32_t xb = g % kXBufs;
-      bool w = wait_phase<true, true>(BAR(B_X_FULL0 + xb), (g / kXBufs) & 1u, err, abort_flag, a.wait_limit, a.wait_every);
-      if (!__all_sync(0xffffffffu, w)) {
-        ok = false;
-        break;
-      }
-      // Re-arm this buffer's barrier for tile g + kXBufs (this warpgroup's
-      // again).  That push cannot land before this warpgroup has pushed tile
-      // g + kXBufs - kXLead, which it does only after finishing tile g.
-      if (wg_leader && g + kXBufs < G) {
-        mbar_arrive_expect_tx(BAR(B_X_FULL0 + xb), (uint32_t)kXBytes);
-        armed[xb] = (int32_t)(g + kXBufs);
-      }
       const uint32_t recv = base + kOffX + xb * kXBytes + row_off;
-#pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        const float4 v = ld_shared_v4(recv + (((uint32_t)k ^ swz) << 4));
-        own[4 * k] = as_u32(__hadd2(as_h2(own[4 * k]), as_h2(__float_as_uint(v.x))));
-        own[4 * k + 1] = as_u32(__hadd2(as_h2(own[4 * k + 1]), as_h2(__float_as_uint(v.y))));
-        own[4 * k + 2] = as_u32(__hadd2(as_h2(own[4 * k + 2]), as_h2(__float_as_uint(v.z))));
-        own[4 * k + 3] = as_u32(__hadd2(as_h2(own[4 * k + 3]), as_h2(__float_as_uint(v.w))));
-      }
-
-      // ---- causal/length mask and the row max of this tile
+      uint64_t seen = ~0ull;
       if constexpr (kMasked) {
-        if (cf.edge()) {
-          const uint64_t seen = cf.visible();
+        if (cf.edge()) seen = cf.visible();
+      } else if (const int valid = cf.vis - cf.pg * kPage; valid < kPage) {
+        seen = TileCursor<kSees>::bits_below(valid);
+      }
+      __half2 mh = __float2half2_rn(-INFINITY);
+      auto join = [&](auto part) -> bool {
+        constexpr int kP = decltype(part)::value, kJ = kP * X::kWords2;
+        const uint32_t bar = BAR(B_X_FULL0 + kP * kXBufs + xb);
+        const bool w = wait_phase<true, true>(bar, (g / kXBufs) & 1u, err, abort_flag, a.wait_limit, a.wait_every);
+        if (!__all_sync(0xffffffffu, w)) return false;
+        // Re-arm this part's barrier for tile g + kXBufs (this warpgroup's
+        // again).  That push cannot land before this warpgroup has pushed tile
+        // g + kXBufs - kXLead, which it does only after finishing tile g.
+        if (wg_leader && g + kXBufs < G) {
+          mbar_arrive_expect_tx(bar, (uint32_t)X::kBytes);
+          armed[kP * kXBufs + xb] = (int32_t)(g + kXBufs);
+        }
 #pragma unroll
-          for (int j = 0; j < kWords; ++j) {
-            if (!((seen >> (2 * j)) & 1u)) own[j] = (own[j] & 0xFFFF0000u) | 0xFC00u;
-            if (!((seen >> (2 * j + 1)) & 1u)) own[j] = (own[j] & 0x0000FFFFu) | 0xFC000000u;
+        for (int k = 0; k < X::kPieces; ++k) {
+          const float4 v = ld_shared_v4(recv + kP * X::kBytes + (((uint32_t)k ^ swz) << 4));
+          own[kJ + 4 * k] = as_u32(__hadd2(as_h2(own[kJ + 4 * k]), as_h2(__float_as_uint(v.x))));
+          own[kJ + 4 * k + 1] = as_u32(__hadd2(as_h2(own[kJ + 4 * k + 1]), as_h2(__float_as_uint(v.y))));
+          own[kJ + 4 * k + 2] = as_u32(__hadd2(as_h2(own[kJ + 4 * k + 2]), as_h2(__float_as_uint(v.z))));
+          own[kJ + 4 * k + 3] = as_u32(__hadd2(as_h2(own[kJ + 4 * k + 3]), as_h2(__float_as_uint(v.w))));
+        }
+        if (seen != ~0ull) {
+          const uint64_t bits = seen >> (2 * kJ);
+#pragma unroll
+          for (int j = 0; j < X::kWords2; ++j) {
+            if (!((bits >> (2 * j)) & 1u)) own[kJ + j] = (own[kJ + j] & 0xFFFF0000u) | 0xFC00u;          // low half -> -inf
+            if (!((bits >> (2 * j + 1)) & 1u)) own[kJ + j] = (own[kJ + j] & 0x0000FFFFu) | 0xFC000000u;  // high half -> -inf
           }
         }
-      } else if (const int valid = cf.vis - cf.pg * kPage; valid < kPage) {
+        __half2 m4[X::kPieces];
 #pragma unroll
-        for (int j = 0; j < kWords; ++j) {
-          if (2 * j >= valid) own[j] = (own[j] & 0xFFFF0000u) | 0xFC00u;          // low half -> -inf
-          if (2 * j + 1 >= valid) own[j] = (own[j] & 0x0000FFFFu) | 0xFC000000u;  // high half -> -inf
-        }
-      }
-      __half2 mx[8];
+        for (int j = 0; j < X::kPieces; ++j)
+          m4[j] = __hmax2(__hmax2(as_h2(own[kJ + 4 * j]), as_h2(own[kJ + 4 * j + 1])),
+                          __hmax2(as_h2(own[kJ + 4 * j + 2]), as_h2(own[kJ + 4 * j + 3])));
 #pragma unroll
-      for (int j = 0; j < 8; ++j)
-        mx[j] = __hmax2(__hmax2(as_h2(own[4 * j]), as_h2(own[4 * j + 1])), __hmax2(as_h2(own[4 * j + 2]), as_h2(own[4 * j + 3])));
-      const __half2 mh = __hmax2(__hmax2(__hmax2(mx[0], mx[1]), __hmax2(mx[2], mx[3])),
-                                 __hmax2(__hmax2(mx[4], mx[5]), __hmax2(mx[6], mx[7])));
+        for (int n = X::kPieces / 2; n > 0; n /= 2)
+#pragma unroll
+          for (int j = 0; j < n; ++j) m4[j] = __hmax2(m4[j], m4[j + n]);
+        mh = __hmax2(mh, m4[0]);
+        return true;
+      };
+      ok = join(Part<0>{});
+      if constexpr (kParts == 2) ok = ok && join(Part<1>{});
+      if (!ok) break;
+      bool w;
       const float mt = fmaxf(__low2float(mh), __high2float(mh));
 
       // ---- reference max: tile g-1's (the other warpgroup's) unless this tile starts a segment
@@ -1347,12 +1379,12 @@ __device__ __forceinline__ void decode_body(const CUtensorMap& kv_map, const CUt
   }
   cluster_sync();  // neither CTA leaves while its peer may still address its shared memory
   if (aborts[0] != 0 || aborts[1] != 0) {
-    // Drain: each exchange buffer has at most one armed phase this CTA did not
-    // see complete.  The peer's counts say how many of that tile's four
+    // Drain: each part of an exchange buffer has at most one armed phase this CTA
+    // did not see complete.  The peer's counts say how many of that tile's four
     // per-warp copies it issued; the bytes of the copies never issued are
     // retired by hand, and the phase then completes once the issued ones land.
     if (threadIdx.x == 0) {
-      for (int b = 0; b < kXBufs; ++b) {
+      for (int b = 0; b < kParts * kXBufs; ++b) {
         const int32_t t = armed[b];
         if (t < 0) continue;
         const uint32_t par = ((uint32_t)t / kXBufs) & 1u;
@@ -1360,7 +1392,7 @@ __device__ __forceinline__ void decode_body(const CUtensorMap& kv_map, const CUt
         const uint32_t idx = (uint32_t)t >> 1, pg = (uint32_t)t & 1u;
         uint32_t issued = 0;
         for (int q = 0; q < 4; ++q) issued += peer_push[pg * 4 + q] > idx ? 1u : 0u;
-        if (issued < 4) mbar_complete_tx(BAR(B_X_FULL0 + b), (4u - issued) * (uint32_t)kXWarp);
+        if (issued < 4) mbar_complete_tx(BAR(B_X_FULL0 + b), (4u - issued) * (uint32_t)X::kWarp);
         const uint64_t t0 = cycles();
         while (!mbar_test_wait_cluster(BAR(B_X_FULL0 + b), par) && cycles() - t0 < kWaitLimitCycles) {
         }
