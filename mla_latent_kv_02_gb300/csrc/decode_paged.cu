@@ -843,6 +843,7 @@ __device__ __forceinline__ void decode_body(const CUtensorMap& kv_map, const CUt
     const float rescale_thr = 8.f / c2;  // lazy-rescale threshold: 8 in log2 units
     const __half2 c2h = __float2half2_rn(c2);
     __syncwarp();
+    const uint32_t peer_x = mapa(base + kOffX, peer), peer_bar = mapa(BAR(B_X_FULL0), peer);
     bool peer_ready = false;  // this warp has waited for the cluster barrier of the set-up
 
     // Q_r of a segment's row into TMEM, this warp's 32 head rows (144 columns
@@ -935,10 +936,10 @@ __device__ __forceinline__ void decode_body(const CUtensorMap& kv_map, const CUt
           cluster_wait();
           peer_ready = true;
         }
-        if (lane == 0)
-          bulk_copy_to_peer(mapa(base + kOffX + (t % kXBufs) * kXBytes + p * X::kBytes + part_off, peer),
+        if (elect_one())
+          bulk_copy_to_peer(peer_x + (t % kXBufs) * kXBytes + p * X::kBytes + part_off,
                             stage + p * X::kBytes + part_off, (uint32_t)X::kWarp,
-                            mapa(BAR(B_X_FULL0 + p * kXBufs + t % kXBufs), peer));
+                            peer_bar + 8u * (p * kXBufs + t % kXBufs));
       }
       if (lane == 0) push_cnt[sw] += 1u;  // tiles this warp sent to the peer, every part
       if (!kRowWarps && c.last() && c.s + 1 < c.s_end) load_q(c.s + 1);
@@ -1018,23 +1019,26 @@ __device__ __forceinline__ void decode_body(const CUtensorMap& kv_map, const CUt
         mh = __hmax2(mh, m4[0]);
         return true;
       };
+      // Asked for ahead of the scores: the previous tile's reference max and
+      // whether its P·V is complete.
+      const uint32_t gp = g - 1;  // the previous tile (the other warpgroup's)
+      const uint32_t gslot = pair + 8u * ((gp & 3u) * kH + h);
       ok = join(Part<0>{});
+      uint2 pv = ld_shared_v2_volatile(gslot);
       if constexpr (kParts == 2) ok = ok && join(Part<1>{});
       if (!ok) break;
       bool w;
       const float mt = fmaxf(__low2float(mh), __high2float(mh));
 
       // ---- reference max: tile g-1's (the other warpgroup's) unless this tile starts a segment
-      const uint32_t gp = g - 1;  // the previous tile (the other warpgroup's)
       const bool od_ready = (g == 0) || mbar_test_wait(BAR(B_O_DONE0 + (gp & 1u)), (gp >> 1) & 1u);
       float m = mt, factor = 1.f;
       bool resc = false;
       if (!cf.first()) {
-        const uint32_t slot = pair + 8u * (((g - 1) & 3u) * kH + h);
-        uint2 v = ld_shared_v2_volatile(slot);
+        uint2 v = pv;
         if (v.y != g - 1) {
           const uint64_t t0 = cycles();
-          for (uint32_t it = 1; (v = ld_shared_v2_volatile(slot)).y != g - 1; ++it) {
+          for (uint32_t it = 1; (v = ld_shared_v2_volatile(gslot)).y != g - 1; ++it) {
             if ((it & a.wait_every) == 0u && (*abort_flag || cycles() - t0 > a.wait_limit)) {
               if (!*abort_flag) atomicOr(err, (int32_t)MLA_DEVERR_TIMEOUT);
               *abort_flag = 1;
@@ -1203,7 +1207,7 @@ __device__ __forceinline__ void decode_body(const CUtensorMap& kv_map, const CUt
       const size_t row0 = (size_t)a.segs[8 * s] * kH + q4 * 32 + wr;
       const uint4* lat = reinterpret_cast<const uint4*>(a.q_abs + row0 * kDC + rank * 256) + wk;
       const uint4* rp = reinterpret_cast<const uint4*>(a.q_r + row0 * kDR + rank * kRopeHalf) + wk;
-      constexpr int kAhead = 3;  // rounds of 64 bytes a row in flight: eight latent, one RoPE
+      constexpr int kAhead = 4;  // rounds of 64 bytes a row in flight: eight latent, one RoPE
       uint4 v[kAhead][4];
       auto fetch = [&](int k) {
 #pragma unroll
