@@ -599,12 +599,11 @@ __device__ __forceinline__ void decode_body(const CUtensorMap& kv_map, const CUt
     const uint64_t rdesc0 = sdesc_sw64(base + kOffKV + 4 * kChunkBytes, 16, 512);
     for (uint32_t tq = 0; cq.valid(); ++tq) {
       const uint32_t st = tq % kStages;
-      bool ok = wait_phase<false, kIssueSuspend>(BAR(B_KV_FULL + st), (tq / kStages) & 1u, err, abort_flag, a.wait_limit, a.wait_every);
-      // FP8: the RoPE half came with the codes (already complete; waited for its TMA visibility)
-      if (kF8) ok = ok && wait_phase<false, kIssueSuspend>(BAR(B_F8_FULL + st), (tq / kStages) & 1u, err, abort_flag, a.wait_limit, a.wait_every);
+      bool ok = true;
+      if (cq.first()) ok = wait_phase<false, kIssueSuspend>(BAR(B_Q_READY), (uint32_t)(cq.s - s_begin) & 1u, err, abort_flag, a.wait_limit, a.wait_every);
       if (tq > 0) ok = ok && wait_phase<false, kIssueSuspend>(BAR(B_S_FREE), (tq - 1) & 1u, err, abort_flag, a.wait_limit, a.wait_every);
-      if (cq.first())
-        ok = ok && wait_phase<false, kIssueSuspend>(BAR(B_Q_READY), (uint32_t)(cq.s - s_begin) & 1u, err, abort_flag, a.wait_limit, a.wait_every);
+      ok = ok && wait_phase<false, kIssueSuspend>(BAR(B_KV_FULL + st), (tq / kStages) & 1u, err, abort_flag, a.wait_limit, a.wait_every);
+      if (kF8) ok = ok && wait_phase<false, kIssueSuspend>(BAR(B_F8_FULL + st), (tq / kStages) & 1u, err, abort_flag, a.wait_limit, a.wait_every);
       if (!__all_sync(0xffffffffu, ok)) break;
       tc_fence_after();
       if (elect_one()) {

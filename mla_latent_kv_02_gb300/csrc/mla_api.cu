@@ -118,10 +118,12 @@ struct PlanKind {
 // 128 KB a CTA, while the next piece's first tile is under way (254 rows over
 // 1 024 to 4 096 tokens: 205 us without it, 195 with four, 198 with eight).
 constexpr int64_t kTreeRowTiles = 4;
-// A partial result, 256 KB written, read and merged, in 64ths of a tile (8 rows
-// over 1 024 tokens: 20.7 us in 32 pieces, 24.9 in 68; one row over 8 192: 24.7
-// in 32 pieces, 28.8 in 64).
-constexpr int64_t kTreePartial = 10;
+// In 64ths of a tile: a partial result, 256 KB written, read and merged; and a
+// round of the merge, whose number is that of the pieces of the row with most
+// (one row over 8 192 tokens: 25.5 us in 64 pieces, 20.8 in 32, 19.1 in 26, 21.0 in 16; four
+// rows over 4 096: 22.6 in 16 pieces each, 19.1 in 11, 20.5 in 8; 32 rows over
+// 1 024: 21.6 in two, 22.6 whole).
+constexpr int64_t kTreePartial = 5, kTreePiece = 16;
 // The share of the L2 cache (129 MB) that a plan counts on for the sequences
 // being read at one time.
 constexpr int64_t kTreeSharedBytes = 64ll << 20;
@@ -262,10 +264,16 @@ mla_status build_plan(const int32_t* seq_lens, const int32_t* q_lens, int32_t B,
     int64_t best_ranges = 0, best_budget = 0, best_cost = INT64_MAX;
     const bool few = (int64_t)rows.size() < 2 * (int64_t)num_clusters;
     for (int64_t ranges = num_clusters; total > 0 && ranges >= 1; ranges = few ? std::min(ranges - 1, ranges * 7 / 8) : 0) {
-      int64_t budget = (total + kTreeRowTiles * std::max<int64_t>(T, ranges) + ranges - 1) / ranges, pieces;
-      while (pieces = 0, !fill(order, ranges, budget, [] {}, [&](int32_t, int64_t, int64_t) { ++pieces; })) budget += 1 + budget / 1024;
-      const int64_t partials = pieces > T ? std::min(pieces, 2 * (pieces - T)) : 0;
-      const int64_t cost = 64 * budget + kTreePartial * partials;
+      int64_t budget = (total + kTreeRowTiles * std::max<int64_t>(T, ranges) + ranges - 1) / ranges, partials, most, run;
+      int32_t of = -1;
+      auto count = [&](int32_t rr, int64_t, int64_t) {
+        run = rr == of ? run + 1 : 1;
+        of = rr;
+        partials += run == 1 ? 0 : run == 2 ? 2 : 1;
+        most = std::max(most, run);
+      };
+      while (partials = most = run = 0, of = -1, !fill(order, ranges, budget, [] {}, count)) budget += 1 + budget / 1024;
+      const int64_t cost = 64 * budget + kTreePartial * partials + (most > 1 ? kTreePiece * most : 0);
       if (cost < best_cost) {
         best_cost = cost;
         best_ranges = ranges;
