@@ -16,10 +16,10 @@
 //    M = 128 heads, N = 64 tokens, A = Q from TMEM, B = the page tile in shared
 //    memory).  The partials are exchanged unscaled as fp16 (the scale times
 //    log2 e enters once, in the exponent of P): each
-//    warp stages its rows and one bulk copy per warp pushes them into the peer
-//    CTA, completing on the peer's mbarrier.  Both CTAs add the same two
-//    rounded halves, so they hold bit-identical S and take identical softmax
-//    decisions.
+//    warp stages its rows and bulk copies (two of 2 KB, over the FP8 cache one
+//    of 4 KB) push them into the peer CTA, completing on the peer's mbarrier.
+//    Both CTAs add the same two rounded halves, so they hold bit-identical S
+//    and take identical softmax decisions.
 //  * Softmax in packed fp16 (add, max, subtract, 2^x with one MUFU issue per
 //    pair), P converted to bf16 and written to TMEM; O_r += P·V_r (tcgen05,
 //    N = 256, B = the same page tile read as an MN-major operand) and the row
@@ -36,7 +36,10 @@
 //    of its tile, the other computes.  The only hand-off between them is the
 //    row's reference max, passed from tile g-1 to tile g through a tagged
 //    shared-memory slot.  QK^T and P·V are issued by two warps, each as soon
-//    as its own inputs are ready.
+//    as its own inputs are ready.  The issuing code is reached by whole warps
+//    and one elected lane issues: behind a branch on the lane's number every
+//    MMA's operands go to uniform registers anew, 47 to 60 cycles for one of
+//    N = 64 whose product takes 32 (768 rows of 8 204 tokens 1 391 -> 1 277 us).
 //  * Online softmax with lazy rescaling: the running reference max only moves
 //    when a tile's max exceeds it by more than 8 (log2 units), so P stays
 //    below 256 and O and l in TMEM are rescaled only on those rare tiles.
@@ -196,8 +199,9 @@ struct Layout : Cfg<kF8, kRows> {
 };
 
 constexpr uint32_t kColO = 0, kColS = 256, kColSum = 320, kColQ = 336, kColP = 480, kTmemCols = 512;
-// The producer and the two MMA-issuing threads poll (mbarrier.test_wait)
-// rather than sleep: their wake-up sits on the score chain.
+// The producer and the two MMA-issuing warps sleep in their waits
+// (mbarrier.try_wait): polling takes issue slots from the softmax warps beside
+// them, 1 % of the whole.
 constexpr bool kIssueSuspend = true;
 constexpr uint32_t kTileThreads = 128;                    // the warpgroup that handles one tile
 
@@ -320,11 +324,11 @@ __device__ __forceinline__ uint32_t as_u32(__half2 h) { return *reinterpret_cast
 // of W tokens costs about W / 64 + 1 tiles.  The row's visibility in a tile is
 // a 64-bit mask, formed for the edge tiles only; the latents of masked tokens
 // are cleared before P·V, so such slots may hold anything.
-// Measured (device time of decode and combine): 128 rows of 2112 tokens 93.9
-// us = 0.42 of the tensor peak on the tokens seen, a tile every 2 100 cycles
+// Measured (device time of decode and combine): 128 rows of 2112 tokens 85.5
+// us = 0.46 of the tensor peak on the tokens seen, a tile every 1 750 cycles
 // as in the full decode plus 1.7 row switches a cluster; 16 rows of 4112 tokens
-// of an FP8 cache 46 us (the code conversion's ring); one row of 516 tokens 13.7
-// us, of which 10 are one cluster's latency and 4 the combine.
+// of an FP8 cache 39.8 us (the code conversion's ring); one row of 516 tokens 13.1
+// us, of which 9 are one cluster's latency and 4 the combine.
 //
 // Sees::kTree: the rows are the nodes of drafted trees.  A tile that holds
 // nodes, or slots past the row's own, is an edge tile of the same kind: a
@@ -333,18 +337,19 @@ __device__ __forceinline__ uint32_t as_u32(__half2 h) { return *reinterpret_cast
 // of a tile, and nothing at all: its maximum is then -infinity, its weights and
 // its sum 0, its output 0.  A tree's rows are many and may be short, so a
 // warpgroup of its own (the row warps) loads the next row's queries and stores
-// the finished row: neither sits on the softmax's way any more (64 nodes of 16
-// sequences of 512 tokens 204 -> 194 us, 12 nodes of 64 sequences of 8 192 tokens
-// 1 415 -> 1 375).  What is left of a row's change is the SM's store rate, 32
-// bytes a cycle, and the queries' nine rounds into TMEM: about two tiles' time.
-// Measured: 254 rows of 1 024 to 4 096 tokens 191 us = 0.56 of the tensor peak on
-// the tokens seen; 768 rows of 8 204 tokens 1 389 us at full clocks = 0.66, 1 450
-// back to back under the power cap; 8 rows of 1 032 tokens 18.6 us, latency.
+// the finished row: neither sits on the softmax's way any more (when that was
+// built, 64 nodes of 16 sequences of 512 tokens 204 -> 194 us, 12 nodes of 64
+// sequences of 8 192 tokens 1 415 -> 1 375; the first is 168 now).  What is left of
+// a row's change is the SM's store rate, 32 bytes a cycle, and the queries' nine
+// rounds into TMEM: about two tiles' time.
+// Measured: 254 rows of 1 024 to 4 096 tokens 168 us = 0.64 of the tensor peak on
+// the tokens seen; 768 rows of 8 204 tokens 1 198 us at full clocks = 0.76, 1 290
+// back to back under the power cap; 8 rows of 1 032 tokens 17.4 us, latency.
 //
 // kF16 without kF8: the pages are f16 rows unpacked from the FP8 cache
 // (unpack_kernel, tree.cu), one after another from the segment's first page;
 // operands and results are those of the FP8 kernel, bit for bit.  64 rows of
-// 32 832 tokens: 453 us with the unpacking = 0.67 of the tensor peak, 880 when
+// 32 832 tokens: 351 us with the unpacking = 0.87 of the tensor peak, 690 when
 // every row converts its pages.
 template <bool kF8, Sees kSees, bool kF16 = kF8>
 __device__ __forceinline__ void decode_body(const CUtensorMap& kv_map, const CUtensorMap& rope_map,
@@ -665,8 +670,8 @@ __device__ __forceinline__ void decode_body(const CUtensorMap& kv_map, const CUt
     // ---------------------------------------------------------------- P·V issue
     // Masked: a tile's masked tokens have their latents cleared once QK^T has read
     // the page, while the softmax is at work: their P is 0, but 0 times an
-    // infinity or a NaN is not 0.  (128 rows of 2112 tokens: 93.9 us, 92.9 without
-    // the clearing, 95.8 with the softmax warps clearing.)
+    // infinity or a NaN is not 0.  (128 rows of 2112 tokens: 1 us of the whole, 3
+    // with the softmax warps clearing.)
     TileCursor<kSees> cp;
     cp.init(a.segs, s_begin, s_end, win, tree);
     // The latent chunks read MN-major for P·V, and the ones tile.
@@ -1318,8 +1323,8 @@ __device__ __forceinline__ void decode_body(const CUtensorMap& kv_map, const CUt
     __syncwarp();
   };
   if constexpr (kRowWarps) {
-    // 512 threads x 128 registers at launch: 128*88 + 256*160 + 128*104.  (The
-    // softmax with 136 or 144 loses 2 to 5 % of the whole.)
+    // 512 threads x 128 registers at launch: 128*88 + 256*160 + 128*104.  (Other
+    // splits, down to 144 for the softmax, are within 1 % of this one.)
     if (warp < 4) {
       regs_dec<88>();
       if (warp == 0) role_producer();

@@ -113,16 +113,17 @@ struct PlanKind {
   uint32_t magic() const { return tree ? MLA_TREE_PLAN_MAGIC : window > 0 ? MLA_WINDOW_PLAN_MAGIC : MLA_PLAN_MAGIC; }
 };
 
-// A tree plan's costs, in tiles (about 1 us).  A piece of a row takes four tiles'
+// A tree plan's costs, in tiles (0.87 us).  A piece of a row takes four tiles'
 // time beside its tiles: the queries into TMEM and the row out of it are 64 to
 // 128 KB a CTA, while the next piece's first tile is under way (254 rows over
-// 1 024 to 4 096 tokens: 205 us without it, 195 with four, 198 with eight).
+// 1 024 to 4 096 tokens: 176 us without it, 172 with two, 167 with four, 166 with
+// eight; 768 rows over 8 204: 1 242, 1 192, 1 190 and 1 271).
 constexpr int64_t kTreeRowTiles = 4;
 // In 64ths of a tile: a partial result, 256 KB written, read and merged; and a
 // round of the merge, whose number is that of the pieces of the row with most
-// (one row over 8 192 tokens: 25.5 us in 64 pieces, 20.8 in 32, 19.1 in 26, 21.0 in 16; four
-// rows over 4 096: 22.6 in 16 pieces each, 19.1 in 11, 20.5 in 8; 32 rows over
-// 1 024: 21.6 in two, 22.6 whole).
+// (one row over 8 192 tokens: 25.5 us in 64 pieces, 20.8 in 32, 19.1 in 26, 21.0 in
+// 16; four rows over 4 096: 22.6 in 16 pieces each, 19.1 in 11, 20.5 in 8; 32 rows
+// over 1 024: 21.6 in two, 22.6 whole).
 constexpr int64_t kTreePartial = 5, kTreePiece = 16;
 // The share of the L2 cache (129 MB) that a plan counts on for the sequences
 // being read at one time.
@@ -133,8 +134,8 @@ constexpr int64_t kTreeSharedBytes = 64ll << 20;
 // together, and every lane at the same time, so that num_clusters / lanes
 // sequences are being read at once, each by `lanes` clusters.  The fewest lanes
 // that keep those in L2, of those that divide the clusters evenly (12 rows of 64
-// sequences of 8 192 tokens: 1 410 us in four lanes, 1 475 in one; two rows: 260
-// us in two lanes, 270 in one).
+// sequences of 8 192 tokens: 1 216 us in four lanes, 1 244 in two, 1 323 in one;
+// two rows: 226 in two, 246 in one).
 int32_t tree_lanes(const int32_t* seq_lens, const int32_t* q_lens, int32_t B, int32_t num_clusters) {
   int64_t tokens = 0, seqs = 0;
   int32_t most = 0;
@@ -381,7 +382,7 @@ mla_status no_throw(F&& body) {
 
 // A tree decode unpacks at most so many pages of the FP8 cache (4.8 GB).
 constexpr int64_t kMostUnpackedPages = 1 << 16;
-constexpr int64_t kUnpackTiles = 256;
+constexpr int64_t kUnpackTiles = 512;
 
 size_t workspace_bytes_for(int64_t partials) {
   return (size_t)partials * (MLA_NUM_HEADS * MLA_LATENT_DIM * 4 + MLA_NUM_HEADS * 4);
@@ -1779,16 +1780,17 @@ mla_status mla_tree_plan(const int32_t* seq_lens_host, const int32_t* q_lens_hos
                      {0, 0, true}, info);
 }
 
-// Whether a tree decode over the FP8 cache unpacks its pages: with two rows to a
-// page or more (a sequence's first row may need one page less), and enough tiles
+// Whether a tree decode over the FP8 cache unpacks its pages: with three rows to a
+// page or more (a sequence's first two may need one page less), and enough tiles
 // to pay for a launch.  A tile of f16 rows takes half the time of one that has to
-// be converted; unpacked and not: 16 sequences of 8 192 tokens, two rows 113 and
-// 125 us, three rows of 2 048 tokens 53 and 64; 12 rows over 4 096 tokens 31 and
-// 36; 16 rows over 1 024 (272 tiles) 26.7 and 27.0; 64 rows over 32 768 459 and
-// 880.
+// be converted; unpacked and not, in us: two rows of 16 sequences of 8 192 tokens
+// 101 and 101, of 64 of 2 048 tokens 109 and 102; three rows of 16 of 2 048 46 and
+// 49, of 8 (792 tiles) 27.8 and 30.5; one sequence: 16 rows over 1 024 tokens (272
+// tiles) 20 and 20, 8 over 2 048 (264) 22.2 and 21.6, 12 over 4 096 (780) 26 and
+// 30, 64 over 32 768 349 and 688; two sequences, 8 rows over 2 048 (528) 24 and 25.
 static bool tree_unpacks(const mla_tree_info& info) {
   return info.total_pages > 0 && info.total_pages <= kMostUnpackedPages && info.num_trees <= 65535 &&
-         info.plan.total_tiles >= kUnpackTiles && info.plan.total_tiles + info.num_trees >= 2 * info.total_pages;
+         info.plan.total_tiles >= kUnpackTiles && info.plan.total_tiles + 2 * info.num_trees >= 3 * info.total_pages;
 }
 static size_t unpacked_bytes(const mla_tree_info& info) { return (size_t)info.total_pages * MLA_PAGE_BYTES; }
 

@@ -347,7 +347,6 @@ __device__ __forceinline__ void tc_commit(uint32_t bar) {
   asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar)
                : "memory");
 }
-// D(tmem) (+)= A(smem) * B(smem)
 // One lane of a converged warp, the same at every call.  An issuing role walks
 // its loop with the whole warp and branches on this around its MMAs: operands
 // that the compiler sees to be the same in every lane stay in uniform registers,
@@ -359,6 +358,7 @@ __device__ __forceinline__ bool elect_one() {
   return p != 0;
 }
 
+// D(tmem) (+)= A(smem) * B(smem)
 __device__ __forceinline__ void mma_ss(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
                                        uint32_t accumulate) {
   asm volatile(
@@ -538,13 +538,6 @@ __device__ __forceinline__ void tmem_ld_wait() { asm volatile("tcgen05.wait::ld.
 // so no use of them can be scheduled before it.
 __device__ __forceinline__ void tmem_ld32_sync(uint32_t taddr, uint32_t (&r)[32]) {
   tmem_ld32(taddr, r);
-  asm volatile("tcgen05.wait::ld.sync.aligned;"
-               : MLA_RW8(r, 0), MLA_RW8(r, 8), MLA_RW8(r, 16), MLA_RW8(r, 24)
-               :
-               : "memory");
-}
-// Wait for columns that tmem_ld32 asked for, tied to the registers they land in.
-__device__ __forceinline__ void tmem_ld32_wait(uint32_t (&r)[32]) {
   asm volatile("tcgen05.wait::ld.sync.aligned;"
                : MLA_RW8(r, 0), MLA_RW8(r, 8), MLA_RW8(r, 16), MLA_RW8(r, 24)
                :
