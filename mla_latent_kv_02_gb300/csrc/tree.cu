@@ -132,10 +132,8 @@ __global__ void __launch_bounds__(256) compact_kernel(const TreeCompactArgs a, i
   if (t == 0 && first) a.new_lens[b] = len - n + kept;
   if (t <= acc) {
     slot[t] = slot_of(a.block_table + (int64_t)b * a.max_pages, a.max_pages, a.c.num_pages, len - n + t);
-    if (mine) {
-      if (slot[t] < 0 && first) atomicOr(a.dev_err, (int32_t)MLA_DEVERR_PAGE_OOB);
-      node[rank] = (int16_t)t;
-    }
+    if (slot[t] < 0 && first && (mine || t < kept)) atomicOr(a.dev_err, (int32_t)MLA_DEVERR_PAGE_OOB);
+    if (mine) node[rank] = (int16_t)t;
   }
   __syncthreads();
   const int piece = t % C::kPer, r0 = t / C::kPer;

@@ -529,6 +529,18 @@ def test_compact_judges_its_inputs(api):
         api.mla_tree_compact(kv[:1].expand(2, 4, 64, 576), *ok[1:])
 
 
+def test_compact_to_a_bad_page(api):
+    """The kept row's page is good, the one that it would move to is not: nothing moves, and the word says so."""
+    raw = layered("bf16", 2, 4, 1)
+    want = raw[0].clone()
+    m = torch.tensor([[1], [2]], dtype=torch.int64, device="cuda")
+    bt = torch.tensor([[9, 1]], dtype=torch.int32, device="cuda")
+    new, err = torch.full((1,), -7, dtype=torch.int32, device="cuda"), word()
+    api.mla_tree_compact(views("bf16", raw, 4)[0], bt, m, i32([0, 2]), i32([65]), i32([1]), new, err)
+    assert int(err.item()) == api.DEVERR_PAGE_OOB
+    assert new.tolist() == [64] and torch.equal(raw[0], want)
+
+
 @pytest.mark.parametrize("kind", ["bf16", "fp8", "nvfp4"])
 @pytest.mark.parametrize("layers, gap, pages, pairs", [(1, 0, 2, 1), (3, 0, 50, 20), (2, 1, 200, 65), (1, 0, 30, 15)])
 def test_copy_pages(api, kind, layers, gap, pages, pairs):
