@@ -289,7 +289,7 @@ struct TileCursor {
   }
   // Whether the row may see less than the whole of the current tile.
   __device__ __forceinline__ bool edge() const {
-    if constexpr (kTree) return (pg + 1) * kPage > wlo;
+    if constexpr (kTree) return pg >= wlo / kPage;  // (pg + 1) * kPage may pass 31 bits
     return pg <= w.sink_tiles || vis - (pg + w.skip) * kPage < kPage;
   }
   static __device__ __forceinline__ uint64_t bits_below(int n) {
