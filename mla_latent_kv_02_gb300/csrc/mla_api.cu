@@ -1598,7 +1598,12 @@ static mla_status tree_compact(const mla::LayerCaches& c, int row_bytes, bool fp
     const void* p;
     uintptr_t bytes;
     const char* what;
-  } in[] = {{seq_lens, len, "seq_lens"}, {accepted, len, "accepted"}, {q_starts, len + 4, "q_starts"}};
+  } in[] = {{seq_lens, len, "seq_lens"},
+            {accepted, len, "accepted"},
+            {q_starts, len + 4, "q_starts"},
+            {masks, (uintptr_t)T * words * 8, "masks"},
+            {block_table, len * max_pages, "block_table"},
+            {dev_err, 4, "dev_err"}};
   for (const auto& x : in)
     if (out < (uintptr_t)x.p + x.bytes && (uintptr_t)x.p < out + len)
       return fail(MLA_ERR_INVALID_ARG, "new_lens and %s overlap", x.what);

@@ -122,6 +122,9 @@ def test_layout_and_compact_refusals(api):
     assert compact(pages=0) == 1 and compact(table=None) == 1 and compact(cols=0) == 1 and compact(words=9) == 1
     assert compact(lens=ok) == 1                            # the lengths would be read and written
     assert compact(lens=C.c_void_p((1 << 20) + 4)) == 1
+    base = 1 << 24                                          # nor may they lie anywhere in the masks, the table or the word
+    for at, kw in ((39, dict(masks=C.c_void_p(base), T=5)), (23, dict(table=C.c_void_p(base))), (3, dict(err=C.c_void_p(base)))):
+        assert compact(lens=C.c_void_p(base + at // 4 * 4), **kw) == 1, kw
     assert compact(acc=None) == 1 and compact(masks=None) == 1 and compact(masks=odd) == 2 and compact(lens=odd) == 2
     assert compact(B=0) == 0
     assert _lib_call("mla_tree_compact_fp8", ok, None, 4, 1, 0, 0, ok, 3, ok, 1, ok, ok, ok, 2, 5, far, ok, None) == 1
