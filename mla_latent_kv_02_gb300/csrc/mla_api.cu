@@ -1505,16 +1505,28 @@ static mla_status copy_pages(const mla::LayerCaches& c, int row_bytes, bool fp8,
   mla_status s = check_layers(c, row_bytes, fp8);
   if (s != MLA_OK) return s;
   return no_throw([&] {
-    std::vector<uint8_t> role((size_t)c.num_pages, 0);  // 1: read, 2: written
-    for (int32_t i = 0; i < n; ++i) {
+    for (int32_t i = 0; i < n; ++i)
       for (const int32_t id : {src[i], dst[i]})
         if (id < 0 || id >= c.num_pages) return fail(MLA_ERR_INVALID_ARG, "copy %d: page id %d out of range", i, id);
-      role[src[i]] |= 1;
-      if (role[dst[i]] & 2) return fail(MLA_ERR_INVALID_ARG, "copy %d: page %d is written twice", i, dst[i]);
-      role[dst[i]] |= 2;
+    // The written pages: a bit each, or for few pairs of a large pool a sorted list
+    // (two pairs of 4 000 000 pages: 183 us with the bits' predecessor, a byte each).
+    if (n <= c.num_pages / 4096) {
+      std::vector<int32_t> written(dst, dst + n);
+      std::sort(written.begin(), written.end());
+      const auto twice = std::adjacent_find(written.begin(), written.end());
+      if (twice != written.end()) return fail(MLA_ERR_INVALID_ARG, "page %d is written twice", *twice);
+      for (int32_t i = 0; i < n; ++i)
+        if (std::binary_search(written.begin(), written.end(), src[i]))
+          return fail(MLA_ERR_INVALID_ARG, "copy %d: page %d is read and written", i, src[i]);
+    } else {
+      std::vector<bool> written((size_t)c.num_pages);
+      for (int32_t i = 0; i < n; ++i) {
+        if (written[dst[i]]) return fail(MLA_ERR_INVALID_ARG, "page %d is written twice", dst[i]);
+        written[dst[i]] = true;
+      }
+      for (int32_t i = 0; i < n; ++i)
+        if (written[src[i]]) return fail(MLA_ERR_INVALID_ARG, "copy %d: page %d is read and written", i, src[i]);
     }
-    for (int32_t i = 0; i < n; ++i)
-      if (role[src[i]] == 3) return fail(MLA_ERR_INVALID_ARG, "copy %d: page %d is read and written", i, src[i]);
     cudaError_t e = mla::launch_copy_pages(c, row_bytes, src, dst, n, (cudaStream_t)stream);
     if (e != cudaSuccess) return cuda_fail(e, "copy_pages launch");
     return MLA_OK;

@@ -144,6 +144,9 @@ def test_copy_pages_refusals(api):
     assert copy(_i32(0, 1), _i32(2, 2)) == 1                # written twice
     assert copy(_i32(0, 1), _i32(1, 2)) == 1                # read and written
     assert copy(_i32(3), _i32(3)) == 1
+    many = 1 << 21                                          # a pool of which few pages are named
+    for src, dst in ((_i32(0, many - 1), _i32(2, 2)), (_i32(0, 1), _i32(1, 2)), (_i32(many), _i32(0)), (_i32(0), _i32(many))):
+        assert copy(src, dst, pages=many, layers=1) == 1
     assert copy(_i32(8), _i32(0)) == 1 and copy(_i32(0), _i32(8)) == 1 and copy(_i32(-1), _i32(0)) == 1
     assert copy(_i32(0), _i32(1), kv=None) == 1 and copy(_i32(0), _i32(1), kv=C.c_void_p((1 << 20) + 8)) == 2
     assert copy(_i32(0), _i32(1), layers=0) == 1 and copy(_i32(0), _i32(1), stride=73728) == 1
