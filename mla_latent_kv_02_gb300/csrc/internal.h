@@ -201,7 +201,8 @@ struct TreeUnpackArgs {
   int32_t B;
   int32_t T;
   int32_t words;
-  int32_t out_pages;
+  int32_t out_pages;           // those of all the trees' sequences
+  int32_t num_trees;
 };
 
 // Trees of drafted nodes, a sequence each (tree.cu): sequence b's nodes are
@@ -280,7 +281,7 @@ cudaError_t launch_decode_window(const CUtensorMap& kv_map, const CUtensorMap& r
 enum class TreeCache { kBf16, kFp8, kUnpacked };
 cudaError_t launch_decode_tree(const CUtensorMap& kv_map, const CUtensorMap& rope_map, const DecodeArgs& args,
                                const TreeArgs& tree, int num_clusters, TreeCache cache, cudaStream_t stream);
-cudaError_t launch_tree_unpack(const TreeUnpackArgs& args, int num_trees, int max_tree_pages, cudaStream_t stream);
+cudaError_t launch_tree_unpack(const TreeUnpackArgs& args, cudaStream_t stream);
 cudaError_t launch_combine(const CombineArgs& args, int num_split_rows, cudaStream_t stream);
 
 cudaError_t launch_kv_append(const uint16_t* c_kv_new, const uint16_t* k_r_new, const int64_t* slots, int32_t n,

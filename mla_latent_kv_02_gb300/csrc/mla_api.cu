@@ -1806,8 +1806,8 @@ mla_status mla_tree_plan(const int32_t* seq_lens_host, const int32_t* q_lens_hos
 // tiles) 20 and 20, 8 over 2 048 (264) 22.2 and 21.6, 12 over 4 096 (780) 26 and
 // 30, 64 over 32 768 349 and 688; two sequences, 8 rows over 2 048 (528) 24 and 25.
 static bool tree_unpacks(const mla_tree_info& info) {
-  return info.total_pages > 0 && info.total_pages <= kMostUnpackedPages && info.num_trees <= 65535 &&
-         info.plan.total_tiles >= kUnpackTiles && info.plan.total_tiles + 2 * info.num_trees >= 3 * info.total_pages;
+  return info.num_trees > 0 && info.total_pages > 0 && info.total_pages <= kMostUnpackedPages &&
+         info.plan.total_tiles >= kUnpackTiles && info.plan.total_tiles + 2ll * info.num_trees >= 3 * info.total_pages;
 }
 static size_t unpacked_bytes(const mla_tree_info& info) { return (size_t)info.total_pages * MLA_PAGE_BYTES; }
 
@@ -1882,8 +1882,8 @@ static mla_status decode_common(const void* q_abs, const void* q_r, const void* 
     uint8_t* out = (uint8_t*)workspace + need_ws;
     const mla::TreeUnpackArgs u = {(const uint8_t*)kv_cache, kv_scales, num_pages, block_table, tree->masks, plan + L.words,
                                    (uint4*)out, dev_err, max_pages, info->B, info->T, tree->words,
-                                   (int32_t)tree_info->total_pages};
-    cudaError_t e = mla::launch_tree_unpack(u, tree_info->num_trees, info->max_pages_needed, (cudaStream_t)stream);
+                                   (int32_t)tree_info->total_pages, tree_info->num_trees};
+    cudaError_t e = mla::launch_tree_unpack(u, (cudaStream_t)stream);
     if (e != cudaSuccess) return cuda_fail(e, "unpack launch");
     kv_cache = out;
     num_pages = tree_info->total_pages;

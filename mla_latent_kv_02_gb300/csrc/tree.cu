@@ -171,21 +171,32 @@ __global__ void __launch_bounds__(256) compact_kernel(const TreeCompactArgs a, i
   }
 }
 
-// One CTA a page (x) of a tree's sequence (y): its 64 rows of E4M3 codes become
-// f16 rows of 576, code * 2^k and RoPE, each value as the FP8 decode forms it on
-// chip.  A token's scale outside the f16 range counts only where a row sees it:
+// One CTA a page: its 64 rows of E4M3 codes become f16 rows of 576, code * 2^k and
+// RoPE, each value as the FP8 decode forms it on chip.  A warp finds the page's
+// sequence in the plan's table, 32 entries a look: a grid of sequences by the
+// longest one's pages is mostly empty for ragged batches
+// (decode of 255 sequences of 1 032 tokens and one of 262 144: 2 023 -> 1 043 us).  A token's scale outside the f16 range counts only where a row sees it:
 // every row sees the tokens before the tree, and the nodes' masks are asked in
 // that case alone.  Rows past the sequence's end become zeros.  Moves 1.8 KB a
 // token: 12.9 us for 32 832 tokens with cold caches, 21 MB from HBM and 38 into L2.
 __global__ void __launch_bounds__(256) unpack_kernel(const TreeUnpackArgs a) {
-  const int4 lo = __ldg(reinterpret_cast<const int4*>(a.trees) + 2 * blockIdx.y);
-  const int4 hi = __ldg(reinterpret_cast<const int4*>(a.trees) + 2 * blockIdx.y + 1);
-  const int32_t b = lo.x, base = lo.y, pages = lo.z, n0 = lo.w, len = hi.x, row0 = hi.y, nodes = hi.z;
-  const int t = threadIdx.x, pg = blockIdx.x;
+  const int t = threadIdx.x;
+  const int32_t page = blockIdx.x;
   if (t == 0) dev::grid_launch_dependents();  // the decode may get ready; it waits before it reads a page
-  if (pg >= pages) return;
-  if (b < 0 || b >= a.B || base < 0 || pages > a.out_pages - base || pages > a.max_pages || n0 < 0 || row0 < 0 ||
-      nodes < 0 || nodes > a.T - row0) {
+  int at = 0;                                 // the last tree whose first page is not behind this one
+  for (int n = a.num_trees; n > 1;) {
+    const int step = (n + 31) / 32, i = (t & 31) * step;
+    const bool le = i < n && __ldg(a.trees + (int64_t)(at + i) * kTreeWords + 1) <= page;
+    const int k = max(__popc(__ballot_sync(0xffffffffu, le)) - 1, 0) * step;
+    at += k;
+    n = min(step, n - k);
+  }
+  const int4 lo = __ldg(reinterpret_cast<const int4*>(a.trees) + 2 * at);
+  const int4 hi = __ldg(reinterpret_cast<const int4*>(a.trees) + 2 * at + 1);
+  const int32_t b = lo.x, base = lo.y, pages = lo.z, n0 = lo.w, len = hi.x, row0 = hi.y, nodes = hi.z;
+  const int64_t pg = (int64_t)page - base;    // of the sequence
+  if (b < 0 || b >= a.B || base < 0 || pg < 0 || pg >= pages || pages > a.max_pages || n0 < 0 || row0 < 0 || nodes < 0 ||
+      nodes > a.T - row0) {
     if (t == 0) atomicOr(a.dev_err, (int32_t)MLA_DEVERR_PLAN);
     return;
   }
@@ -195,13 +206,13 @@ __global__ void __launch_bounds__(256) unpack_kernel(const TreeUnpackArgs a) {
     id = 0;
   }
   const uint4* src = reinterpret_cast<const uint4*>(a.rows + (int64_t)id * MLA_PAGE_SIZE * MLA_FP8_ROW_BYTES);
-  uint4* dst = a.out + ((int64_t)base + pg) * MLA_PAGE_SIZE * (MLA_TOKEN_ELEMS / 8);
+  uint4* dst = a.out + (int64_t)page * MLA_PAGE_SIZE * (MLA_TOKEN_ELEMS / 8);
   // Eight codes and one 16-byte store a thread, two warps a row: a warp stores
   // 512 bytes in one piece (16 codes and two stores left half sectors: 100 MB
   // through L2 for 38).
   constexpr int kRows = 8;  // of a thread at a time
   const int piece = t % 64, r0 = t / 64;
-  const int last = min(len - pg * MLA_PAGE_SIZE, MLA_PAGE_SIZE);
+  const int last = (int)min((int64_t)len - pg * MLA_PAGE_SIZE, (int64_t)MLA_PAGE_SIZE);
 #pragma unroll
   for (int half = 0; half < 2; ++half) {
     uint2 code[kRows];
@@ -218,7 +229,7 @@ __global__ void __launch_bounds__(256) unpack_kernel(const TreeUnpackArgs a) {
       bool ok;
       const uint32_t f = dev::fp8_f16_factor(scale[j], ok);
       if (!ok) {
-        const int k = pg * MLA_PAGE_SIZE + r - n0;  // its node
+        const int k = (int)(pg * MLA_PAGE_SIZE + r - n0);  // its node
         bool seen = k < 0;
         if (k >= 0 && (k >> 6) < a.words)
           for (int i = k + piece; i < nodes; i += 64)
@@ -254,8 +265,8 @@ cudaError_t run_compact(const TreeCompactArgs& a, cudaStream_t stream) {
 
 }  // namespace tree
 
-cudaError_t launch_tree_unpack(const TreeUnpackArgs& args, int num_trees, int max_tree_pages, cudaStream_t stream) {
-  tree::unpack_kernel<<<dim3(max_tree_pages, num_trees), 256, 0, stream>>>(args);
+cudaError_t launch_tree_unpack(const TreeUnpackArgs& args, cudaStream_t stream) {
+  tree::unpack_kernel<<<args.out_pages, 256, 0, stream>>>(args);
   return cudaGetLastError();
 }
 

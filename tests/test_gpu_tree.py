@@ -263,6 +263,22 @@ def test_unpacked_pages_give_the_same_bits(api, nodes):
     check(few, q_abs[:2], q_r[:2], m2, o3, lse3, [2])
 
 
+@pytest.mark.parametrize("trees", [1, 31, 33, 1030])
+def test_unpacked_pages_of_ragged_batches(api, trees):
+    """Each page is found in the table of the trees: few and many of them, short ones beside a long one, some without nodes."""
+    nodes = [0 if b % 7 == 3 else 4 + b % 5 for b in range(trees)] + [16]
+    cache = Cache(api, [30 + 17 * (b % 9) for b in range(trees)] + [3000], "fp8", trees)
+    m = torch.from_numpy(masks([tree(b, n) for b, n in enumerate(nodes)], 1)).cuda()
+    q_abs, q_r = queries(sum(nodes), trees)
+    plans = [api.mla_tree_plan(cache.n, nodes) for _ in range(2)]
+    assert api.mla_tree_workspace_size(plans[0].info, True) > api.mla_tree_workspace_size(plans[0].info, False)
+    o, lse, err = decode(api, cache, q_abs, q_r, m, plans[0])
+    o2, lse2, err2 = decode(api, cache, q_abs, q_r, m, direct(api, plans[1]))
+    assert api.mla_check(err) == 0 and api.mla_check(err2) == 0
+    assert torch.equal(o, o2) and torch.equal(lse, lse2)
+    check(cache, q_abs, q_r, m, o, lse, nodes, set(range(0, sum(nodes), max(1, sum(nodes) // 12))))
+
+
 def test_unpacked_decode_is_captured(api):
     """First use of a plan inside a capture, two graphs of one plan, replayed in turn after the cache has changed."""
     n0, q = 1200, 48
