@@ -532,6 +532,13 @@ def _torch_stream(stream, raw: int, dev: int):
     return torch.cuda.ExternalStream(raw, device=dev) if raw else torch.cuda.default_stream(dev)
 
 
+def _capturing(stream, dev: int) -> bool:
+    if stream is None or stream.cuda_stream == _on(None, dev):
+        return torch.cuda.is_current_stream_capturing()
+    with torch.cuda.stream(_torch_stream(stream, stream.cuda_stream, dev)):
+        return torch.cuda.is_current_stream_capturing()
+
+
 def _use(plan, stream, dev: int) -> int:
     """The raw handle of the stream that a call reads or writes a plan's buffers
     on.  The allocator learns of every such stream: a plan may be dropped as soon
@@ -932,6 +939,7 @@ class TreePlan:
     rows: int = 0               # the summary's T and B, at hand for every call
     seqs: int = 0
     unpack: bool = field(default=False, repr=False, compare=False)  # the workspace was judged for an FP8 cache
+    captured: list = field(default_factory=list, repr=False, compare=False)  # workspaces that captured graphs name
 
     @property
     def num_clusters(self) -> int:
@@ -944,7 +952,10 @@ def mla_tree_plan(seq_lens: Sequence[int], q_lens: Sequence[int], device=None, n
     seq_lens[b] tokens): one plan serves every layer of a step, whatever the
     trees' shapes.  Uploads, streams, sharing and `into` as for mla_window_plan.
     The first decode over an FP8 cache that several rows share takes a larger
-    workspace (mla_tree_workspace_size); it stays with the plan."""
+    workspace (mla_tree_workspace_size); it stays with the plan, and one that a
+    captured decode used before stays as well: keep the plan as long as the graph."""
+    if into is not None and not isinstance(into, TreePlan):
+        raise TypeError("into must be a plan of mla_tree_plan")
     if num_clusters is None:
         num_clusters = mla_decode_max_clusters()
     buf, info = mla_tree_plan_host(seq_lens, q_lens, num_clusters)
@@ -971,7 +982,7 @@ def mla_decode_tree_fp8(q_abs, q_r, rows, scales, block_table, masks, plan: Tree
     pages = rows.shape[0]
     cache = (_in(rows, "rows", torch.uint8, (pages, PAGE, FP8_ROW_BYTES), dev),
              _in(scales, "scales", torch.float32, (pages, PAGE), dev))
-    if isinstance(plan, TreePlan) and not plan.unpack:
+    if isinstance(plan, TreePlan) and not plan.unpack and plan.plan.get_device() == dev:
         _room_to_unpack(plan, stream, dev)
     _decode_tree(lib().mla_decode_tree_fp8, cache, pages, q_abs, q_r, block_table, masks, plan, o_lat, dev_err, lse, scale,
                  stream, dev)
@@ -985,6 +996,8 @@ def _decode_tree(call, cache, pages, q_abs, q_r, block_table, masks, plan, o_lat
     table, cols = _table(block_table, plan.seqs, dev)
     if plan.plan.get_device() != dev or ws.get_device() != dev:
         raise ValueError(f"the plan is on {plan.plan.device}, the current device is cuda:{dev}")
+    if _capturing(stream, dev) and not any(w is ws for w in plan.captured):
+        plan.captured.append(ws)
     _check(call(_in(q_abs, "q_abs", torch.bfloat16, (T, H, D_C), dev), _in(q_r, "q_r", torch.bfloat16, (T, H, D_R), dev),
                 *cache, pages, table, cols, m, words, plan.plan.data_ptr(), plan.info, scale, ws.data_ptr(), ws.numel(),
                 _in(o_lat, "o_lat", torch.bfloat16, (T, H, D_C), dev),

@@ -279,6 +279,55 @@ def test_unpacked_pages_of_ragged_batches(api, trees):
     check(cache, q_abs, q_r, m, o, lse, nodes, set(range(0, sum(nodes), max(1, sum(nodes) // 12))))
 
 
+def test_a_captured_workspace_outlives_the_next(api):
+    """A graph of the bf16 decode, then the same plan over an FP8 cache takes a larger workspace: the graph's stays."""
+    n0, q = 3000, 20
+    cache, eight = Cache(api, [n0 + q], "bf16", 31), Cache(api, [n0 + q], "fp8", 31)
+    m = torch.from_numpy(masks([tree(0, q)], 1)).cuda()
+    q_abs, q_r = queries(q, 31)
+    plan = api.mla_tree_plan(cache.n, [q])
+    plan.workspace = plan.workspace[:api.mla_tree_workspace_size(plan.info, False)].clone()   # none to spare
+    want = decode(api, cache, q_abs, q_r, m, api.mla_tree_plan(cache.n, [q]))[0]
+    wait = torch.cuda.Stream()
+    o, err, graph = torch.zeros_like(want), word(), torch.cuda.CUDAGraph()
+    lse = torch.zeros((q, 128), device="cuda")
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph, stream=wait):
+        decode(api, cache, q_abs, q_r, m, plan, o=o, lse=lse, err=err)
+        decode(api, cache, q_abs, q_r, m, plan, o=o, lse=lse, err=err, stream=wait)
+    held = plan.workspace
+    assert held.numel() > 0 and len(plan.captured) == 1 and plan.captured[0] is held
+    e = decode(api, eight, q_abs, q_r, m, plan)[2]
+    assert plan.workspace.data_ptr() != held.data_ptr() and plan.captured[0] is held
+    graph.replay()
+    torch.cuda.synchronize()
+    assert int(e.item()) == 0 and int(err.item()) == 0 and torch.equal(o, want)
+    with pytest.raises(TypeError):
+        api.mla_tree_plan(cache.n, [q], into=api.mla_decode_plan(cache.n, [q]))
+
+
+@pytest.mark.parametrize("kind", ["bf16", "fp8"])
+def test_longest_positions(api, kind):
+    """2^31 - 1 tokens, all on one page but the last: its first node is NaN, which the second does not see."""
+    n = 2 ** 31 - 1
+    cache = Cache(api, [64, 64], kind, 41)
+    table = torch.full((1, (n + 63) // 64), int(cache.bt[0, 0]), dtype=torch.int32, device="cuda")
+    last = int(cache.bt[1, 0])
+    table[0, -1] = last
+    if kind == "bf16":
+        cache.kv[last, 61] = float("nan")                    # position n - 2
+    else:
+        cache.rows[last, 61] = 0x7F
+    m = torch.tensor([[1], [2]], dtype=torch.int64, device="cuda")
+    plan = api.mla_tree_plan([n], [2])
+    q_abs, q_r = queries(2, 41)
+    cache.table = table
+    o, lse, err = decode(api, cache, q_abs, q_r, m, plan)
+    assert api.mla_check(err) == 0
+    assert bool(torch.isnan(o[0]).all())
+    assert bool(torch.isfinite(o[1]).all()) and bool(torch.isfinite(lse[1]).all())
+
+
 def test_unpacked_decode_is_captured(api):
     """First use of a plan inside a capture, two graphs of one plan, replayed in turn after the cache has changed."""
     n0, q = 1200, 48
