@@ -307,6 +307,41 @@ def test_a_captured_workspace_outlives_the_next(api):
 
 
 @pytest.mark.parametrize("kind", ["bf16", "fp8"])
+def test_wider_masks_and_tables(api, kind):
+    """Words that no tree needs, rows and columns of the table past the batch: the same bits, whatever they hold."""
+    nodes = [20, 64, 3]
+    cache = Cache(api, [300, 64, 1000], kind, 51)
+    m = torch.from_numpy(masks([tree(b, n) for b, n in enumerate(nodes)], 1)).cuda()
+    q_abs, q_r = queries(sum(nodes), 51)
+    o, lse, err = decode(api, cache, q_abs, q_r, m, api.mla_tree_plan(cache.n, nodes))
+    wide = torch.full((sum(nodes), 4), -1, dtype=torch.int64, device="cuda")
+    wide[:, :1] = m
+    table = torch.full((5, cache.table.shape[1] + 9), 1 << 30, dtype=torch.int32, device="cuda")
+    table[:3, :cache.table.shape[1]] = cache.table
+    cache.table = table
+    o2, lse2, err2 = decode(api, cache, q_abs, q_r, wide, api.mla_tree_plan(cache.n, nodes))
+    assert int(err.item()) == 0 and int(err2.item()) == 0 and torch.equal(o, o2) and torch.equal(lse, lse2)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "fp8", "nvfp4"])
+def test_batches_without_nodes(api, kind):
+    err, none = word(), torch.empty((0, 1), dtype=torch.int64, device="cuda")
+    new = torch.zeros(2, dtype=torch.int32, device="cuda")
+    raw = layered(kind, 2, 4, 2)
+    want = [x.clone() for x in raw]
+    table = torch.tensor([[0, 1], [2, 3]], dtype=torch.int32, device="cuda")
+    api.mla_tree_layout(i32([]), i32([0, 0, 0]), i32([70, 5]), none, err)
+    call(api, "mla_tree_compact", kind, *views(kind, raw, 4), table, none, i32([0, 0, 0]), i32([70, 5]), i32([-1, -1]), new, err)
+    assert int(err.item()) == 0 and new.tolist() == [70, 5]
+    assert all(torch.equal(x, w) for x, w in zip(raw, want))
+    if kind != "nvfp4":
+        cache = Cache(api, [70, 5], kind, 52)
+        q_abs, q_r = (torch.empty((0, 128, d), dtype=torch.bfloat16, device="cuda") for d in (512, 64))
+        decode(api, cache, q_abs, q_r, none, api.mla_tree_plan([70, 5], [0, 0]), err=err)
+        assert int(err.item()) == 0
+
+
+@pytest.mark.parametrize("kind", ["bf16", "fp8"])
 def test_longest_positions(api, kind):
     """2^31 - 1 tokens, all on one page but the last: its first node is NaN, which the second does not see."""
     n = 2 ** 31 - 1
