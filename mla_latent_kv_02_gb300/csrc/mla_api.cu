@@ -16,6 +16,7 @@
 #include <mutex>
 #include <new>
 #include <string>
+#include <utility>
 #include <vector>
 
 #include "../../include/mla.h"
@@ -113,12 +114,15 @@ struct PlanKind {
   uint32_t magic() const { return tree ? MLA_TREE_PLAN_MAGIC : window > 0 ? MLA_WINDOW_PLAN_MAGIC : MLA_PLAN_MAGIC; }
 };
 
-// A tree plan's costs, in tiles (0.87 us).  A piece of a row takes four tiles'
+// A tree plan's costs, in tiles (0.85 us).  A piece of a row takes four tiles'
 // time beside its tiles: the queries into TMEM and the row out of it are 64 to
-// 128 KB a CTA, while the next piece's first tile is under way (254 rows over
-// 1 024 to 4 096 tokens: 176 us without it, 172 with two, 167 with four, 166 with
-// eight; 768 rows over 8 204: 1 242, 1 192, 1 190 and 1 271).
+// 128 KB a CTA, while the next piece's first tile is under way (two, six and eight
+// tiles are within 1 %, as long as rows are dealt out, and contiguous ranges lost
+// 5 % without it: 254 rows over 1 024 to 4 096 tokens).
 constexpr int64_t kTreeRowTiles = 4;
+// No smaller piece is cut off a row that is dealt out (192 rows over 8 192 tokens:
+// 279 us, 288 with eight tiles, 292 with two).
+constexpr int64_t kTreeCrumb = 16;
 // In 64ths of a tile: a partial result, 256 KB written, read and merged; and a
 // round of the merge, whose number is that of the pieces of the row with most
 // (one row over 8 192 tokens: 25.5 us in 64 pieces, 20.8 in 32, 19.1 in 26, 21.0 in
@@ -129,13 +133,13 @@ constexpr int64_t kTreePartial = 5, kTreePiece = 16;
 // being read at one time.
 constexpr int64_t kTreeSharedBytes = 64ll << 20;
 
-// Lanes of a tree plan.  Rows are planned lane by lane, lane j holding the j-th
-// share of every sequence's rows: the clusters of a lane walk the sequences
-// together, and every lane at the same time, so that num_clusters / lanes
-// sequences are being read at once, each by `lanes` clusters.  The fewest lanes
-// that keep those in L2, of those that divide the clusters evenly (12 rows of 64
-// sequences of 8 192 tokens: 1 216 us in four lanes, 1 244 in two, 1 323 in one;
-// two rows: 226 in two, 246 in one).
+// Lanes of a tree plan of fewer rows than clusters.  Rows are planned lane by lane,
+// lane j holding the j-th share of every sequence's rows: the clusters of a lane
+// walk the sequences together, and every lane at the same time, so that
+// num_clusters / lanes sequences are being read at once, each by `lanes` clusters.
+// The fewest lanes that keep those in L2, of those that divide the clusters evenly
+// (two rows of 32 sequences of 8 192 tokens: 123 us in two lanes, 134 in one; four
+// of 16 of 16 384: 214 in four, 240 in one).
 int32_t tree_lanes(const int32_t* seq_lens, const int32_t* q_lens, int32_t B, int32_t num_clusters) {
   int64_t tokens = 0, seqs = 0;
   int32_t most = 0;
@@ -250,7 +254,97 @@ mla_status build_plan(const int32_t* seq_lens, const int32_t* q_lens, int32_t B,
     }
     return true;
   };
-  if (kind.tree) {
+  // Rows dealt out one after another, each to the range with least so far: a row
+  // that passes `budget` goes on in the next range, and no piece under `crumb` tiles
+  // is cut off it.  Neighbouring rows, a sequence's, are then read at the same time,
+  // from DRAM once, and few are cut (against contiguous ranges: 768 rows over 8 204
+  // tokens 1 183 -> 1 131 us, 1 086 over 200 to 20 000 tokens 2 694 -> 2 331, 254 over
+  // 1 024 to 4 096 167 -> 151).  Returns the cost of what finds no place, 0 when all
+  // is dealt; take(row, range, first, last).
+  auto deal = [&](int64_t ranges, int64_t budget, auto take) {
+    const int64_t crumb = std::min(std::max(budget / 4, kMinTilesPerCluster), kTreeCrumb);
+    std::vector<std::pair<int64_t, int32_t>> open;  // a heap, least first: cost so far, range
+    for (int32_t c = 0; c < ranges; ++c) open.push_back({0, c});
+    auto sink = [&] {  // the first one has grown
+      const size_t n = open.size();
+      const auto x = open[0];
+      size_t i = 0;
+      for (size_t k = 1; k < n; k = 2 * i + 1) {
+        if (k + 1 < n && open[k + 1] < open[k]) ++k;
+        if (!(open[k] < x)) break;
+        open[i] = open[k];
+        i = k;
+      }
+      open[i] = x;
+    };
+    for (int64_t r = 0; r < T; ++r) {
+      for (int64_t at = 0, n = rows[r].npages; at < n;) {
+        if (open.empty()) {
+          int64_t rest = n - at + kTreeRowTiles;
+          for (int64_t k = r + 1; k < T; ++k) rest += rows[k].npages + kTreeRowTiles;
+          return rest;
+        }
+        int64_t t = std::min(budget - open[0].first - kTreeRowTiles, n - at);
+        if (t < std::min(crumb, n - at)) {
+          open[0] = open.back();
+          open.pop_back();
+        } else {
+          if (n - at - t < kMinTilesPerCluster) t = n - at;  // no crumb stays behind
+          take((int32_t)r, open[0].second, at, at + t);
+          at += t;
+          open[0].first += t + kTreeRowTiles;
+        }
+        if (!open.empty()) sink();
+      }
+    }
+    return (int64_t)0;
+  };
+  // What a plan costs beside its longest range: partial results and the merge.
+  struct Merge {
+    int64_t partials = 0, most = 0, run = 0;
+    int32_t of = -1;
+    void add(int32_t row) {  // the pieces of a row come one after another
+      run = row == of ? run + 1 : 1;
+      of = row;
+      partials += run == 1 ? 0 : run == 2 ? 2 : 1;
+      most = std::max(most, run);
+    }
+    int64_t cost(int64_t budget) const { return 64 * budget + kTreePartial * partials + (most > 1 ? kTreePiece * most : 0); }
+  };
+  if (kind.tree && T >= num_clusters) {
+    struct Dealt {
+      int32_t row, range;
+      int64_t pb, pe;
+    };
+    std::vector<Dealt> best, now;
+    int64_t best_cost = INT64_MAX, best_ranges = 0;
+    // All ranges, or fewer that take whole rows alike.
+    const int64_t each = (T + num_clusters - 1) / num_clusters, even = (T + each - 1) / each;
+    for (int64_t ranges = num_clusters; ranges; ranges = ranges > even ? even : 0) {
+      int64_t budget = (total + kTreeRowTiles * T + ranges - 1) / ranges, rest;
+      Merge m;
+      while ((rest = (now.clear(), m = {}, deal(ranges, budget, [&](int32_t row, int32_t c, int64_t pb, int64_t pe) {
+                now.push_back({row, c, pb, pe});
+                m.add(row);
+              }))) > 0)
+        budget += 1 + std::min(rest / ranges, budget / 256);
+      if (m.cost(budget) < best_cost) {
+        best_cost = m.cost(budget);
+        best_ranges = ranges;
+        best.swap(now);
+      }
+    }
+    // A range's pieces are walked last first: the ones cut short then come at the
+    // start, and the ranges do not change rows all at the same time (254 rows 158 ->
+    // 153 us, 256 over 4 096 tokens 207 -> 201).
+    std::vector<std::vector<const Dealt*>> of(best_ranges);
+    for (const Dealt& d : best) of[d.range].push_back(&d);
+    for (const auto& range : of) {
+      if (range.empty()) continue;
+      seg_off.push_back((int32_t)segs.size());
+      for (auto d = range.rbegin(); d != range.rend(); ++d) piece((*d)->row, (*d)->pb, (*d)->pe);
+    }
+  } else if (kind.tree) {
     std::vector<int32_t> order;
     order.reserve(rows.size());
     const int32_t lanes = tree_lanes(seq_lens, q_lens, B, num_clusters);
@@ -260,23 +354,15 @@ mla_status build_plan(const int32_t* seq_lens, const int32_t* q_lens, int32_t B,
         for (int64_t i = (int64_t)q_lens[b] * lane / lanes; i < (int64_t)q_lens[b] * (lane + 1) / lanes; ++i)
           order.push_back(r + (int32_t)i);
     }
-    // Ranges: all of them, or for few rows as many as pay: each further piece of
-    // a row is a partial result to write, read and merge.
+    // As many ranges as pay: each further piece of a row is a partial result to
+    // write, read and merge.
     int64_t best_ranges = 0, best_budget = 0, best_cost = INT64_MAX;
-    const bool few = (int64_t)rows.size() < 2 * (int64_t)num_clusters;
-    for (int64_t ranges = num_clusters; total > 0 && ranges >= 1; ranges = few ? std::min(ranges - 1, ranges * 7 / 8) : 0) {
-      int64_t budget = (total + kTreeRowTiles * std::max<int64_t>(T, ranges) + ranges - 1) / ranges, partials, most, run;
-      int32_t of = -1;
-      auto count = [&](int32_t rr, int64_t, int64_t) {
-        run = rr == of ? run + 1 : 1;
-        of = rr;
-        partials += run == 1 ? 0 : run == 2 ? 2 : 1;
-        most = std::max(most, run);
-      };
-      while (partials = most = run = 0, of = -1, !fill(order, ranges, budget, [] {}, count)) budget += 1 + budget / 1024;
-      const int64_t cost = 64 * budget + kTreePartial * partials + (most > 1 ? kTreePiece * most : 0);
-      if (cost < best_cost) {
-        best_cost = cost;
+    for (int64_t ranges = num_clusters; total > 0 && ranges >= 1; ranges = std::min(ranges - 1, ranges * 7 / 8)) {
+      int64_t budget = (total + kTreeRowTiles * std::max<int64_t>(T, ranges) + ranges - 1) / ranges;
+      Merge m;
+      while (m = {}, !fill(order, ranges, budget, [] {}, [&](int32_t rr, int64_t, int64_t) { m.add(rr); })) budget += 1 + budget / 1024;
+      if (m.cost(budget) < best_cost) {
+        best_cost = m.cost(budget);
         best_ranges = ranges;
         best_budget = budget;
       }
@@ -310,14 +396,18 @@ mla_status build_plan(const int32_t* seq_lens, const int32_t* q_lens, int32_t B,
   std::vector<int32_t> split;  // {row, slot_begin, n, 0}
   int32_t nslots = 0;
   {
+    std::vector<Seg*> cut_up;
+    for (auto& s : segs)
+      if (row_pieces[s.row] > 1) cut_up.push_back(&s);
+    if (kind.tree)  // dealt pieces of a row lie apart
+      std::sort(cut_up.begin(), cut_up.end(), [](const Seg* x, const Seg* y) { return x->row != y->row ? x->row < y->row : x->pb < y->pb; });
     int32_t last_row = -1;
-    for (auto& s : segs) {
-      if (row_pieces[s.row] < 2) continue;
-      if (s.row != last_row) {
-        split.insert(split.end(), {s.row, nslots, row_pieces[s.row], 0});
-        last_row = s.row;
+    for (Seg* s : cut_up) {
+      if (s->row != last_row) {
+        split.insert(split.end(), {s->row, nslots, row_pieces[s->row], 0});
+        last_row = s->row;
       }
-      s.slot = nslots++;
+      s->slot = nslots++;
     }
   }
   const int64_t nsplit = (int64_t)split.size() / mla::kSplitWords;
