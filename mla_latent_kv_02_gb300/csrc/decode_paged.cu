@@ -339,11 +339,11 @@ __device__ __forceinline__ uint32_t as_u32(__half2 h) { return *reinterpret_cast
 // warpgroup of its own (the row warps) loads the next row's queries and stores
 // the finished row: neither sits on the softmax's way any more (when that was
 // built, 64 nodes of 16 sequences of 512 tokens 204 -> 194 us, 12 nodes of 64
-// sequences of 8 192 tokens 1 415 -> 1 375; the first is 168 now).  What is left of
+// sequences of 8 192 tokens 1 415 -> 1 375; the first is 159 now).  What is left of
 // a row's change is the SM's store rate, 32 bytes a cycle, and the queries' nine
 // rounds into TMEM: about two tiles' time.
-// Measured: 254 rows of 1 024 to 4 096 tokens 168 us = 0.64 of the tensor peak on
-// the tokens seen; 768 rows of 8 204 tokens 1 198 us at full clocks = 0.76, 1 290
+// Measured: 254 rows of 1 024 to 4 096 tokens 152 us = 0.70 of the tensor peak on
+// the tokens seen; 768 rows of 8 204 tokens 1 130 us at full clocks = 0.81, 1 192
 // back to back under the power cap; 8 rows of 1 032 tokens 17.4 us, latency.
 //
 // kF16 without kF8: the pages are f16 rows unpacked from the FP8 cache
