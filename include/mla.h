@@ -819,8 +819,9 @@ typedef struct mla_tree_info {
 /*
  * The split schedule of mla_decode_plan_host for trees: the same arguments
  * (q_lens[b] nodes, at most MLA_TREE_MAX_NODES, else MLA_ERR_UNSUPPORTED) and
- * errors, in a buffer of mla_tree_plan_bytes.  It depends on the lengths alone,
- * not on the trees' shapes.  A plan of one kind passed to the other kind's
+ * errors, in a buffer of mla_tree_plan_bytes; from as many rows as clusters on,
+ * whole rows are dealt out and only the last ones cut.  It depends on the lengths
+ * alone, not on the trees' shapes.  A plan of one kind passed to the other kind's
  * decode is MLA_ERR_INVALID_ARG.
  */
 mla_status mla_tree_plan_bytes(int32_t T, int32_t num_clusters, size_t* bytes);
