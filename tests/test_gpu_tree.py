@@ -673,6 +673,37 @@ def test_copy_pages_of_more_than_a_launch(api):
     assert torch.equal(raw, want)
 
 
+@pytest.mark.parametrize("pairs", [3, 300])
+def test_copies_and_compaction_are_captured(api, pairs):
+    """A graph on a side stream, replayed after the caches, the accepted nodes and the lists of pages have changed."""
+    kv = torch.randn((2, 2 * pairs + 2, 64, 576), device="cuda").to(torch.bfloat16)
+    src, dst = np.arange(pairs, dtype=np.int32), np.arange(pairs, 2 * pairs, dtype=np.int32)
+    t = tree(3, 9)
+    m = torch.from_numpy(masks([t], 1)).cuda()
+    table = torch.tensor([[2 * pairs, 2 * pairs + 1]], dtype=torch.int32, device="cuda")
+    q, seq, acc, new, err = i32([0, 9]), i32([69]), i32([8]), i32([0]), word()
+    side, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph, stream=side):
+        api.mla_copy_pages(kv, src, dst)
+        api.mla_tree_compact(kv, table, m, q, seq, acc, new, err)
+    src[:], dst[:] = 0, 1                                    # they were read when the call was made
+    for step in range(2):
+        kv.normal_()
+        last = 8 if step == 0 else 5
+        acc.fill_(last)
+        want = kv.clone()
+        want[:, pairs:2 * pairs] = want[:, :pairs]
+        keep = path(t, last)
+        for r, k in enumerate(sorted(keep)):
+            at, to = 60 + k, 60 + r
+            want[:, 2 * pairs + to // 64, to % 64] = want[:, 2 * pairs + at // 64, at % 64].clone()
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert int(err.item()) == 0 and new.tolist() == [60 + len(keep)] and torch.equal(kv, want)
+
+
 def test_copy_pages_refusals(api):
     kv = torch.zeros((2, 8, 64, 576), dtype=torch.bfloat16, device="cuda")
     for src, dst, error in (([0, 1], [2, 2], api.MlaError), ([0, 1], [1, 2], api.MlaError), ([8], [0], api.MlaError),
