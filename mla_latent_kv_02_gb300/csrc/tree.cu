@@ -182,6 +182,7 @@ __global__ void __launch_bounds__(256) compact_kernel(const TreeCompactArgs a, i
 __global__ void __launch_bounds__(256) unpack_kernel(const TreeUnpackArgs a) {
   const int t = threadIdx.x;
   const int32_t page = blockIdx.x;
+  dev::grid_dependency_wait();
   if (t == 0) dev::grid_launch_dependents();  // the decode may get ready; it waits before it reads a page
   int at = 0;                                 // the last tree whose first page is not behind this one
   for (int n = a.num_trees; n > 1;) {
@@ -266,8 +267,7 @@ cudaError_t run_compact(const TreeCompactArgs& a, cudaStream_t stream) {
 }  // namespace tree
 
 cudaError_t launch_tree_unpack(const TreeUnpackArgs& args, cudaStream_t stream) {
-  tree::unpack_kernel<<<args.out_pages, 256, 0, stream>>>(args);
-  return cudaGetLastError();
+  return launch_dependent(tree::unpack_kernel, dim3(args.out_pages), 256, 0, true, stream, args);
 }
 
 cudaError_t launch_tree_layout(const TreeLayoutArgs& args, cudaStream_t stream) {

@@ -306,6 +306,63 @@ def test_a_captured_workspace_outlives_the_next(api):
         api.mla_tree_plan(cache.n, [q], into=api.mla_decode_plan(cache.n, [q]))
 
 
+@pytest.mark.parametrize("captured", [False, True])
+@pytest.mark.parametrize("kind, n0, q", [("bf16", 200, 6), ("bf16", 3000, 100), ("fp8", 200, 6), ("fp8", 2000, 48)])
+def test_inputs_written_just_before(api, kind, n0, q, captured):
+    """The launch does not wait for the kernels before it, the kernel does: inputs written on the stream right before
+    each call, by kernels and copies, on it and on another that it joins; the output taken right after."""
+    cache = Cache(api, [n0 + q], kind, 61)
+    m = torch.from_numpy(masks([tree(0, q)], 1 if q <= 64 else 2)).cuda()
+    plan, rounds = api.mla_tree_plan(cache.n, [q]), 4
+    qs = [queries(q, 62 + i) for i in range(rounds)]
+    tables = [cache.table.clone() for _ in range(rounds)]
+    for i in range(1, rounds):                               # the first pages in another order
+        tables[i][0, :3] = tables[0][0, :3].roll(i)
+    want = []
+    for (a, r), t in zip(qs, tables):
+        cache.table = t
+        want.append(decode(api, cache, a, r, m, plan)[:2])
+        torch.cuda.synchronize()
+    cache.table = tables[0].clone()
+    a, r, mm = (torch.zeros_like(x) for x in (*qs[0], m))
+    o, lse, err = torch.empty_like(want[0][0]), torch.empty_like(want[0][1]), word()
+    got = [(torch.zeros_like(o), torch.zeros_like(lse)) for _ in range(rounds)]
+    busy = torch.randn((2048, 2048), device="cuda")
+    main, other = torch.cuda.Stream(), torch.cuda.Stream()
+
+    def work():
+        for i in range(rounds):
+            other.wait_stream(main)
+            with torch.cuda.stream(other):
+                busy.mul_(1.0)
+                r.copy_(qs[i][1])
+            torch.mul(m, 1, out=mm)
+            cache.table.copy_(tables[i])
+            busy.mul_(1.0)
+            main.wait_stream(other)
+            torch.mul(qs[i][0], 1, out=a)
+            decode(api, cache, a, r, mm, plan, o=o, lse=lse, err=err)
+            got[i][0].copy_(o)
+            got[i][1].copy_(lse)
+            a.zero_()
+
+    torch.cuda.synchronize()
+    if captured:
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=main):
+            work()
+        for _ in range(3):
+            graph.replay()
+    else:
+        with torch.cuda.stream(main):
+            for _ in range(3):
+                work()
+    torch.cuda.synchronize()
+    assert int(err.item()) == 0
+    for (x, y), (wx, wy) in zip(got, want):
+        assert torch.equal(x, wx) and torch.equal(y, wy)
+
+
 @pytest.mark.parametrize("kind", ["bf16", "fp8"])
 def test_wider_masks_and_tables(api, kind):
     """Words that no tree needs, rows and columns of the table past the batch: the same bits, whatever they hold."""
