@@ -843,7 +843,8 @@ def _copy_pages(call, cache, src, dst, stream, dev: int) -> None:
     src, dst = _i32(src, "src"), _i32(dst, "dst")
     if src.ndim != 1 or src.shape != dst.shape:
         raise ValueError(f"src and dst must be lists of one length, got shapes {src.shape} and {dst.shape}")
-    _check(call(*cache, src.ctypes.data, dst.ctypes.data, src.size, _on(stream, dev)))
+    # as bytes: an array's address takes ctypes longer than the copy does
+    _check(call(*cache, src.tobytes(), dst.tobytes(), src.size, _on(stream, dev)))
 
 
 def mla_copy_pages(kv_cache, src, dst, stream=None) -> None:

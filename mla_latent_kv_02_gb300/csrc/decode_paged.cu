@@ -344,7 +344,7 @@ __device__ __forceinline__ uint32_t as_u32(__half2 h) { return *reinterpret_cast
 // rounds into TMEM: about two tiles' time.
 // Measured: 254 rows of 1 024 to 4 096 tokens 152 us = 0.70 of the tensor peak on
 // the tokens seen; 768 rows of 8 204 tokens 1 130 us at full clocks = 0.81, 1 192
-// back to back under the power cap; 8 rows of 1 032 tokens 17.4 us, latency.
+// back to back under the power cap; 8 rows of 1 032 tokens 17.2 us, latency.
 //
 // kF16 without kF8: the pages are f16 rows unpacked from the FP8 cache
 // (unpack_kernel, tree.cu), one after another from the segment's first page;
