@@ -851,7 +851,10 @@ mla_status mla_tree_workspace_size(const mla_tree_info* info, int32_t fp8, size_
  * nothing (n0 = 0 and no bit set) has o_lat = 0 and lse = -infinity.  Of the
  * pages that are read, slots that a row does not see may hold anything,
  * infinities and NaN among them; over the FP8 cache their scales are not judged.
- * What is held in 16 bits is as for the windowed decode.
+ * What is held in 16 bits is as for the windowed decode.  The launch does not
+ * wait for the kernel before it on the stream, the kernel on the device does; a
+ * kernel of the caller's that is launched that way has to wait for its own
+ * predecessors, as is usual for such launches.
  */
 mla_status mla_decode_tree(const void* q_abs, const void* q_r, const void* kv_cache, int64_t num_pages,
                            const int32_t* block_table, int32_t max_pages, const uint64_t* masks, int32_t words,

@@ -260,11 +260,16 @@ mla_status build_plan(const int32_t* seq_lens, const int32_t* q_lens, int32_t B,
   // from DRAM once, and few are cut (against contiguous ranges: 768 rows over 8 204
   // tokens 1 183 -> 1 131 us, 1 086 over 200 to 20 000 tokens 2 694 -> 2 331, 254 over
   // 1 024 to 4 096 167 -> 151).  Returns the cost of what finds no place, 0 when all
-  // is dealt; take(row, range, first, last).
-  auto deal = [&](int64_t ranges, int64_t budget, auto take) {
-    const int64_t crumb = std::min(std::max(budget / 4, kMinTilesPerCluster), kTreeCrumb);
+  // is dealt; take(row, range, first, last).  Begins at `from` and leaves there the
+  // first row that was not taken whole: up to it a larger budget changes nothing.
+  struct Deal {
     std::vector<std::pair<int64_t, int32_t>> open;  // a heap, least first: cost so far, range
-    for (int32_t c = 0; c < ranges; ++c) open.push_back({0, c});
+    int64_t row = 0;
+  };
+  auto deal = [&](Deal& from, int64_t budget, auto take) {
+    const int64_t crumb = std::min(std::max(budget / 4, kMinTilesPerCluster), kTreeCrumb);
+    auto open = from.open;
+    bool whole = true;
     auto sink = [&] {  // the first one has grown
       const size_t n = open.size();
       const auto x = open[0];
@@ -277,7 +282,7 @@ mla_status build_plan(const int32_t* seq_lens, const int32_t* q_lens, int32_t B,
       }
       open[i] = x;
     };
-    for (int64_t r = 0; r < T; ++r) {
+    for (int64_t r = from.row; r < T; ++r) {
       for (int64_t at = 0, n = rows[r].npages; at < n;) {
         if (open.empty()) {
           int64_t rest = n - at + kTreeRowTiles;
@@ -285,6 +290,10 @@ mla_status build_plan(const int32_t* seq_lens, const int32_t* q_lens, int32_t B,
           return rest;
         }
         int64_t t = std::min(budget - open[0].first - kTreeRowTiles, n - at);
+        if (whole && t < n) {
+          whole = false;
+          from = {open, r};
+        }
         if (t < std::min(crumb, n - at)) {
           open[0] = open.back();
           open.pop_back();
@@ -322,8 +331,11 @@ mla_status build_plan(const int32_t* seq_lens, const int32_t* q_lens, int32_t B,
     const int64_t each = (T + num_clusters - 1) / num_clusters, even = (T + each - 1) / each;
     for (int64_t ranges = num_clusters; ranges; ranges = ranges > even ? even : 0) {
       int64_t budget = (total + kTreeRowTiles * T + ranges - 1) / ranges, rest;
+      Deal from;
+      for (int32_t c = 0; c < ranges; ++c) from.open.push_back({0, c});
       Merge m;
-      while ((rest = (now.clear(), m = {}, deal(ranges, budget, [&](int32_t row, int32_t c, int64_t pb, int64_t pe) {
+      now.clear();
+      while ((rest = (now.resize(from.row), m = {}, deal(from, budget, [&](int32_t row, int32_t c, int64_t pb, int64_t pe) {
                 now.push_back({row, c, pb, pe});
                 m.add(row);
               }))) > 0)
