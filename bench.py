@@ -53,7 +53,7 @@ def workload_stats(case):
 # the sha1 prefix of the decode kernel source it was taken on and the
 # workload.  Captured at half batch and scaled by the query rows (see
 # profiles/decode_kernel_mtp2_b32_ncu.md); any other source reads as null.
-MEASURED_TRAFFIC = {("14f10aa13792", 2): 657.49e6}
+MEASURED_TRAFFIC = {("92270284c471", 2): 658.57e6}
 
 
 def decode_traffic(workload: int, batch):

@@ -340,11 +340,12 @@ __device__ __forceinline__ uint32_t as_u32(__half2 h) { return *reinterpret_cast
 // the finished row: neither sits on the softmax's way any more (when that was
 // built, 64 nodes of 16 sequences of 512 tokens 204 -> 194 us, 12 nodes of 64
 // sequences of 8 192 tokens 1 415 -> 1 375; the first is 159 now).  What is left of
-// a row's change is the SM's store rate, 32 bytes a cycle, and the queries' nine
-// rounds into TMEM: about two tiles' time.
-// Measured: 254 rows of 1 024 to 4 096 tokens 152 us = 0.70 of the tensor peak on
-// the tokens seen; 768 rows of 8 204 tokens 1 130 us at full clocks = 0.81, 1 192
-// back to back under the power cap; 8 rows of 1 032 tokens 17.2 us, latency.
+// a row's change, three to four tiles' time: the queries' nine rounds into TMEM, 4 300
+// cycles of which the next QK^T waits for most, and the row's way out (an SM sends 32
+// bytes a cycle at most, the score exchange included).
+// Measured: 254 rows of 1 024 to 4 096 tokens 149 us = 0.72 of the tensor peak on
+// the tokens seen; 768 rows of 8 204 tokens 1 119 us at full clocks = 0.82, 1 185
+// back to back under the power cap; 8 rows of 1 032 tokens 16.5 us, latency.
 //
 // kF16 without kF8: the pages are f16 rows unpacked from the FP8 cache
 // (unpack_kernel, tree.cu), one after another from the segment's first page;
@@ -1212,40 +1213,44 @@ __device__ __forceinline__ void decode_body(const CUtensorMap& kv_map, const CUt
       const size_t row0 = (size_t)a.segs[8 * s] * kH + q4 * 32 + wr;
       const uint4* lat = reinterpret_cast<const uint4*>(a.q_abs + row0 * kDC + rank * 256) + wk;
       const uint4* rp = reinterpret_cast<const uint4*>(a.q_r + row0 * kDR + rank * kRopeHalf) + wk;
-      constexpr int kAhead = 4;  // rounds of 64 bytes a row in flight: eight latent, one RoPE
+      constexpr int kAhead = 3;  // rounds of 64 bytes a row in flight: eight latent, one RoPE
       uint4 v[kAhead][4];
-      auto fetch = [&](int k) {
+      auto fetch = [&](int k, uint4 (&to)[4]) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) v[k % kAhead][i] = k < 8 ? __ldg(lat + 4 * k + i * kDC) : __ldg(rp + i * kDR);
+        for (int i = 0; i < 4; ++i) to[i] = k < 8 ? __ldg(lat + 4 * k + i * kDC) : __ldg(rp + i * kDR);
       };
 #pragma unroll
-      for (int k = 0; k < kAhead; ++k) fetch(k);
+      for (int k = 0; k < kAhead; ++k) fetch(k, v[k]);
       if (s > s_begin) {
         const bool w = wait_phase<false, true>(BAR(B_Q_FREE), phase, err, abort_flag, a.wait_limit, a.wait_every);
         if (!__all_sync(0xffffffffu, w)) return false;
         tc_fence_after();
       }
+      // Rolled: this code runs once a row, and a third of it is a third to fetch.
+#pragma unroll 1
+      for (int k0 = 0; k0 < 9; k0 += kAhead) {
 #pragma unroll
-      for (int k = 0; k < 9; ++k) {
+        for (int u = 0; u < kAhead; ++u) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) st_shared_v4(at(8 * i + wr, wk), v[k % kAhead][i].x, v[k % kAhead][i].y, v[k % kAhead][i].z, v[k % kAhead][i].w);
-        __syncwarp();
-        if (k + kAhead < 9) fetch(k + kAhead);
-        uint32_t r[16];
+          for (int i = 0; i < 4; ++i) st_shared_v4(at(8 * i + wr, wk), v[u][i].x, v[u][i].y, v[u][i].z, v[u][i].w);
+          __syncwarp();
+          if (k0 + kAhead < 9) fetch(k0 + kAhead + u, v[u]);
+          uint32_t r[16];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const float4 x = ld_shared_v4(at(lane, j));
-          r[4 * j] = __float_as_uint(x.x);
-          r[4 * j + 1] = __float_as_uint(x.y);
-          r[4 * j + 2] = __float_as_uint(x.z);
-          r[4 * j + 3] = __float_as_uint(x.w);
+          for (int j = 0; j < 4; ++j) {
+            const float4 x = ld_shared_v4(at(lane, j));
+            r[4 * j] = __float_as_uint(x.x);
+            r[4 * j + 1] = __float_as_uint(x.y);
+            r[4 * j + 2] = __float_as_uint(x.z);
+            r[4 * j + 3] = __float_as_uint(x.w);
+          }
+          __syncwarp();
+          if constexpr (kF16) {
+#pragma unroll
+            for (int j = 0; j < 16; ++j) r[j] = bf16x2_to_f16x2(r[j]);
+          }
+          tmem_st16(tl + kColQ + 16 * (k0 + u), r);
         }
-        __syncwarp();
-        if constexpr (kF16) {
-#pragma unroll
-          for (int j = 0; j < 16; ++j) r[j] = bf16x2_to_f16x2(r[j]);
-        }
-        tmem_st16(tl + kColQ + 16 * k, r);
       }
       tmem_st_wait();
       tc_fence_before();
@@ -1264,41 +1269,49 @@ __device__ __forceinline__ void decode_body(const CUtensorMap& kv_map, const CUt
       const float lt = __uint_as_float(tmem_ld1_sync(tl + kColSum));
       const float inv = lt == 0.f ? 0.f : 1.f / lt;
       const uint64_t keep = l2_policy_evict_last();  // partials are read once, by the combine right after
-      uint32_t o[32];
-      tmem_ld32_sync(tl + kColO, o);
+      if (slot < 0) {
+        // 64 columns at a time, as bf16 at once: half as many waits for TMEM, and O is
+        // free with a quarter of the row still to store (254 rows 152 -> 149 us).
+        uint16_t* dst = a.o_lat + ((size_t)row * kH + q4 * 32 + wr) * kDC + rank * 256 + wk * 8;
 #pragma unroll 1
-      for (int c = 0; c < 256; c += 32) {
-        uint32_t x[32];
+        for (int c = 0; c < 256; c += 64) {
+          uint32_t o[64], y[32];
+          tmem_ld64_sync(tl + kColO + c, o);
 #pragma unroll
-        for (int i = 0; i < 32; ++i) x[i] = __float_as_uint(__uint_as_float(o[i]) * inv);
-        if (c + 32 < 256) {
-          tmem_ld32_sync(tl + kColO + c + 32, o);
-        } else {
-          tc_fence_before();
-          mbar_arrive(BAR(B_O_FREE));
-        }
-        if (slot < 0) {
-          uint16_t* dst = a.o_lat + ((size_t)row * kH + q4 * 32 + wr) * kDC + rank * 256 + c + wk * 8;
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            uint32_t y[4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) y[j] = pack_bf16x2(__uint_as_float(x[8 * k + 2 * j]), __uint_as_float(x[8 * k + 2 * j + 1]));
-            st_shared_v4(at(lane, k), y[0], y[1], y[2], y[3]);
+          for (int i = 0; i < 32; ++i) y[i] = pack_bf16x2(__uint_as_float(o[2 * i]) * inv, __uint_as_float(o[2 * i + 1]) * inv);
+          if (c == 192) {
+            tc_fence_before();
+            mbar_arrive(BAR(B_O_FREE));
           }
-          __syncwarp();
-#pragma unroll
-          for (int i = 0; i < 4; ++i) *reinterpret_cast<float4*>(dst + (size_t)(8 * i) * kDC) = ld_shared_v4(at(8 * i + wr, wk));
-          __syncwarp();
-        } else {
-          float* dst = a.part_o + ((size_t)slot * kH + q4 * 32 + wr) * kDC + rank * 256 + c + wk * 4;
 #pragma unroll
           for (int hf = 0; hf < 2; ++hf) {
 #pragma unroll
-            for (int k = 0; k < 4; ++k) st_shared_v4(at(lane, k), x[16 * hf + 4 * k], x[16 * hf + 4 * k + 1], x[16 * hf + 4 * k + 2], x[16 * hf + 4 * k + 3]);
+            for (int k = 0; k < 4; ++k) st_shared_v4(at(lane, k), y[16 * hf + 4 * k], y[16 * hf + 4 * k + 1], y[16 * hf + 4 * k + 2], y[16 * hf + 4 * k + 3]);
             __syncwarp();
 #pragma unroll
-            for (int i = 0; i < 4; ++i) st_global_v4_hint(dst + (size_t)(8 * i) * kDC + 16 * hf, ld_shared_v4(at(8 * i + wr, wk)), keep);
+            for (int i = 0; i < 4; ++i) *reinterpret_cast<float4*>(dst + (size_t)(8 * i) * kDC + c + 32 * hf) = ld_shared_v4(at(8 * i + wr, wk));
+            __syncwarp();
+          }
+        }
+      } else {
+        float* dst = a.part_o + ((size_t)slot * kH + q4 * 32 + wr) * kDC + rank * 256 + wk * 4;
+#pragma unroll 1
+        for (int c = 0; c < 256; c += 32) {
+          uint32_t o[32];
+          tmem_ld32_sync(tl + kColO + c, o);
+          if (c == 224) {
+            tc_fence_before();
+            mbar_arrive(BAR(B_O_FREE));
+          }
+#pragma unroll
+          for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * inv);
+#pragma unroll
+          for (int hf = 0; hf < 2; ++hf) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) st_shared_v4(at(lane, k), o[16 * hf + 4 * k], o[16 * hf + 4 * k + 1], o[16 * hf + 4 * k + 2], o[16 * hf + 4 * k + 3]);
+            __syncwarp();
+#pragma unroll
+            for (int i = 0; i < 4; ++i) st_global_v4_hint(dst + (size_t)(8 * i) * kDC + c + 16 * hf, ld_shared_v4(at(8 * i + wr, wk)), keep);
             __syncwarp();
           }
         }
