@@ -178,7 +178,7 @@ __global__ void __launch_bounds__(256) compact_kernel(const TreeCompactArgs a, i
 // of 1 032 tokens and one of 262 144: 2 023 -> 1 043 us).  A token's scale outside
 // the f16 range counts only where a row sees it: every row sees the tokens before
 // the tree, and the nodes' masks are asked in that case alone.  Rows past the
-// sequence's end become zeros.  Moves 1.8 KB a token: 12.9 us for 32 832 tokens with cold caches, 21 MB from HBM and 38 into L2.
+// sequence's end become zeros.  Moves 1.8 KB a token: 14 us for 32 832 tokens with cold caches, 21 MB from HBM and 38 into L2.
 __global__ void __launch_bounds__(256) unpack_kernel(const TreeUnpackArgs a) {
   const int t = threadIdx.x;
   const int32_t page = blockIdx.x;
