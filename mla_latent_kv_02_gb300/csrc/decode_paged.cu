@@ -58,6 +58,7 @@
 #include <cmath>
 #include <cstdint>
 
+#include "exchange.h"
 #include "fp8.cuh"
 #include "internal.h"
 #include "ptx.cuh"
@@ -72,27 +73,10 @@ constexpr int kChunk = 64;                                // elements in one 128
 constexpr int kChunkBytes = kPage * kChunk * 2;           // [64 tokens x 64] bf16 = 8 KB
 constexpr int kRopeHalf = 32;                             // RoPE dims per CTA
 constexpr int kRopeBytes = kPage * kRopeHalf * 2;         // [64 tokens x 32] bf16 = 4 KB, 64-byte rows
-constexpr int kXBytes = kH * kPage * 2;                   // one CTA's fp16 partial S (16 KB)
 // Softmax: two warpgroups take alternate tiles whole (thread = head row).
 constexpr int kSWarps = 8;
 constexpr int kWords = kPage / 2;                         // fp16x2 words of a row's 64 scores
-constexpr int kXWarp = kXBytes / 4;                       // a warp's share of an exchange buffer (4 KB)
-// The scores of a tile cross in parts, each with a barrier of its own.  In two,
-// 32 tokens each, the second part's way (an SM sends about 20 bytes a cycle) is
-// under the first part's arithmetic: 64 unpacked rows of 32 832 tokens 392 -> 369
-// us, 768 rows of 8 204 tokens 1 259 -> 1 229.  Over the FP8 cache, where the
-// converters bind and leave fewer registers, one part is faster (320 and 344 us on
-// 128 rows of 8 194 tokens).
-template <int kParts>
-struct Exchange {
-  static constexpr int kBytes = kXBytes / kParts;         // [128 heads x 64 / kParts tokens] fp16
-  static constexpr int kRow = kPage * 2 / kParts;         // a row's scores
-  static constexpr int kWarp = 32 * kRow;                 // one warp's 32 rows
-  static constexpr int kPieces = kRow / 16;               // 16-byte pieces of a row, swizzled
-  static constexpr int kWords2 = kWords / kParts;         // fp16x2 words of a row
-  static __device__ __forceinline__ uint32_t swizzle(int h) { return kParts == 1 ? (uint32_t)(h & 7) : (uint32_t)((h >> 1) & 3); }
-  static_assert(kParts == 1 || kParts == 2, "the swizzles above");
-};
+static_assert(kXHeads == kH && kXTokens == kPage, "the exchange buffers");
 constexpr int kXBufs = 4;                                 // exchange ring depth
 constexpr int kXLead = kXBufs - 2;                        // staging buffer offset
 static_assert(kXLead >= 1 && kXLead <= kXBufs - 2, "the exchange ring needs two tiles between staging and reuse");
@@ -838,10 +822,6 @@ __device__ __forceinline__ void decode_body(const CUtensorMap& kv_map, const CUt
     const int q4 = warp & 3;                 // TMEM lane quarter this warp may access
     const int h = q4 * 32 + lane;            // head row = TMEM lane
     const uint32_t tl = tmem + ((uint32_t)(q4 * 32) << 16);
-    const uint32_t swz = X::swizzle(h);  // 16-byte piece k of a row sits at k ^ swz
-    const uint32_t row_off = (uint32_t)(h * X::kRow);
-    const uint32_t part_off = (uint32_t)(q4 * X::kWarp);
-    const uint32_t warp_off = (uint32_t)(q4 * kXWarp);
     const bool wg_leader = ((sw & 3) == 0 && lane == 0);
     // Scores cross the pair and are compared unscaled; the scale (times
     // log2 e) enters once, in the exponent.
@@ -934,7 +914,7 @@ __device__ __forceinline__ void decode_body(const CUtensorMap& kv_map, const CUt
 #pragma unroll
         for (int k = 0; k < X::kPieces; ++k) {
           const int j = p * X::kWords2 + 4 * k;
-          st_shared_v4(stage + p * X::kBytes + row_off + (((uint32_t)k ^ swz) << 4), own[j], own[j + 1], own[j + 2], own[j + 3]);
+          st_shared_v4(stage + X::scores(h, p, k), own[j], own[j + 1], own[j + 2], own[j + 3]);
         }
         fence_proxy_async_smem();
         __syncwarp();
@@ -943,8 +923,7 @@ __device__ __forceinline__ void decode_body(const CUtensorMap& kv_map, const CUt
           peer_ready = true;
         }
         if (elect_one())
-          bulk_copy_to_peer(peer_x + (t % kXBufs) * kXBytes + p * X::kBytes + part_off,
-                            stage + p * X::kBytes + part_off, (uint32_t)X::kWarp,
+          bulk_copy_to_peer(peer_x + (t % kXBufs) * kXBytes + X::share(q4, p), stage + X::share(q4, p), (uint32_t)X::kWarp,
                             peer_bar + 8u * (p * kXBufs + t % kXBufs));
       }
       if (lane == 0) push_cnt[sw] += 1u;  // tiles this warp sent to the peer, every part
@@ -977,7 +956,7 @@ __device__ __forceinline__ void decode_body(const CUtensorMap& kv_map, const CUt
       // ---- add what the peer sent (fp16, unscaled), part by part; mask it (causal,
       //      length, window, tree) and take the row max
       const uint32_t xb = g % kXBufs;
-      const uint32_t recv = base + kOffX + xb * kXBytes + row_off;
+      const uint32_t recv = base + kOffX + xb * kXBytes;
       uint64_t seen = ~0ull;
       if constexpr (kMasked) {
         if (cf.edge()) seen = cf.visible();
@@ -999,7 +978,7 @@ __device__ __forceinline__ void decode_body(const CUtensorMap& kv_map, const CUt
         }
 #pragma unroll
         for (int k = 0; k < X::kPieces; ++k) {
-          const float4 v = ld_shared_v4(recv + kP * X::kBytes + (((uint32_t)k ^ swz) << 4));
+          const float4 v = ld_shared_v4(recv + X::scores(h, kP, k));
           own[kJ + 4 * k] = as_u32(__hadd2(as_h2(own[kJ + 4 * k]), as_h2(__float_as_uint(v.x))));
           own[kJ + 4 * k + 1] = as_u32(__hadd2(as_h2(own[kJ + 4 * k + 1]), as_h2(__float_as_uint(v.y))));
           own[kJ + 4 * k + 2] = as_u32(__hadd2(as_h2(own[kJ + 4 * k + 2]), as_h2(__float_as_uint(v.z))));
@@ -1126,19 +1105,16 @@ __device__ __forceinline__ void decode_body(const CUtensorMap& kv_map, const CUt
         const float inv = kTree && lt == 0.f ? 0.f : 1.f / lt;
         // The rows lie 1 KB (partials 2 KB) apart, so a thread's own stores
         // would write 32 lines an instruction: the warp's rows cross through
-        // its part of tile g's exchange buffer, 128 bytes of each row a round,
-        // and leave as whole lines.  That buffer is this warpgroup's until it
-        // stages tile g + 2: the scores in it are consumed, and the peer's
-        // next push into it (tile g + kXBufs) waits for tile g + 2.
-        const uint32_t ebuf = base + kOffX + (g % kXBufs) * kXBytes + warp_off;
+        // tile g's exchange buffer, 128 bytes of each row a round, and leave as
+        // whole lines.  The bytes are those that hold this warp's own scores:
+        // consumed, staged over by this warp alone (tile g + 2), and the peer's
+        // next push into them (tile g + kXBufs) waits for tile g + 2.
+        const uint32_t ebuf = base + kOffX + (g % kXBufs) * kXBytes;
         const uint32_t er = (uint32_t)lane >> 3, ep = (uint32_t)lane & 7u;
         auto put = [&](int k, uint32_t x, uint32_t y, uint32_t z, uint32_t w4) {
-          st_shared_v4(ebuf + (uint32_t)lane * 128u + (((uint32_t)k ^ ((uint32_t)lane & 7u)) << 4), x, y, z, w4);
+          st_shared_v4(ebuf + X::finished(q4, lane, k), x, y, z, w4);
         };
-        auto take = [&](int i) {
-          const uint32_t r = 4u * (uint32_t)i + er;
-          return ld_shared_v4(ebuf + r * 128u + ((ep ^ (r & 7u)) << 4));
-        };
+        auto take = [&](int i) { return ld_shared_v4(ebuf + X::finished(q4, 4u * (uint32_t)i + er, ep)); };
         if (slot < 0) {
           uint16_t* dst = a.o_lat + ((size_t)row * kH + q4 * 32 + er) * kDC + rank * 256 + ep * 8;
 #pragma unroll 1
