@@ -593,7 +593,8 @@ mla_status mla_decode_paged_fp8(const void* q_abs, const void* q_r, const void* 
  *     about e^(4 S 2^-11), S the largest |score| of the row after the scale:
  *     0.2 % of itself for S = 1, 14 % for S = 72 (1 000 before the default
  *     scale).  A score past 65 504 before the scale (4 700 after it) does not
- *     fit: the row's result is then wrong or NaN, and no error is set;
+ *     fit: the row's result is then wrong or NaN, and no error is set.  A scale
+ *     below 2^-24 ln 2 (4.2e-8) counts as that, here and in the chunks;
  *   - the weights 2^x: fp16, and bf16 on their way into P.V over the bf16 cache;
  *   - over the FP8 cache also q_abs, q_r and the cached RoPE keys, rounded from
  *     bf16 to f16: exact for magnitudes in [2^-17, 65 280], saturating at

@@ -472,6 +472,11 @@ mla_status build_plan(const int32_t* seq_lens, const int32_t* q_lens, int32_t B,
   return MLA_OK;
 }
 
+// The factor of an exponent of 2.  The kernels take it in fp16 too, where less than
+// 2^-24 would be 0, and 0 times the -infinity of a hidden score is no weight of 0;
+// raised to 2^-24 it moves no score that fits fp16 by more than 2^-8.
+float scale_log2(float scale) { return std::max((float)((double)scale * 1.4426950408889634), 0x1p-24f); }
+
 // A call whose body may run out of host memory: no exception passes.
 template <typename F>
 mla_status no_throw(F&& body) {
@@ -1217,7 +1222,7 @@ mla_status mla_prefill_attention(const void* q_c, const void* q_r, int32_t M, co
   mla::PrefillArgs a = {};
   a.nb = 1;
   a.seq[0] = {M, N, 0, 0};
-  a.scale_log2 = (float)((double)scale * 1.4426950408889634);
+  a.scale_log2 = scale_log2(scale);
   a.out = (uint16_t*)out;
   a.dev_err = dev_err;
   return prefill_attention_launch(q_c, q_r, M, rows, k_c, v_c, N, a, stream);
@@ -1304,7 +1309,7 @@ mla_status mla_prefill_decompress_batch(const void* q_c, const void* q_r, const 
   g.nb = nb;
   g.total = total;
   a.nb = nb;
-  a.scale_log2 = (float)((double)scale * 1.4426950408889634);
+  a.scale_log2 = scale_log2(scale);
   a.out = (uint16_t*)out;
   a.dev_err = dev_err;
   uint8_t* ws = (uint8_t*)workspace;
@@ -1438,7 +1443,7 @@ static mla_status prefill_window(const void* q_c, const void* q_r, const int32_t
   g.block_table = block_table;
   g.dev_err = dev_err;
   a.nb = nb;
-  a.scale_log2 = (float)((double)scale * 1.4426950408889634);
+  a.scale_log2 = scale_log2(scale);
   a.out = (uint16_t*)out;
   a.dev_err = dev_err;
   a.window = std::min(window, 1 << 25);  // past the kept tokens (at most 2^24) a window is all the same; positions minus it stay in 32 bits
@@ -2065,7 +2070,7 @@ static mla_status decode_common(const void* q_abs, const void* q_r, const void* 
   a.num_pages = num_pages;
   a.seg_off = plan + L.seg_off;
   a.segs = plan + L.seg_base;
-  a.scale_log2 = (float)((double)scale * 1.4426950408889634);
+  a.scale_log2 = scale_log2(scale);
   a.o_lat = (uint16_t*)o_lat;
   a.lse = lse;
   a.part_o = part_o;
