@@ -884,6 +884,15 @@ def _masks(masks, T: int, dev: int):
     return _in(masks, "masks", torch.int64, shape, dev), shape[1]
 
 
+def _count(t, name: str) -> int:
+    """The rows of a tensor that says how many there are."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dim() < 1:
+        raise ValueError(f"{name} has no dimension")
+    return t.shape[0]
+
+
 def mla_tree_layout(parents, q_starts, seq_lens, masks, dev_err, positions=None, slots=None, block_table=None,
                     num_pages: int = 0, stream=None) -> None:
     """The ancestors' masks of drafted nodes: parents int32 [T] (within each tree,
@@ -892,7 +901,7 @@ def mla_tree_layout(parents, q_starts, seq_lens, masks, dev_err, positions=None,
     wanted positions int32 [T] and slots int64 [T] (by block_table [B, pages] of a
     pool of num_pages).  All tensors on the device."""
     dev = torch.cuda.current_device()
-    T, B = parents.shape[0], seq_lens.shape[0]
+    T, B = _count(parents, "parents"), _count(seq_lens, "seq_lens")
     m, words = _masks(masks, T, dev)
     if slots is not None and block_table is None:
         raise ValueError("slots need a block_table")
@@ -970,7 +979,7 @@ def mla_decode_tree(q_abs, q_r, kv_cache, block_table, masks, plan: TreePlan, o_
     """mla_decode_paged for the nodes of trees: a row sees the tokens before its
     tree and the nodes of its mask (masks int64 [T, words], mla_tree_layout)."""
     dev = torch.cuda.current_device()
-    pages = kv_cache.shape[0]
+    pages = _count(kv_cache, "kv_cache")
     cache = (_in(kv_cache, "kv_cache", torch.bfloat16, (pages, PAGE, D_QK), dev),)
     _decode_tree(lib().mla_decode_tree, cache, pages, q_abs, q_r, block_table, masks, plan, o_lat, dev_err, lse, scale,
                  stream, dev)
@@ -980,7 +989,7 @@ def mla_decode_tree_fp8(q_abs, q_r, rows, scales, block_table, masks, plan: Tree
                         scale: float = 1.0 / (192 ** 0.5), stream=None) -> None:
     """mla_decode_tree over the FP8 cache."""
     dev = torch.cuda.current_device()
-    pages = rows.shape[0]
+    pages = _count(rows, "rows")
     cache = (_in(rows, "rows", torch.uint8, (pages, PAGE, FP8_ROW_BYTES), dev),
              _in(scales, "scales", torch.float32, (pages, PAGE), dev))
     if isinstance(plan, TreePlan) and not plan.unpack and plan.plan.get_device() == dev:
@@ -1007,7 +1016,7 @@ def _decode_tree(call, cache, pages, q_abs, q_r, block_table, masks, plan, o_lat
 
 
 def _tree_compact(call, cache, block_table, masks, q_starts, seq_lens, accepted, new_lens, dev_err, stream, dev) -> None:
-    T, B = masks.shape[0], seq_lens.shape[0]
+    T, B = _count(masks, "masks"), _count(seq_lens, "seq_lens")
     m, words = _masks(masks, T, dev)
     table, cols = _table(block_table, B, dev)
     _check(call(*cache, table, cols, m, words, _in(q_starts, "q_starts", torch.int32, (B + 1,), dev),
