@@ -119,8 +119,8 @@ class MlaPool:
     and `fork` add them, `free` takes one away from each id."""
 
     def __init__(self, num_pages: int):
-        self._h = C.c_void_p()
-        _check(lib().mla_pool_create(int(num_pages), C.byref(self._h)))
+        self._h, self._pages = C.c_void_p(), int(num_pages)
+        _check(lib().mla_pool_create(self._pages, C.byref(self._h)))
 
     def alloc(self, n: int) -> np.ndarray:
         ids = np.zeros(max(n, 1), dtype=np.int32)
@@ -169,6 +169,7 @@ class MlaPool:
         k = operator.index(max_moves)
         if not 0 <= k < 2 ** 31:
             raise ValueError(f"max_moves = {k}: out of range")
+        k = min(k, self._pages // 2)  # a move takes a free page and a held one
         src, dst, n = np.zeros(max(k, 1), dtype=np.int32), np.zeros(max(k, 1), dtype=np.int32), C.c_int32()
         _check(lib().mla_pool_compact(self._h, k, src.ctypes.data_as(_P32), dst.ctypes.data_as(_P32), C.byref(n)))
         return src[:n.value].copy(), dst[:n.value].copy()
