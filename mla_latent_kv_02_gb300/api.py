@@ -949,7 +949,7 @@ class TreePlan:
     streams: set = field(default_factory=set, repr=False, compare=False)  # raw handles of the streams that use the buffers
     rows: int = 0               # the summary's T and B, at hand for every call
     seqs: int = 0
-    unpack: bool = field(default=False, repr=False, compare=False)  # the workspace was judged for an FP8 cache
+    unpack: bool = field(default=False, repr=False, compare=False)  # the workspace was judged for an FP8 cache, or stays as it is
     captured: list = field(default_factory=list, repr=False, compare=False)  # workspaces that captured graphs name
 
     @property
@@ -958,20 +958,24 @@ class TreePlan:
 
 
 def mla_tree_plan(seq_lens: Sequence[int], q_lens: Sequence[int], device=None, num_clusters: Optional[int] = None,
-                  stream=None, into: Optional[TreePlan] = None) -> TreePlan:
+                  stream=None, into: Optional[TreePlan] = None, unpack: bool = True) -> TreePlan:
     """mla_decode_plan for trees of drafted nodes (q_lens[b] of them, the last of
     seq_lens[b] tokens): one plan serves every layer of a step, whatever the
     trees' shapes.  Uploads, streams, sharing and `into` as for mla_window_plan.
-    The first decode over an FP8 cache that several rows share takes a larger
-    workspace (mla_tree_workspace_size); it stays with the plan, and one that a
-    captured decode used before stays as well: keep the plan as long as the graph."""
+    The first decode over an FP8 cache that three rows a page or more share takes a
+    larger workspace, 72 KB for each page of the sequences, up to 4.8 GB
+    (mla_tree_workspace_size); it stays with the plan, and one that a captured
+    decode used before stays as well: keep the plan as long as the graph.  A new
+    plan a step without `into` holds such a workspace while the last one is still
+    alive.  unpack=False takes none: the decode then converts the pages row by
+    row, with the same results, unless the plan of `into` has one already."""
     if into is not None and not isinstance(into, TreePlan):
         raise TypeError("into must be a plan of mla_tree_plan")
     if num_clusters is None:
         num_clusters = mla_decode_max_clusters()
     buf, info = mla_tree_plan_host(seq_lens, q_lens, num_clusters)
     plan = _planned(TreePlan, buf, info, num_clusters, device, stream, into)
-    plan.rows, plan.seqs, plan.unpack = int(info.plan.T), int(info.plan.B), False
+    plan.rows, plan.seqs, plan.unpack = int(info.plan.T), int(info.plan.B), not unpack
     return plan
 
 
