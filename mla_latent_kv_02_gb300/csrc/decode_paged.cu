@@ -822,6 +822,7 @@ __device__ __forceinline__ void decode_body(const CUtensorMap& kv_map, const CUt
     const int q4 = warp & 3;                 // TMEM lane quarter this warp may access
     const int h = q4 * 32 + lane;            // head row = TMEM lane
     const uint32_t tl = tmem + ((uint32_t)(q4 * 32) << 16);
+    const uint32_t swz = X::swizzle(h), row_off = X::row(h), part_off = X::share(q4);
     const bool wg_leader = ((sw & 3) == 0 && lane == 0);
     // Scores cross the pair and are compared unscaled; the scale (times
     // log2 e) enters once, in the exponent.
@@ -914,7 +915,7 @@ __device__ __forceinline__ void decode_body(const CUtensorMap& kv_map, const CUt
 #pragma unroll
         for (int k = 0; k < X::kPieces; ++k) {
           const int j = p * X::kWords2 + 4 * k;
-          st_shared_v4(stage + X::scores(h, p, k), own[j], own[j + 1], own[j + 2], own[j + 3]);
+          st_shared_v4(stage + p * X::kBytes + row_off + X::piece(k, swz), own[j], own[j + 1], own[j + 2], own[j + 3]);
         }
         fence_proxy_async_smem();
         __syncwarp();
@@ -923,7 +924,8 @@ __device__ __forceinline__ void decode_body(const CUtensorMap& kv_map, const CUt
           peer_ready = true;
         }
         if (elect_one())
-          bulk_copy_to_peer(peer_x + (t % kXBufs) * kXBytes + X::share(q4, p), stage + X::share(q4, p), (uint32_t)X::kWarp,
+          bulk_copy_to_peer(peer_x + (t % kXBufs) * kXBytes + p * X::kBytes + part_off,
+                            stage + p * X::kBytes + part_off, (uint32_t)X::kWarp,
                             peer_bar + 8u * (p * kXBufs + t % kXBufs));
       }
       if (lane == 0) push_cnt[sw] += 1u;  // tiles this warp sent to the peer, every part
@@ -956,7 +958,7 @@ __device__ __forceinline__ void decode_body(const CUtensorMap& kv_map, const CUt
       // ---- add what the peer sent (fp16, unscaled), part by part; mask it (causal,
       //      length, window, tree) and take the row max
       const uint32_t xb = g % kXBufs;
-      const uint32_t recv = base + kOffX + xb * kXBytes;
+      const uint32_t recv = base + kOffX + xb * kXBytes + row_off;
       uint64_t seen = ~0ull;
       if constexpr (kMasked) {
         if (cf.edge()) seen = cf.visible();
@@ -978,7 +980,7 @@ __device__ __forceinline__ void decode_body(const CUtensorMap& kv_map, const CUt
         }
 #pragma unroll
         for (int k = 0; k < X::kPieces; ++k) {
-          const float4 v = ld_shared_v4(recv + X::scores(h, kP, k));
+          const float4 v = ld_shared_v4(recv + kP * X::kBytes + X::piece(k, swz));
           own[kJ + 4 * k] = as_u32(__hadd2(as_h2(own[kJ + 4 * k]), as_h2(__float_as_uint(v.x))));
           own[kJ + 4 * k + 1] = as_u32(__hadd2(as_h2(own[kJ + 4 * k + 1]), as_h2(__float_as_uint(v.y))));
           own[kJ + 4 * k + 2] = as_u32(__hadd2(as_h2(own[kJ + 4 * k + 2]), as_h2(__float_as_uint(v.z))));

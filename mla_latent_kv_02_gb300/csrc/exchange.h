@@ -30,12 +30,15 @@ struct Exchange {
   static constexpr int kWarp = 32 * kRow;                 // one warp's 32 rows: one copy to the peer
   static constexpr int kPieces = kRow / 16;               // 16-byte pieces of a row, swizzled
   static constexpr int kWords2 = kXTokens / 2 / kParts;   // fp16x2 words of a row
-  static MLA_EXCHANGE_HD constexpr uint32_t swizzle(uint32_t h) { return kParts == 1 ? h & 7u : (h >> 1) & 3u; }
-  // The first byte of what warp q4 stages, sends and receives of part p.
-  static MLA_EXCHANGE_HD constexpr uint32_t share(uint32_t q4, uint32_t p) { return p * kBytes + q4 * kWarp; }
+  static MLA_EXCHANGE_HD constexpr uint32_t swizzle(int h) { return kParts == 1 ? (uint32_t)(h & 7) : (uint32_t)((h >> 1) & 3); }
+  // The first byte of what warp q4 stages, sends and receives, in a part.
+  static MLA_EXCHANGE_HD constexpr uint32_t share(int q4) { return (uint32_t)(q4 * kWarp); }
+  // The first byte of head row h's scores in a part, and piece k of a row swizzled by swz.
+  static MLA_EXCHANGE_HD constexpr uint32_t row(int h) { return (uint32_t)(h * kRow); }
+  static MLA_EXCHANGE_HD constexpr uint32_t piece(uint32_t k, uint32_t swz) { return (k ^ swz) << 4; }
   // 16-byte piece k of the scores of head row h in part p.
   static MLA_EXCHANGE_HD constexpr uint32_t scores(uint32_t h, uint32_t p, uint32_t k) {
-    return p * kBytes + h * kRow + ((k ^ swizzle(h)) << 4);
+    return p * kBytes + row((int)h) + piece(k, swizzle((int)h));
   }
   // 16-byte piece k of eight of a finished row, row r of warp q4's 32, on its way
   // to memory: in the places of the same warp's scores, so that the four warps of a
@@ -50,7 +53,7 @@ struct Exchange {
     for (uint32_t q4 = 0; q4 < 4; ++q4)
       for (uint32_t r = 0; r < 32; ++r)
         for (uint32_t k = 0; k < 8; ++k) {
-          const uint32_t at = finished(q4, r, k), from = share(q4, k / kPieces);
+          const uint32_t at = finished(q4, r, k), from = k / kPieces * kBytes + share((int)q4);
           if (at < from || at + 16u > from + kWarp) return false;
         }
     return true;

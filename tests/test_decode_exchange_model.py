@@ -32,7 +32,7 @@ PROGRAM = r"""
 template <int kParts> void print() {
   using X = mla::decode::Exchange<kParts>;
   for (unsigned w = 0; w < 4; ++w) {
-    for (unsigned p = 0; p < kParts; ++p) std::printf("share %d %u %u %u %d\n", kParts, w, p, X::share(w, p), X::kWarp);
+    for (unsigned p = 0; p < kParts; ++p) std::printf("share %d %u %u %u %d\n", kParts, w, p, p * X::kBytes + X::share(w), X::kWarp);
     for (unsigned r = 0; r < 32; ++r) {
       for (unsigned p = 0; p < kParts; ++p)
         for (unsigned k = 0; k < X::kPieces; ++k) std::printf("scores %d %u %u %u\n", kParts, w, p, X::scores(32 * w + r, p, k));
