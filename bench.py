@@ -50,22 +50,24 @@ def workload_stats(case):
 
 
 # DRAM traffic (read + write) per decode launch from an ncu capture, keyed by
-# the sha1 prefix of the decode kernel source it was taken on and the
-# workload.  Captured at half batch and scaled by the query rows (see
+# the sha1 prefix of the decode kernel source (decode_paged.cu, then exchange.h)
+# it was taken on and the workload.  Captured at half batch and scaled by the query rows (see
 # profiles/decode_kernel_mtp2_b32_ncu.md); any other source reads as null.
-MEASURED_TRAFFIC = {("92270284c471", 2): 658.57e6}
+MEASURED_TRAFFIC = {("ab97a7fa383b", 2): 656.99e6}
 
 
 def decode_traffic(workload: int, batch):
     import hashlib
-    src = os.path.join(ROOT, "mla_latent_kv_02_gb300", "csrc", "decode_paged.cu")
+    sha = hashlib.sha1()
     try:
-        sha = hashlib.sha1(open(src, "rb").read()).hexdigest()[:12]
+        for name in ("decode_paged.cu", "exchange.h"):
+            with open(os.path.join(ROOT, "mla_latent_kv_02_gb300", "csrc", name), "rb") as f:
+                sha.update(f.read())
     except OSError:
         return None
     if batch is not None:
         return None
-    return MEASURED_TRAFFIC.get((sha, workload))
+    return MEASURED_TRAFFIC.get((sha.hexdigest()[:12], workload))
 
 
 def load_peaks():

@@ -43,11 +43,14 @@
 //  * Online softmax with lazy rescaling: the running reference max only moves
 //    when a tile's max exceeds it by more than 8 (log2 units), so P stays
 //    below 256 and O and l in TMEM are rescaled only on those rare tiles.
-//  * Warp roles: warp 0 TMA producer, warp 1 TMEM allocation + QK^T issue,
-//    warps 2-9 softmax/epilogue (two warpgroups), warp 10 P·V issue.
-//  * Work: the plan cuts all rows' 64-token tiles into equal contiguous ranges,
-//    one per cluster; a row cut by a boundary is written as fp32 partials
-//    (normalised O and log2-sum-exp) and merged by the combine kernel.
+//  * Warp roles over the bf16 cache: warp 0 TMA producer, warp 1 TMEM allocation
+//    + QK^T issue, warps 2-9 softmax and the finished rows (two warpgroups), warp
+//    10 P·V issue; over the FP8 cache and for trees as said at Cfg, the rows of
+//    trees stored by a warpgroup of their own.
+//  * Work: a range of 64-token tiles for each cluster, cut by the plan: equal and
+//    contiguous over all rows, for trees rows dealt out and few of them cut; a row
+//    cut by a boundary is written as fp32 partials (normalised O and
+//    log2-sum-exp) and merged by the combine kernel.
 //  * Every wait in the loop is bounded (DecodeArgs::wait_limit); on expiry the
 //    kernel raises an abort flag that every role polls, drains its own TMA
 //    loads and MMAs, waits until the score copies the peer already issued

@@ -1908,8 +1908,8 @@ mla_status mla_tree_plan(const int32_t* seq_lens_host, const int32_t* q_lens_hos
 // page or more (a sequence's first two may need one page less), and enough tiles
 // to pay for a launch.  A tile of f16 rows takes half the time of one that has to
 // be converted; unpacked and not, in us: two rows of 16 sequences of 8 192 tokens
-// 101 and 101, of 64 of 2 048 tokens 109 and 102; three rows of 16 of 2 048 46 and
-// 49, of 8 (792 tiles) 27.8 and 30.5; one sequence: 16 rows over 1 024 tokens (272
+// 107 and 100, of 64 of 2 048 tokens 109 and 109; three rows of 16 of 2 048 45 and
+// 46, of 8 (792 tiles) 26.5 and 29.1; one sequence: 16 rows over 1 024 tokens (272
 // tiles) 20 and 20, 8 over 2 048 (264) 22.2 and 21.6, 12 over 4 096 (780) 26 and
 // 30, 64 over 32 768 349 and 688; two sequences, 8 rows over 2 048 (528) 24 and 25.
 static bool tree_unpacks(const mla_tree_info& info) {

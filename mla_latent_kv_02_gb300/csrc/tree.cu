@@ -93,7 +93,8 @@ __global__ void __launch_bounds__(kMaxNodes) layout_kernel(const TreeLayoutArgs 
 // wrote.  A CTA takes a sequence (x) in `per` layers (y), layer after layer, so
 // that the look-up of its slots, four loads one behind the other, is paid once.
 // Four rows a thread in flight: 2.5 us for one sequence in one layer, 8.0 for 64
-// in 60 (36.5 MB, 4.6 TB/s; eight rows in flight 8.8: fewer CTAs fit an SM).
+// in 60 (36.5 MB, 4.6 TB/s; eight rows in flight 8.8: fewer CTAs fit an SM); of an
+// FP8 cache 6.6 (20 MB), of an NVFP4 cache 4.3 (13 MB).
 template <int kPieces, bool kScales>
 struct CompactCfg {
   static constexpr int kPer = kPieces + (kScales ? 1 : 0);  // threads a row: its 16-byte pieces and its scale
@@ -178,7 +179,9 @@ __global__ void __launch_bounds__(256) compact_kernel(const TreeCompactArgs a, i
 // of 1 032 tokens and one of 262 144: 2 023 -> 1 043 us).  A token's scale outside
 // the f16 range counts only where a row sees it: every row sees the tokens before
 // the tree, and the nodes' masks are asked in that case alone.  Rows past the
-// sequence's end become zeros.  Moves 1.8 KB a token: 14 us for 32 832 tokens with cold caches, 21 MB from HBM and 38 into L2.
+// sequence's end become zeros.  Moves 1.8 KB a token: 14 us for 32 832 tokens with
+// cold caches, 21 MB from HBM and 38 into L2 (59 by the sectors counted there, half
+// as much again as is stored, as for page copies).
 __global__ void __launch_bounds__(256) unpack_kernel(const TreeUnpackArgs a) {
   const int t = threadIdx.x;
   const int32_t page = blockIdx.x;
@@ -210,7 +213,7 @@ __global__ void __launch_bounds__(256) unpack_kernel(const TreeUnpackArgs a) {
   uint4* dst = a.out + (int64_t)page * MLA_PAGE_SIZE * (MLA_TOKEN_ELEMS / 8);
   // Eight codes and one 16-byte store a thread, two warps a row: a warp stores
   // 512 bytes in one piece (16 codes and two stores left half sectors: 100 MB
-  // through L2 for 38).
+  // counted at L2 for 59).
   constexpr int kRows = 8;  // of a thread at a time
   const int piece = t % 64, r0 = t / 64;
   const int last = (int)min((int64_t)len - pg * MLA_PAGE_SIZE, (int64_t)MLA_PAGE_SIZE);
